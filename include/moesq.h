@@ -350,6 +350,157 @@ moesq_status_t moesq_grouped_spgemm_act4(const moesq_act4_t *x, const int32_t *p
                                          hipStream_t stream);
 
 /*
+ * Router: top-k experts and their weights from the router's scores, the ids
+ * and weights that moesq_route, moesq_route_grouped_spgemm and
+ * moesq_unpermute take.  Row t of the logits is one token's scores:
+ *   l     = logits[t][e]; NaN counts as -inf, +inf as the largest finite fp32
+ *   p[e]  = softmax of l over the E experts, or sigmoid(l)
+ *   key   = l without a bias (the order of l is the order of p), else
+ *           p[e] + bias[e].  Keys are compared as 64-bit values, so the
+ *           selection is the exact one also where two scores differ by less
+ *           than an fp32 rounding.  An expert is masked (never selected)
+ *           when its l or its bias is -inf, or its bias NaN; a bias of +inf
+ *           counts as the largest finite fp32.
+ *   groups: with n_group > 1 the experts form n_group runs of E / n_group.  A
+ *           group scores its largest key (MOESQ_GROUP_MAX), or the sum of its
+ *           two largest p[e] + bias[e] (MOESQ_GROUP_TOP2; a missing or masked
+ *           second counts as nothing).  The topk_group best groups stay, equal
+ *           scores to the lower group; a group whose experts are all masked
+ *           is never kept.
+ *   ids   = the k largest keys of what stays, in descending order, equal keys
+ *           to the lower expert.  When fewer than k experts are left, the
+ *           slots behind them get id -1 and weight 0: moesq_route does not
+ *           route those, moesq_unpermute adds nothing for them.
+ *   w[j]  = p[ids[j]], divided by the sum of the k selected p with
+ *           `renormalize` (0 where that sum is 0), times `scale`; computed in
+ *           64 bits and rounded to fp32 once.
+ *   logits [T][E] of `dtype` (fp32 or bf16); bias [E] fp32 or NULL; gate: host
+ *   pointer; topk_ids [T*k] int32 and topk_weights [T*k] fp32 out, flat order
+ *   t*k + j.
+ *   n_rows: device pointer to one int32, or NULL.  Rows t >= *n_rows (the
+ *   padding of a decode batch captured at a larger size) get ids -1 and
+ *   weights 0.
+ * Limits: 1 <= E <= MOESQ_MAX_EXPERTS, 1 <= k <= min(E, MOESQ_GATE_MAX_TOPK),
+ *         1 <= topk_group <= n_group <= MOESQ_GATE_MAX_GROUPS, E % n_group == 0,
+ *         k <= topk_group * (E / n_group), T >= 0, T*k < 2^31, scale finite.
+ */
+typedef enum { MOESQ_F32 = 0, MOESQ_BF16 = 1 } moesq_dtype_t;
+typedef enum { MOESQ_SCORE_SOFTMAX = 0, MOESQ_SCORE_SIGMOID = 1 } moesq_score_t;
+typedef enum { MOESQ_GROUP_MAX = 0, MOESQ_GROUP_TOP2 = 1 } moesq_group_score_t;
+#define MOESQ_GATE_MAX_TOPK 64
+#define MOESQ_GATE_MAX_GROUPS 64
+typedef struct {
+  int32_t k;
+  int32_t score;        /* MOESQ_SCORE_*                                   */
+  int32_t n_group;      /* 1: no groups                                    */
+  int32_t topk_group;   /* groups kept                                     */
+  int32_t group_score;  /* MOESQ_GROUP_* (not read when n_group == 1)      */
+  int32_t renormalize;  /* 0 or 1                                          */
+  float scale;          /* factor of every weight                          */
+} moesq_gate_t;
+moesq_status_t moesq_gate_topk(const void *logits, int32_t dtype, int32_t T, int32_t E,
+                               const float *bias, const moesq_gate_t *gate, const int32_t *n_rows,
+                               int32_t *topk_ids, float *topk_weights, hipStream_t stream);
+
+/*
+ * Microscaled (MX) rows: blocks of 32 consecutive elements of a row share one
+ * power-of-two scale (E8M0: byte s stands for 2^(s-127), 0xFF for NaN), the
+ * elements are E2M1 (MXFP4) or E4M3 (MXFP8).  Power-of-two scales are what
+ * the scaled MFMA of gfx950 takes, so moesq_mx_gemm contracts these rows as
+ * they are, without decoding them (the NVFP4 rows of moesq_act4_t have E4M3
+ * scales and are decoded to bf16 first).
+ *   codes   MXFP4: [rows][K/2], two per byte, position 2i in the low nibble
+ *           MXFP8: [rows][K]
+ *   scales  [rows][K/32]
+ *   x~[r][i] = element(code) * 2^(scale - 127)
+ * As MXFP4 weights: rows = E*N, expert e's output feature n is row e*N + n.
+ * The struct is a host object; its pointers are device pointers, the codes
+ * 16-byte aligned.
+ */
+typedef enum {
+  MOESQ_ROWS_NONE = 0,
+  MOESQ_ROWS_MXFP4 = 1,
+  MOESQ_ROWS_MXFP8 = 2,
+  MOESQ_ROWS_NVFP4 = 3   /* the rows of moesq_act4_t (moesq_rmsnorm only)   */
+} moesq_rows_t;
+typedef struct {
+  const uint8_t *codes;
+  const uint8_t *scales;
+  int32_t rows, K;
+  int32_t format;        /* MOESQ_ROWS_MXFP4 or MOESQ_ROWS_MXFP8            */
+} moesq_mx_t;
+
+/*
+ * Quantize rows to MX, every block on its own:
+ *   s    = max(0, 127 + floor(log2 amax_b) - emax), emax = 2 (E2M1) or
+ *          8 (E4M3); 0 for a zero block
+ *   code = element nearest to x / 2^(s-127), ties to the even code, saturating
+ *          at 6 or 448; a zero is +0
+ * A block that holds an infinity or a NaN gets s = 0xFF (NaN) and codes 0.
+ *   x [rows][K] of `dtype` (fp32: weights, or bf16: activations), 16-byte
+ *   aligned; codes (16-byte aligned) and scales out.
+ * Limits: K % 32 == 0, K > 0, rows >= 0; format MXFP4 or MXFP8.
+ */
+moesq_status_t moesq_mx_quantize(const void *x, int32_t dtype, int32_t rows, int32_t K,
+                                 int32_t format, uint8_t *codes, uint8_t *scales,
+                                 hipStream_t stream);
+
+/*
+ * The values of MX rows in bf16: x~ above, rounded to nearest even only where
+ * the value leaves bf16's normal range (every other value is exact); a block
+ * with scale 0xFF is NaN.  x: host descriptor; out [rows][K] bf16, 16-byte
+ * aligned.
+ */
+moesq_status_t moesq_mx_decode(const moesq_mx_t *x, uint16_t *out, hipStream_t stream);
+
+/*
+ * RMS norm, with the residual's addition before it and the quantization of
+ * its result behind it:
+ *   s[t][i] = bf16_rne(x[t][i] + residual[t][i])   (residual == NULL: x)
+ *   r[t]    = fp32(1 / sqrt(mean_i(s[t][i]^2) + eps)), sums and root in 64 bits
+ *   y[t][i] = bf16_rne((s[t][i] * r[t]) * weight[i]), fp32 products
+ *   x [T][K] bf16; weight [K] bf16; residual [T][K] bf16 or NULL.
+ *   residual_out [T][K] bf16: receives s (required with a residual, may be
+ *   the residual's own buffer or x's; NULL without one).
+ *   y [T][K] bf16 out, or NULL when only the quantized rows are wanted; may
+ *   be x's buffer when no residual is given.
+ *   rows_format: MOESQ_ROWS_NONE, or the format in which the rows of y are
+ *   also written: codes, scales and, for NVFP4 alone, row_scale, bit for bit
+ *   what moesq_mx_quantize (MXFP4, MXFP8) or moesq_quantize_activations
+ *   (NVFP4) makes of y.
+ * All buffers but scales and row_scale 16-byte aligned.
+ * Limits: K % 8 == 0 (K % 32 == 0 with a rows_format), K > 0, T >= 0,
+ *         eps >= 0 and finite.
+ */
+moesq_status_t moesq_rmsnorm(const uint16_t *x, const uint16_t *residual, const uint16_t *weight,
+                             int32_t T, int32_t K, double eps, uint16_t *residual_out, uint16_t *y,
+                             int32_t rows_format, uint8_t *codes, uint8_t *scales,
+                             float *row_scale, hipStream_t stream);
+
+/*
+ * Product of MX activation rows with MXFP4 weights on the scaled MFMA, dense
+ * or over all experts in one call:
+ *   acc[r][n] = sum_k x~[src(r)][k] * w~_e[n][k]     (fp32 accumulation)
+ *   epilogue NONE:   y[r][n] = bf16_rne(acc[r][n]),  y is [M][N]
+ *   epilogue SWIGLU: y[r][c] = bf16_rne(silu(acc[r][c]) * acc[r][c+N/2]), y is [M][N/2]
+ *   x: host descriptor, MXFP4 or MXFP8; w: host descriptor, MXFP4 of E*N rows
+ *   with w->K == x->K.
+ *   expert_offsets [E+1] int32: rows [offsets[e], offsets[e+1]) are expert
+ *   e's (clamped to [0, M]); NULL with E == 1: every row (a dense layer, such
+ *   as a shared expert).
+ *   perm, T, k: as in moesq_grouped_spgemm_act4.  perm == NULL: src(r) = r,
+ *   x->rows == M.  Otherwise src(r) = perm[r] / k, x->rows == T, M == T*k, and
+ *   rows with perm[r] outside [0, T*k) come out zero; needs expert_offsets.
+ *   MOESQ_OUT_FLAT in the epilogue stores row r at y[perm[r]] (needs perm).
+ *   y 16-byte aligned.  Rows of y outside every expert range are not written.
+ * Limits: K % 32 == 0, N % 16 == 0 (SWIGLU: N % 32 == 0),
+ *         1 <= E <= MOESQ_MAX_EXPERTS, w->rows == E*N, M >= 0.
+ */
+moesq_status_t moesq_mx_gemm(const moesq_mx_t *x, const int32_t *perm, int32_t T, int32_t k,
+                             const int32_t *expert_offsets, int32_t M, const moesq_mx_t *w,
+                             int32_t E, int32_t epilogue, uint16_t *y, hipStream_t stream);
+
+/*
  * Combine.
  *   topk_weights != NULL: out[t][:] = bf16_rne( sum_{j<k} w[t*k+j] * y[inv_perm[t*k+j]][:] ),
  *                         fp32 accumulation in j order; out is [T][N].

@@ -31,6 +31,8 @@ from .pack import PackedExpert, decode, quantize, support
 from .paired import (PAIRS, PackedPairedExpert, decode_paired, paired_pattern,
                      paired_support, pattern_mask, quantize_paired)
 from .route import route
+from .gate import gate_topk
+from .mx import mx_decode, mx_gemm, mx_quantize, rmsnorm
 from .moe import (grouped_gemm, moe_chain, permute, silu, swiglu, unpermute,
                   expert_gemm)
 from .w4a4 import (PackedActivations, decode_activations, quantize_activations,

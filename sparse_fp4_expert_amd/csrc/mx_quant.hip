@@ -1,0 +1,131 @@
+// Quantization of fp32 and bf16 rows to MX (MXFP4, MXFP8) and the values of
+// MX rows in bf16.
+//
+// A block of 32 elements takes the exponent of its largest magnitude, less
+// that of the element format's largest value, as its scale 2^e; the codes are
+// round-to-nearest-even of x / 2^e, an exact quotient, so the result is the
+// format's definition bit for bit.  Rows are whole blocks (K % 32 == 0), so
+// both kernels run over the flat units of 8 elements: four neighbouring lanes
+// hold a block and share its maximum by two lane exchanges.  Both are streams
+// (bf16 in, MXFP4 out: 2.53 bytes an element), bound by HBM.
+#include <algorithm>
+
+#include "mx.hpp"
+
+namespace moesq {
+
+constexpr int MXQ_THREADS = 256;
+
+template <bool FP8, bool F32>
+__global__ __launch_bounds__(MXQ_THREADS) void mx_quant_kernel(const uint4 *__restrict__ x,
+                                                               size_t units, uint8_t *codes,
+                                                               uint8_t *scales) {
+  // units is a multiple of 4 and the stride of 64, so the lanes of a block
+  // stay in the loop together
+  const size_t stride = (size_t)gridDim.x * MXQ_THREADS;
+  for (size_t u = (size_t)blockIdx.x * MXQ_THREADS + threadIdx.x; u < units; u += stride) {
+    float v[8];
+    if constexpr (F32) {
+      const uint4 a = x[2 * u], b = x[2 * u + 1];
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+      unpack_bf16x8(x[u], v);
+    }
+    mx_store_unit<FP8>(v, u, codes, scales);
+  }
+}
+
+template <bool FP8>
+__global__ __launch_bounds__(MXQ_THREADS) void mx_decode_kernel(const uint8_t *__restrict__ codes,
+                                                                const uint8_t *__restrict__ scales,
+                                                                size_t units, uint4 *out) {
+  const size_t stride = (size_t)gridDim.x * MXQ_THREADS;
+  for (size_t u = (size_t)blockIdx.x * MXQ_THREADS + threadIdx.x; u < units; u += stride) {
+    const float s = mx_scale_f32(scales[u >> 2]);
+    float v[8];
+    if constexpr (FP8) {
+      const uint2 c = reinterpret_cast<const uint2 *>(codes)[u];
+      const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false);
+      const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true);
+      const f32x2_t d = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false);
+      const f32x2_t e = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true);
+      v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1];
+      v[4] = d[0], v[5] = d[1], v[6] = e[0], v[7] = e[1];
+    } else {
+      const uint32_t c = reinterpret_cast<const uint32_t *>(codes)[u];
+      const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0);
+      const f32x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
+      const f32x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2);
+      const f32x2_t e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
+      v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1];
+      v[4] = d[0], v[5] = d[1], v[6] = e[0], v[7] = e[1];
+    }
+    out[u] = make_uint4(pack_bf16x2(v[0] * s, v[1] * s), pack_bf16x2(v[2] * s, v[3] * s),
+                        pack_bf16x2(v[4] * s, v[5] * s), pack_bf16x2(v[6] * s, v[7] * s));
+  }
+}
+
+// One unit a lane; past 32 workgroups a CU the lanes stride.
+static unsigned mx_grid(size_t units) {
+  const size_t blocks = (units + MXQ_THREADS - 1) / MXQ_THREADS;
+  return (unsigned)std::min<size_t>(blocks, (size_t)device_cu_count() * 32);
+}
+
+}  // namespace moesq
+
+using namespace moesq;
+
+extern "C" moesq_status_t moesq_mx_quantize(const void *x, int32_t dtype, int32_t rows, int32_t K,
+                                            int32_t format, uint8_t *codes, uint8_t *scales,
+                                            hipStream_t stream) {
+  const std::string who("moesq_mx_quantize");
+  clear_error();
+  if (rows < 0) return fail(MOESQ_ERR_SHAPE, who + ": rows must be >= 0");
+  if (K < 32 || K % 32) return fail(MOESQ_ERR_SHAPE, who + ": K must be a positive multiple of 32");
+  if (dtype != MOESQ_F32 && dtype != MOESQ_BF16)
+    return fail(MOESQ_ERR_ARG, who + ": dtype must be MOESQ_F32 or MOESQ_BF16");
+  if (format != MOESQ_ROWS_MXFP4 && format != MOESQ_ROWS_MXFP8)
+    return fail(MOESQ_ERR_ARG, who + ": format must be MXFP4 or MXFP8");
+  if (rows == 0) return MOESQ_OK;
+  if (!x || !codes || !scales) return fail(MOESQ_ERR_NULL, who + ": NULL buffer");
+  if (((uintptr_t)x | (uintptr_t)codes) & 15)
+    return fail(MOESQ_ERR_ARG, who + ": x and codes must be 16-byte aligned");
+  const size_t units = (size_t)rows * (size_t)(K / 8);
+  const auto *src = static_cast<const uint4 *>(x);
+  const dim3 grid(mx_grid(units)), block(MXQ_THREADS);
+  const bool f8 = format == MOESQ_ROWS_MXFP8, f32 = dtype == MOESQ_F32;
+  if (f8 && f32)
+    hipLaunchKernelGGL((mx_quant_kernel<true, true>), grid, block, 0, stream, src, units, codes, scales);
+  else if (f8)
+    hipLaunchKernelGGL((mx_quant_kernel<true, false>), grid, block, 0, stream, src, units, codes, scales);
+  else if (f32)
+    hipLaunchKernelGGL((mx_quant_kernel<false, true>), grid, block, 0, stream, src, units, codes, scales);
+  else
+    hipLaunchKernelGGL((mx_quant_kernel<false, false>), grid, block, 0, stream, src, units, codes, scales);
+  return launch_status("moesq_mx_quantize");
+}
+
+extern "C" moesq_status_t moesq_mx_decode(const moesq_mx_t *x, uint16_t *out, hipStream_t stream) {
+  const std::string who("moesq_mx_decode");
+  clear_error();
+  if (!x) return fail(MOESQ_ERR_NULL, who + ": descriptor is NULL");
+  if (x->rows < 0) return fail(MOESQ_ERR_SHAPE, who + ": rows must be >= 0");
+  if (x->K < 32 || x->K % 32)
+    return fail(MOESQ_ERR_SHAPE, who + ": K must be a positive multiple of 32");
+  if (x->format != MOESQ_ROWS_MXFP4 && x->format != MOESQ_ROWS_MXFP8)
+    return fail(MOESQ_ERR_ARG, who + ": format must be MXFP4 or MXFP8");
+  if (x->rows == 0) return MOESQ_OK;
+  if (!x->codes || !x->scales || !out) return fail(MOESQ_ERR_NULL, who + ": NULL buffer");
+  if (((uintptr_t)x->codes | (uintptr_t)out) & 15)
+    return fail(MOESQ_ERR_ARG, who + ": codes and out must be 16-byte aligned");
+  const size_t units = (size_t)x->rows * (size_t)(x->K / 8);
+  const dim3 grid(mx_grid(units)), block(MXQ_THREADS);
+  auto *dst = reinterpret_cast<uint4 *>(out);
+  if (x->format == MOESQ_ROWS_MXFP8)
+    hipLaunchKernelGGL((mx_decode_kernel<true>), grid, block, 0, stream, x->codes, x->scales, units, dst);
+  else
+    hipLaunchKernelGGL((mx_decode_kernel<false>), grid, block, 0, stream, x->codes, x->scales, units, dst);
+  return launch_status("moesq_mx_decode");
+}

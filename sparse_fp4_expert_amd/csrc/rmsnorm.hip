@@ -1,0 +1,222 @@
+// RMS norm with the residual's addition before it and the quantization of
+// its rows behind it.
+//
+//   s = bf16(x + residual),  r = 1 / sqrt(mean(s^2) + eps),  y = bf16(s r w)
+//
+// One workgroup per row; a thread keeps its 8-element units of s in
+// registers between the sum and the scaling, so a row is read once.  Squares
+// of bf16 values are exact in 64 bits and the sum of a row is rounded far
+// below an fp32 step, so r is the correctly rounded fp32 value but for rows
+// next to a rounding border, whatever the order of the sum: the quantized
+// rows, whose scales turn on single bits of y, then do not depend on it.
+// (64-bit multiply-adds run at the fp32 rate on this chip; the kernel is a
+// stream, 5 to 9 bytes an element, bound by HBM.)
+#include "encode.hpp"
+#include "mx.hpp"
+
+namespace moesq {
+
+constexpr int RN_THREADS = 256;
+constexpr int RN_WAVES = RN_THREADS / 64;
+
+struct RmsNormArgs {
+  const uint4 *x, *residual, *weight;
+  uint4 *residual_out, *y;
+  uint8_t *codes, *scales;
+  float *row_scale;
+  int units;                 // K / 8
+  double eps;
+};
+
+// Sum of v over the workgroup, in every thread.
+__device__ __forceinline__ double block_sum(double v, double *part) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double t = 0.0;
+#pragma unroll
+  for (int w = 0; w < RN_WAVES; ++w) t += part[w];
+  return t;
+}
+
+__device__ __forceinline__ float block_max(float v, float *part) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float t = 0.0f;
+#pragma unroll
+  for (int w = 0; w < RN_WAVES; ++w) t = fmaxf(t, part[w]);
+  return t;
+}
+
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  return pack_bf16x2(bf16_lo(a) + bf16_lo(b), bf16_hi(a) + bf16_hi(b));
+}
+
+__device__ __forceinline__ uint32_t norm_bf16x2(uint32_t s, uint32_t w, float r) {
+  return pack_bf16x2((bf16_lo(s) * r) * bf16_lo(w), (bf16_hi(s) * r) * bf16_hi(w));
+}
+
+// The NVFP4 codes and block scale of one lane's unit, the steps of
+// moesq_quantize_activations.
+__device__ __forceinline__ void nvfp4_store_unit(const float (&v)[8], float g, size_t unit,
+                                                 uint8_t *codes, uint8_t *scales) {
+  const float bmax = __uint_as_float(mx_block_amax(v));
+  const uint32_t sc = e4m3_encode(__fdiv_rn(bmax, 6.0f * g));
+  const float sg = e4m3_to_f32(sc) * g;
+  uint32_t c = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    c |= (sg > 0.0f ? e2m1_encode(__fdiv_rn(v[i], sg)) : 0u) << (4 * i);
+  reinterpret_cast<uint32_t *>(codes)[unit] = c;
+  if ((unit & 3) == 0) scales[unit >> 2] = (uint8_t)sc;
+}
+
+// NU units a thread (K up to 2048 * NU); NU == 0: rows of any length, read a
+// second time for the scaling (s from residual_out when there is one).
+template <int NU, int ROWS>
+__global__ __launch_bounds__(RN_THREADS) void rmsnorm_kernel(RmsNormArgs a) {
+  __shared__ double psum[RN_WAVES];
+  __shared__ float pmax[RN_WAVES];
+  constexpr int N = NU ? NU : 1, UNROLL = N;
+  const int tid = threadIdx.x, units = a.units;
+  const size_t base = (size_t)blockIdx.x * units;
+  const int iters = NU ? NU : (units + RN_THREADS - 1) / RN_THREADS;
+
+  uint4 s[N];
+  double ss = 0.0;
+#pragma unroll UNROLL
+  for (int i = 0; i < iters; ++i) {
+    const int u = i * RN_THREADS + tid;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (u < units) {
+      v = a.x[base + u];
+      if (a.residual) {
+        const uint4 d = a.residual[base + u];
+        v = make_uint4(add_bf16x2(v.x, d.x), add_bf16x2(v.y, d.y), add_bf16x2(v.z, d.z),
+                       add_bf16x2(v.w, d.w));
+        a.residual_out[base + u] = v;
+      }
+    }
+    float f[8];
+    unpack_bf16x8(v, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fma((double)f[j], (double)f[j], ss);
+    if constexpr (NU > 0) s[i] = v;
+  }
+  const float r = (float)(1.0 / sqrt(block_sum(ss, psum) / (8.0 * units) + a.eps));
+
+  auto norm = [&](int i, int u) {
+    const uint4 v = NU ? s[NU ? i : 0] : (a.residual ? a.residual_out[base + u] : a.x[base + u]);
+    const uint4 w = a.weight[u];
+    return make_uint4(norm_bf16x2(v.x, w.x, r), norm_bf16x2(v.y, w.y, r), norm_bf16x2(v.z, w.z, r),
+                      norm_bf16x2(v.w, w.w, r));
+  };
+
+  float g = 1.0f;
+  if constexpr (ROWS == MOESQ_ROWS_NVFP4) {
+    float m = 0.0f;
+#pragma unroll UNROLL
+    for (int i = 0; i < iters; ++i) {
+      const int u = i * RN_THREADS + tid;
+      if (u < units) {
+        float f[8];
+        const uint4 y = norm(i, u);
+        unpack_bf16x8(y, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+      }
+    }
+    const float amax = block_max(m, pmax);
+    g = amax > 0.0f ? __fdiv_rn(amax, 2688.0f) : 1.0f;
+    if (tid == 0) a.row_scale[blockIdx.x] = g;
+  }
+
+#pragma unroll UNROLL
+  for (int i = 0; i < iters; ++i) {
+    const int u = i * RN_THREADS + tid;
+    // a block's four units are four neighbouring lanes and units % 4 == 0
+    // with quantized rows, so they leave together
+    if (u >= units) break;
+    const uint4 y = norm(i, u);
+    if (a.y) a.y[base + u] = y;
+    if constexpr (ROWS != MOESQ_ROWS_NONE) {
+      float f[8];
+      unpack_bf16x8(y, f);
+      if constexpr (ROWS == MOESQ_ROWS_NVFP4)
+        nvfp4_store_unit(f, g, base + u, a.codes, a.scales);
+      else
+        mx_store_unit<ROWS == MOESQ_ROWS_MXFP8>(f, base + u, a.codes, a.scales);
+    }
+  }
+}
+
+template <int NU>
+static void launch_rows(const RmsNormArgs &a, int T, int rows_format, hipStream_t stream) {
+  const dim3 grid((unsigned)T), block(RN_THREADS);
+  switch (rows_format) {
+    case MOESQ_ROWS_MXFP4:
+      hipLaunchKernelGGL((rmsnorm_kernel<NU, MOESQ_ROWS_MXFP4>), grid, block, 0, stream, a);
+      break;
+    case MOESQ_ROWS_MXFP8:
+      hipLaunchKernelGGL((rmsnorm_kernel<NU, MOESQ_ROWS_MXFP8>), grid, block, 0, stream, a);
+      break;
+    case MOESQ_ROWS_NVFP4:
+      hipLaunchKernelGGL((rmsnorm_kernel<NU, MOESQ_ROWS_NVFP4>), grid, block, 0, stream, a);
+      break;
+    default:
+      hipLaunchKernelGGL((rmsnorm_kernel<NU, MOESQ_ROWS_NONE>), grid, block, 0, stream, a);
+  }
+}
+
+}  // namespace moesq
+
+using namespace moesq;
+
+extern "C" moesq_status_t moesq_rmsnorm(const uint16_t *x, const uint16_t *residual,
+                                        const uint16_t *weight, int32_t T, int32_t K, double eps,
+                                        uint16_t *residual_out, uint16_t *y, int32_t rows_format,
+                                        uint8_t *codes, uint8_t *scales, float *row_scale,
+                                        hipStream_t stream) {
+  const std::string who("moesq_rmsnorm");
+  clear_error();
+  if (T < 0) return fail(MOESQ_ERR_SHAPE, who + ": T must be >= 0");
+  if (rows_format < MOESQ_ROWS_NONE || rows_format > MOESQ_ROWS_NVFP4)
+    return fail(MOESQ_ERR_ARG, who + ": unknown rows_format");
+  const bool rows = rows_format != MOESQ_ROWS_NONE;
+  if (K < 8 || K % 8) return fail(MOESQ_ERR_SHAPE, who + ": K must be a positive multiple of 8");
+  if (rows && K % 32)
+    return fail(MOESQ_ERR_SHAPE, who + ": quantized rows need K % 32 == 0");
+  if (!(eps >= 0.0 && eps <= 1e300)) return fail(MOESQ_ERR_ARG, who + ": eps must be finite and >= 0");
+  if (T == 0) return MOESQ_OK;
+  if (!x || !weight) return fail(MOESQ_ERR_NULL, who + ": x or weight is NULL");
+  if ((residual != nullptr) != (residual_out != nullptr))
+    return fail(MOESQ_ERR_NULL, who + ": residual and residual_out go together");
+  if (!y && !rows) return fail(MOESQ_ERR_NULL, who + ": neither y nor quantized rows asked for");
+  if (rows && (!codes || !scales || (rows_format == MOESQ_ROWS_NVFP4 && !row_scale)))
+    return fail(MOESQ_ERR_NULL, who + ": NULL codes, scales or row_scale");
+  if (y && (y == residual || y == residual_out || (residual && y == x)))
+    return fail(MOESQ_ERR_ARG, who + ": y must not share the residual's buffers, nor x's with a residual");
+  const uintptr_t bits = (uintptr_t)x | (uintptr_t)residual | (uintptr_t)weight |
+                         (uintptr_t)residual_out | (uintptr_t)y | (uintptr_t)(rows ? codes : nullptr);
+  if (bits & 15) return fail(MOESQ_ERR_ARG, who + ": buffers must be 16-byte aligned");
+  RmsNormArgs a{};
+  a.x = reinterpret_cast<const uint4 *>(x);
+  a.residual = reinterpret_cast<const uint4 *>(residual);
+  a.weight = reinterpret_cast<const uint4 *>(weight);
+  a.residual_out = reinterpret_cast<uint4 *>(residual_out);
+  a.y = reinterpret_cast<uint4 *>(y);
+  a.codes = codes;
+  a.scales = scales;
+  a.row_scale = row_scale;
+  a.units = K / 8;
+  a.eps = eps;
+  if (K <= 2048) launch_rows<1>(a, T, rows_format, stream);
+  else if (K <= 4096) launch_rows<2>(a, T, rows_format, stream);
+  else if (K <= 8192) launch_rows<4>(a, T, rows_format, stream);
+  else if (K <= 16384) launch_rows<8>(a, T, rows_format, stream);
+  else launch_rows<0>(a, T, rows_format, stream);
+  return launch_status("moesq_rmsnorm");
+}

@@ -12,6 +12,7 @@ importing this module without it raises ImportError.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -30,6 +31,12 @@ OUT_FLAT = 0x100
 LAYOUT_CANONICAL, LAYOUT_TILED, LAYOUT_PAIRED, LAYOUT_PAIRED_TILED = 0, 1, 2, 3
 PAIRED_LAYOUTS = (LAYOUT_PAIRED, LAYOUT_PAIRED_TILED)
 MAX_EXPERTS = 1024
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
+GATE_MAX_TOPK, GATE_MAX_GROUPS = 64, 64
+# Formats of quantized rows: microscaled FP4 / FP8 (Mx), NVFP4 (Act4).
+ROWS_NONE, ROWS_MXFP4, ROWS_MXFP8, ROWS_NVFP4 = 0, 1, 2, 3
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 
@@ -43,6 +50,17 @@ class WeightsDesc(ctypes.Structure):
 class Act4Desc(ctypes.Structure):
     """moesq_act4_t."""
     _fields_ = [("codes", _vp), ("scales", _vp), ("row_scale", _vp), ("rows", _i32), ("K", _i32)]
+
+
+class GateDesc(ctypes.Structure):
+    """moesq_gate_t."""
+    _fields_ = [("k", _i32), ("score", _i32), ("n_group", _i32), ("topk_group", _i32),
+                ("group_score", _i32), ("renormalize", _i32), ("scale", ctypes.c_float)]
+
+
+class MxDesc(ctypes.Structure):
+    """moesq_mx_t."""
+    _fields_ = [("codes", _vp), ("scales", _vp), ("rows", _i32), ("K", _i32), ("format", _i32)]
 
 
 def _sig(name, restype, *argtypes):
@@ -75,6 +93,14 @@ _tile = _sig("moesq_tile_weights", _i32, ctypes.POINTER(WeightsDesc), _vp, _vp, 
 _validate = _sig("moesq_validate", _i32, _vp, _i32, _i32, _i32, _vp, ctypes.POINTER(WeightsDesc),
                  ctypes.POINTER(ctypes.c_uint64), _vp)
 _stream_read = _sig("moesq_stream_read", _i32, _vp, _sz, _vp, _vp)
+_gate_topk = _sig("moesq_gate_topk", _i32, _vp, _i32, _i32, _i32, _vp, ctypes.POINTER(GateDesc), _vp,
+                  _vp, _vp, _vp)
+_mx_quantize = _sig("moesq_mx_quantize", _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp)
+_mx_decode = _sig("moesq_mx_decode", _i32, ctypes.POINTER(MxDesc), _vp, _vp)
+_rmsnorm = _sig("moesq_rmsnorm", _i32, _vp, _vp, _vp, _i32, _i32, ctypes.c_double, _vp, _vp, _i32, _vp,
+                _vp, _vp, _vp)
+_mx_gemm = _sig("moesq_mx_gemm", _i32, ctypes.POINTER(MxDesc), _vp, _i32, _i32, _vp, _i32,
+                ctypes.POINTER(MxDesc), _i32, _i32, _vp, _vp)
 _status_string = _sig("moesq_status_string", ctypes.c_char_p, _i32)
 _last_error = _sig("moesq_last_error", ctypes.c_char_p)
 _version = _sig("moesq_version", _i32)
@@ -86,6 +112,8 @@ EXPORTED = ["moesq_route", "moesq_route_workspace_bytes", "moesq_route_noalloc",
             "moesq_quantize_activations", "moesq_grouped_spgemm_act4",
             "moesq_pack_weights", "moesq_pack_weights_paired", "moesq_tile_weights",
             "moesq_decode_weights",
+            "moesq_gate_topk", "moesq_mx_quantize", "moesq_mx_decode", "moesq_rmsnorm",
+            "moesq_mx_gemm",
             "moesq_validate", "moesq_stream_read", "moesq_status_string",
             "moesq_last_error", "moesq_version"]
 
@@ -213,6 +241,74 @@ class Act4:
         u8 = dict(dtype=torch.uint8, device=device)
         return Act4(torch.empty(rows, K // 2, **u8), torch.empty(rows, K // 32, **u8),
                     torch.empty(rows, dtype=torch.float32, device=device))
+
+
+class Gate:
+    """Settings of the router's top-k selection (moesq_gate_t); build once and
+    pass to gate_topk."""
+
+    def __init__(self, k: int, score: int = SCORE_SOFTMAX, n_group: int = 1, topk_group: int = 1,
+                 group_score: int = GROUP_TOP2, renormalize: bool = True, scale: float = 1.0):
+        self.k = int(k)
+        self.desc = GateDesc(self.k, score, n_group, topk_group, group_score, int(bool(renormalize)),
+                             scale)
+
+
+class Mx:
+    """Device tensors of microscaled rows: scales uint8 [..., K/32] (E8M0) and
+    codes uint8 [..., K/2] (ROWS_MXFP4) or [..., K] (ROWS_MXFP8).  Activations
+    are [rows, ...]; MXFP4 weights [E, N, ...], or [N, ...] for one matrix."""
+
+    def __init__(self, codes, scales, format: int):
+        if format not in (ROWS_MXFP4, ROWS_MXFP8):
+            raise ValueError("format must be ROWS_MXFP4 or ROWS_MXFP8")
+        self.shape = tuple(codes.shape[:-1])
+        self.K = int(codes.shape[-1]) * (2 if format == ROWS_MXFP4 else 1)
+        if tuple(scales.shape) != self.shape + (self.K // 32,) or self.K % 32:
+            raise ValueError(f"scales has shape {tuple(scales.shape)}, expected "
+                             f"{self.shape + (self.K // 32,)} (K = {self.K}, a multiple of 32)")
+        self.rows = 1
+        for n in self.shape:
+            self.rows *= int(n)
+        self.codes, self.scales, self.format = codes, scales, format
+        self.desc = MxDesc(_ptr(codes, torch.uint8, "codes", True),
+                           _ptr(scales, torch.uint8, "scales", True), self.rows, self.K, format)
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+    @staticmethod
+    def empty(shape, K: int, format: int, device="cuda"):
+        """`shape`: the leading dimensions, (rows,) or (E, N)."""
+        u8 = dict(dtype=torch.uint8, device=device)
+        return Mx(torch.empty(*shape, K // 2 if format == ROWS_MXFP4 else K, **u8),
+                  torch.empty(*shape, K // 32, **u8), format)
+
+
+def _launch(stream, *tensors):
+    """(device context, raw stream) of a call on these tensors: all on one
+    device, which is made current for the launch; without a `stream` that
+    device's current one.  A stream of another device is refused."""
+    dev = None
+    for t in tensors:
+        if t is None or not t.is_cuda:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    if dev is None:
+        return _HERE, _stream(stream)
+    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+        raise ValueError(f"stream of {stream.device} for tensors on {dev}")
+    here = _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    if stream is None:
+        return here, torch.cuda.current_stream(dev).cuda_stream
+    return here, _stream(stream)
+
+
+_HERE = contextlib.nullcontext()
 
 
 # ------------------------------------------------------------ C-ABI mirrors
@@ -355,6 +451,85 @@ def moesq_decode_weights(w: Weights, expert: int, dense, stream=None):
     _sizes((dense, w.N * w.K, "dense"))
     _check(_decode(ctypes.byref(w.desc), expert, _ptr(dense, torch.bfloat16, "dense"),
                    _stream(stream)))
+
+
+def _dtype(t, name):
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def moesq_gate_topk(logits, T: int, E: int, bias, gate: Gate, n_rows, topk_ids, topk_weights,
+                    stream=None):
+    _sizes((logits, T * E, "logits"), (bias, E, "bias"), (n_rows, 1, "n_rows"),
+           (topk_ids, T * gate.k, "topk_ids"), (topk_weights, T * gate.k, "topk_weights"))
+    dtype = _dtype(logits, "logits")
+    args = (_ptr(logits, logits.dtype, "logits"), dtype, T, E, _ptr(bias, torch.float32, "bias", True),
+            ctypes.byref(gate.desc), _ptr(n_rows, torch.int32, "n_rows", True),
+            _ptr(topk_ids, torch.int32, "topk_ids"), _ptr(topk_weights, torch.float32, "topk_weights"))
+    here, st = _launch(stream, logits, bias, n_rows, topk_ids, topk_weights)
+    with here:
+        _check(_gate_topk(*args, st))
+
+
+def _rows_buffers(format, rows, K, codes, scales, row_scale=None):
+    """Size checks of quantized-row buffers."""
+    _sizes((codes, rows * K // (1 if format == ROWS_MXFP8 else 2), "codes"),
+           (scales, rows * K // 32, "scales"), (row_scale, rows, "row_scale"))
+
+
+def moesq_mx_quantize(x, rows: int, K: int, format: int, codes, scales, stream=None):
+    _sizes((x, rows * K, "x"))
+    _rows_buffers(format, rows, K, codes, scales)
+    dtype = _dtype(x, "x")
+    args = (_ptr(x, x.dtype, "x"), dtype, rows, K, format, _ptr(codes, torch.uint8, "codes"),
+            _ptr(scales, torch.uint8, "scales"))
+    here, st = _launch(stream, x, codes, scales)
+    with here:
+        _check(_mx_quantize(*args, st))
+
+
+def moesq_mx_decode(x: Mx, out, stream=None):
+    _sizes((out, x.rows * x.K, "out"))
+    ptr = _ptr(out, torch.bfloat16, "out")
+    here, st = _launch(stream, x.codes, x.scales, out)
+    with here:
+        _check(_mx_decode(ctypes.byref(x.desc), ptr, st))
+
+
+def moesq_rmsnorm(x, residual, weight, T: int, K: int, eps: float, residual_out, y,
+                  rows_format: int = ROWS_NONE, codes=None, scales=None, row_scale=None, stream=None):
+    _sizes((x, T * K, "x"), (residual, T * K, "residual"), (weight, K, "weight"),
+           (residual_out, T * K, "residual_out"), (y, T * K, "y"))
+    if rows_format != ROWS_NONE:
+        _rows_buffers(rows_format, T, K, codes, scales, row_scale)
+    bf, u8 = torch.bfloat16, torch.uint8
+    args = (_ptr(x, bf, "x"), _ptr(residual, bf, "residual", True), _ptr(weight, bf, "weight"), T, K, eps,
+            _ptr(residual_out, bf, "residual_out", True), _ptr(y, bf, "y", True), rows_format,
+            _ptr(codes, u8, "codes", True), _ptr(scales, u8, "scales", True),
+            _ptr(row_scale, torch.float32, "row_scale", True))
+    here, st = _launch(stream, x, residual, weight, residual_out, y, codes, scales, row_scale)
+    with here:
+        _check(_rmsnorm(*args, st))
+
+
+def moesq_mx_gemm(x: Mx, perm, T: int, k: int, expert_offsets, M: int, w: Mx, E: int, epilogue: int,
+                  y, stream=None):
+    if E < 1 or w.rows % E:
+        raise ValueError(f"weights have {w.rows} rows, not E = {E} matrices")
+    N = w.rows // E
+    _sizes((perm, M, "perm"), (expert_offsets, E + 1, "expert_offsets"),
+           (y, M * (N // 2 if (epilogue & ~OUT_FLAT) == EPI_SWIGLU else N), "y"))
+    if x.K != w.K:
+        raise ValueError(f"activations have K = {x.K}, the weights {w.K}")
+    if x.rows != (T if perm is not None else M):
+        raise ValueError(f"activations have {x.rows} rows, need {T if perm is not None else M}")
+    args = (ctypes.byref(x.desc), _ptr(perm, torch.int32, "perm", True), T, k,
+            _ptr(expert_offsets, torch.int32, "expert_offsets", True), M, ctypes.byref(w.desc), E,
+            epilogue, _ptr(y, torch.bfloat16, "y"))
+    here, st = _launch(stream, x.codes, x.scales, perm, expert_offsets, w.codes, w.scales, y)
+    with here:
+        _check(_mx_gemm(*args, st))
 
 
 VALIDATE_CHECKS = ("ids", "offsets", "masks", "scales", "global_scales")
@@ -518,4 +693,81 @@ def tile_weights(w: Weights, stream=None) -> Weights:
 def decode_weights(w: Weights, expert: int, stream=None):
     out = torch.empty(w.N, w.K, dtype=torch.bfloat16, device=w.values.device)
     moesq_decode_weights(w, expert, out, stream)
+    return out
+
+
+def gate_topk(logits, gate: Gate, bias=None, n_rows=None, stream=None):
+    """Router scores [T, E] (float32 or bfloat16) -> (topk_ids int32 [T*k],
+    topk_weights float32 [T*k]) as moesq_route and moesq_unpermute take them.
+    bias: float32 [E], moves the selection but not the weights.  n_rows: a
+    1-element int32 device tensor; rows from *n_rows on get ids -1."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [T, E], got {tuple(logits.shape)}")
+    T, E = logits.shape
+    ids = torch.empty(T * gate.k, dtype=torch.int32, device=logits.device)
+    weights = torch.empty(T * gate.k, dtype=torch.float32, device=logits.device)
+    moesq_gate_topk(logits, T, E, bias, gate, n_rows, ids, weights, stream)
+    return ids, weights
+
+
+def mx_quantize(x, format: int = ROWS_MXFP4, stream=None) -> Mx:
+    """float32 or bfloat16 [rows, K] or [E, N, K] -> its MX rows."""
+    if x.dim() < 2:
+        raise ValueError(f"x must be [..., K], got {tuple(x.shape)}")
+    K = x.shape[-1]
+    _dtype(x, "x")
+    if format not in (ROWS_MXFP4, ROWS_MXFP8) or K % 32:
+        raise ValueError(f"need an MX format and K % 32 == 0, got format {format}, K = {K}")
+    q = Mx.empty(x.shape[:-1], K, format, device=x.device)
+    moesq_mx_quantize(x, q.rows, K, format, q.codes, q.scales, stream)
+    return q
+
+
+def mx_decode(x: Mx, stream=None):
+    """The bfloat16 values that MX rows stand for, [..., K]."""
+    out = torch.empty(*x.shape, x.K, dtype=torch.bfloat16, device=x.codes.device)
+    moesq_mx_decode(x, out, stream)
+    return out
+
+
+def rmsnorm(x, weight, eps: float = 1e-6, residual=None, y: bool = True, rows: int | None = None,
+            stream=None):
+    """RMS norm of bfloat16 rows [T, K], after adding `residual` if given.
+    Returns (y, residual_out, quantized rows): y is None with y=False,
+    residual_out (x + residual in bfloat16) None without a residual, the rows
+    an Mx (rows=ROWS_MXFP4 / ROWS_MXFP8), an Act4 (ROWS_NVFP4) or None."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, K], got {tuple(x.shape)}")
+    T, K = x.shape
+    rows = rows or ROWS_NONE
+    out = torch.empty_like(x) if y else None
+    res = torch.empty_like(x) if residual is not None else None
+    q, codes, scales, row_scale = None, None, None, None
+    if rows in (ROWS_MXFP4, ROWS_MXFP8):
+        q = Mx.empty((T,), K, rows, device=x.device)
+    elif rows == ROWS_NVFP4:
+        q = Act4.empty(T, K, device=x.device)
+        row_scale = q.row_scale
+    if q is not None:
+        codes, scales = q.codes, q.scales
+    moesq_rmsnorm(x, residual, weight, T, K, eps, res, out, rows, codes, scales, row_scale, stream)
+    return out, res, q
+
+
+def mx_gemm(x: Mx, w: Mx, expert_offsets=None, perm=None, k: int = 1, epilogue: int = EPI_NONE,
+            out=None, stream=None):
+    """Product of MX rows with MXFP4 weights: dense (w [N, ...] or [1, N, ...],
+    no expert_offsets), or grouped over the E experts of w [E, N, ...].  With
+    `perm`, routed row r reads row perm[r] // k of x; else x's rows are the
+    routed rows."""
+    E = w.shape[0] if len(w.shape) == 2 else 1
+    N = w.shape[-1]
+    M = x.rows * k if perm is not None else x.rows
+    n_out = N // 2 if (epilogue & ~OUT_FLAT) == EPI_SWIGLU else N
+    if out is None:
+        out = torch.empty(M, n_out, dtype=torch.bfloat16, device=x.codes.device)
+    elif tuple(out.shape) != (M, n_out):
+        raise ValueError(f"out must be [{M}, {n_out}], got {tuple(out.shape)}")
+    moesq_mx_gemm(x, perm, x.rows if perm is not None else 0, k, expert_offsets, M, w, E, epilogue, out,
+                  stream)
     return out
