@@ -10,10 +10,13 @@
 // of row l % 16 and block q whatever the element type.  Weights are the first
 // operand, tokens the second: a lane's four results are four neighbouring
 // output features of one token.
+#include <stddef.h>
+
 #include <algorithm>
 #include <type_traits>
 
 #include "mx.hpp"
+#include "route_dev.hpp"
 
 namespace moesq {
 
@@ -27,22 +30,21 @@ struct MxGemmArgs {
   uint16_t *y;
   int k, M, E, N, K;
   int flat;
-  bool far;                    // an expert's codes or all activation codes from 4 GiB on
-  uint32_t x_bytes, xs_bytes;  // of all activation rows (not far)
+  uint32_t x_bytes, xs_bytes;  // of all activation rows
 };
 
 // Element formats of the MFMA's operands.
 constexpr int MX_E4M3 = 0, MX_E2M1 = 4;
 
-template <bool FP8>
+// The scales are byte SEL of their registers.
+template <bool FP8, int SEL>
 __device__ __forceinline__ f32x4_t mfma_mx(i32x8_t w, i32x8_t x, f32x4_t c, uint32_t sw, uint32_t sx) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, MX_E2M1, FP8 ? MX_E4M3 : MX_E2M1, 0,
-                                                          (int)sw, 0, (int)sx);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, MX_E2M1, FP8 ? MX_E4M3 : MX_E2M1, SEL,
+                                                          (int)sw, SEL, (int)sx);
 }
 
 // Rows of expert e.
 __device__ __forceinline__ int2 mx_rows_of(const MxGemmArgs &a, int e) {
-  if (!a.offsets) return make_int2(0, a.M);
   const int lo = min(max(a.offsets[e], 0), a.M), hi = min(max(a.offsets[e + 1], 0), a.M);
   return make_int2(lo, hi);
 }
@@ -51,31 +53,39 @@ struct MxTile {
   int e, row0, rows;   // e < 0: no such tile
 };
 
+constexpr int FIND_BATCH = 4;
+
 // The t-th token tile of up to BM rows, experts in order; a whole wave calls
 // it and gets the same answer in every lane.
 template <int BM>
 __device__ __forceinline__ MxTile mx_find_tile(const MxGemmArgs &a, int t, int lane) {
+  if (!a.offsets) {
+    const int row0 = t * BM;
+    return row0 < a.M ? MxTile{0, row0, min(BM, a.M - row0)} : MxTile{-1, 0, 0};
+  }
   int before = 0;
-  for (int e0 = 0; e0 < a.E; e0 += 64) {
-    const int e = e0 + lane;
-    int2 r = make_int2(0, 0);
-    if (e < a.E) r = mx_rows_of(a, e);
-    const int tiles = r.y > r.x ? (r.y - r.x + BM - 1) / BM : 0;
-    int incl = tiles;
+  for (int b0 = 0; b0 < a.E; b0 += 64 * FIND_BATCH) {
+    int2 r[FIND_BATCH];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += v;
+    for (int j = 0; j < FIND_BATCH; ++j) {   // loads of a batch in flight together
+      const int e = b0 + 64 * j + lane;
+      r[j] = e < a.E ? mx_rows_of(a, e) : make_int2(0, 0);
     }
-    const uint64_t hit = __ballot(before + incl > t);
-    if (hit) {
-      const int who = __ffsll((unsigned long long)hit) - 1;
-      const int lo = __shfl(r.x, who, 64), hi = __shfl(r.y, who, 64);
-      const int first = before + __shfl(incl - tiles, who, 64);
-      const int row0 = lo + (t - first) * BM;
-      return MxTile{e0 + who, row0, min(BM, hi - row0)};
+#pragma unroll
+    for (int j = 0; j < FIND_BATCH; ++j) {
+      const int e0 = b0 + 64 * j;
+      if (e0 >= a.E) break;
+      const int tiles = r[j].y > r[j].x ? (r[j].y - r[j].x + BM - 1) / BM : 0;
+      const int incl = wave_incl_scan(tiles, lane);
+      const uint64_t hit = __ballot(before + incl > t);
+      if (hit) {
+        const int who = __ffsll((unsigned long long)hit) - 1;
+        const int lo = __shfl(r[j].x, who, 64), hi = __shfl(r[j].y, who, 64);
+        const int row0 = lo + (t - before - __shfl(incl - tiles, who, 64)) * BM;
+        return MxTile{e0 + who, row0, min(BM, hi - row0)};
+      }
+      before += __shfl(incl, 63, 64);
     }
-    before += __shfl(incl, 63, 64);
   }
   return MxTile{-1, 0, 0};
 }
@@ -101,102 +111,13 @@ __device__ __forceinline__ i32x8_t as_operand(uint4 lo, uint4 hi) {
   return v;
 }
 
-// The lane's 16 bytes of E2M1 codes and scale byte of positions
-// [k0 + 32q, +32) of a row; zero behind K or without a row.
-__device__ __forceinline__ void load_fp4(const uint8_t *codes, const uint8_t *scales, bool ok, int blk,
-                                         int nb, i32x8_t &v, uint32_t &s) {
-  uint4 c = make_uint4(0, 0, 0, 0);
-  s = 0;
-  if (ok && blk < nb) {
-    c = *reinterpret_cast<const uint4 *>(codes + (size_t)blk * 16);
-    s = scales[blk];
-  }
-  v = as_operand(c, make_uint4(0, 0, 0, 0));
-}
-__device__ __forceinline__ void load_fp8(const uint8_t *codes, const uint8_t *scales, bool ok, int b0, int q,
-                                         int nb, i32x8_t &v, uint32_t &s) {
-  uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-  s = 0;
-  if (ok) {
-    if (b0 + (q >> 1) < nb) lo = *reinterpret_cast<const uint4 *>(codes + (size_t)b0 * 32 + 16 * q);
-    if (b0 + 2 + (q >> 1) < nb) hi = *reinterpret_cast<const uint4 *>(codes + (size_t)b0 * 32 + 64 + 16 * q);
-    if (b0 + q < nb) s = scales[b0 + q];
-  }
-  v = as_operand(lo, hi);
-}
-
-constexpr int MXG_WAVES = 4;
-
-// One wave per 16 output features x 16 tokens.
-template <bool FP8, bool SWIGLU>
-__global__ __launch_bounds__(MXG_WAVES * 64) void mx_gemm_kernel(MxGemmArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int q = lane >> 4, rl = lane & 15;
-  const int cols = SWIGLU ? a.N / 2 : a.N;
-  const int n0 = (blockIdx.y * MXG_WAVES + wave) * 16;
-  if (n0 >= cols) return;
-  const MxTile t = mx_find_tile<16>(a, blockIdx.x, lane);
-  if (t.e < 0) return;
-  const int nb = a.K / 32;
-  const int src = rl < t.rows ? mx_src(a, t.row0 + rl) : -1;
-  const bool ok = src >= 0;
-  const uint8_t *xc = a.xc + (size_t)(ok ? src : 0) * (a.K / (FP8 ? 1 : 2));
-  const uint8_t *xs = a.xs + (size_t)(ok ? src : 0) * nb;
-  const size_t wrow = (size_t)t.e * a.N + n0 + rl;
-  const uint8_t *wc = a.wc + wrow * (a.K / 2), *ws = a.ws + wrow * nb;
-  const size_t up_c = (size_t)cols * (a.K / 2), up_s = (size_t)cols * nb;
-  f32x4_t acc = {0, 0, 0, 0}, acc2 = {0, 0, 0, 0};
-  for (int b0 = 0; b0 < nb; b0 += 4) {
-    i32x8_t X, W;
-    uint32_t sx, sw;
-    if constexpr (FP8)
-      load_fp8(xc, xs, ok, b0, q, nb, X, sx);
-    else
-      load_fp4(xc, xs, ok, b0 + q, nb, X, sx);
-    load_fp4(wc, ws, true, b0 + q, nb, W, sw);
-    acc = mfma_mx<FP8>(W, X, acc, sw, sx);
-    if constexpr (SWIGLU) {
-      load_fp4(wc + up_c, ws + up_s, true, b0 + q, nb, W, sw);
-      acc2 = mfma_mx<FP8>(W, X, acc2, sw, sx);
-    }
-  }
-  if (rl >= t.rows) return;
-  const int dst = mx_dst(a, t.row0 + rl);
-  if (dst < 0) return;
-  float v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = SWIGLU ? silu_f32(acc[i]) * acc2[i] : acc[i];
-  *reinterpret_cast<uint2 *>(a.y + (size_t)dst * cols + n0 + 4 * q) =
-      make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-}
-
-// ------------------------------------------------------------------ LDS-tiled kernel
+// ------------------------------------------------------------------ copies to LDS
 //
-// A workgroup of 8 waves computes BN weight rows x BM tokens.  Stages of 256
-// positions of both operands go from global memory to LDS without passing
-// through registers, two stages in turn: while one is contracted the next is
-// in flight.  (The copies are written as asm without register results, so
-// the compiler's wait counts know nothing of them; the only waits for them
-// are the one asm statement and the barrier at the head of each stage, and
-// the reads of LDS stay ordinary loads that the compiler schedules.)
-//
-// LDS rows are as in memory, 16-byte chunks of a row permuted by its row
-// number so that the 16 rows that read one chunk position together touch all
-// 64 banks once: chunk c of row r sits at c ^ ((r >> 1) & 7) in the 128-byte
-// rows of E2M1 codes and at c ^ (r & 15) in the 256-byte rows of E4M3 ones.
+// Written as asm without register results, so the compiler's wait counts know
+// nothing of them: a kernel waits for its copies by a count of its own, and
+// its reads of LDS stay ordinary loads that the compiler schedules.
 
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
-
-// 32 x 64 by 64 x 32: lane l holds row l % 32 and, with h = l / 32, the
-// positions [32h, 32h + 32) of the 64 (E2M1) or [16h, +16) and [32 + 16h, +16)
-// (E4M3); its results are features 8 (i / 4) + 4 h + i % 4 of token l % 32.
-// The scales are byte SEL of their registers.
-template <bool FP8, int SEL>
-__device__ __forceinline__ f32x16_t mfma_mx32(i32x8_t w, i32x8_t x, f32x16_t c, uint32_t sw, uint32_t sx) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, MX_E2M1, FP8 ? MX_E4M3 : MX_E2M1, SEL,
-                                                         (int)sw, SEL, (int)sx);
-}
 
 __device__ __forceinline__ i32x4_t raw_buffer(const void *p, uint32_t bytes) {
   const uint64_t u = (uint64_t)(uintptr_t)p;
@@ -222,6 +143,357 @@ __device__ __forceinline__ void copy4_to_lds(uint32_t lds, i32x4_t buf, uint32_t
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
                "s"(buf), "s"(soff)
                : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_copies() {   // all but the last N have landed
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Adds the KSPLIT waves' sums (through `lds`, no longer in use otherwise), and
+// stores the results.  The waves of a row group each finish some of its token
+// fragments.
+template <bool SWIGLU, int KSPLIT, int FM>
+__device__ __forceinline__ void mx_stream_finish(const MxGemmArgs &a, const MxTile &t, f32x4_t (&acc)[FM], void *lds,
+                                                 int c0, int cols, bool live, int wave, int lane) {
+  const int q = lane >> 4, rl = lane & 15, kw = wave % KSPLIT;
+  f32x4_t *part = static_cast<f32x4_t *>(lds);     // [waves][FM][64]
+  if constexpr (KSPLIT > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < FM; ++g) part[(wave * FM + g) * 64 + lane] = acc[g];
+    __syncthreads();
+    if (kw >= FM) return;
+  }
+#pragma unroll
+  for (int g = 0; g < FM; ++g) {
+    if (KSPLIT > 1 && g % KSPLIT != kw) continue;
+    f32x4_t v = acc[g];
+    if constexpr (KSPLIT > 1) {
+      v = part[((wave - kw) * FM + g) * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < KSPLIT; ++w) v += part[((wave - kw + w) * FM + g) * 64 + lane];
+    }
+    f32x4_t up;
+    if constexpr (SWIGLU) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) up[i] = __shfl_down(v[i], 32, 64);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = silu_f32(v[i]) * up[i];
+    }
+    const int r = 16 * g + rl;
+    if (!live || r >= t.rows || (SWIGLU && q >= 2)) continue;
+    const int dst = mx_dst(a, t.row0 + r);
+    if (dst < 0) continue;
+    const bool ok = mx_src(a, t.row0 + r) >= 0;
+    *reinterpret_cast<uint2 *>(a.y + (size_t)dst * cols + c0 + 4 * q) =
+        ok ? make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])) : make_uint2(0, 0);
+  }
+}
+
+// Chunk positions in LDS: rows are as in memory, their 16-byte pieces permuted
+// by the row number so that the 16 rows that read one piece together touch
+// all 64 banks once.  Piece c of row r of 128-byte rows (256 positions of
+// E2M1) and of 256-byte rows (E4M3).
+__device__ __forceinline__ int piece4(int r, int c) { return c ^ ((r >> 1) & 7); }
+__device__ __forceinline__ int piece8(int r, int c) { return c ^ (r & 15); }
+
+// ------------------------------------------------------------------ streaming kernel (K % 128 == 0)
+//
+// Few rows: bound by the stream of weights.  A wave contracts 16 weight rows
+// with FM fragments of 16 tokens in stages of 256 positions, copied to a ring
+// of its own in LDS: an MFMA operand takes 16 bytes of each of 16 rows, which
+// as a direct load is 64 separate pieces for the address unit (a quarter of
+// its rate), while a copy takes whole lines.  No wave waits for another but
+// for the final sum: KSPLIT waves of a workgroup share 16 rows, each with its
+// own stages, and add their sums in LDS in a fixed order.
+//
+// SwiGLU: rows 0-7 of a fragment are gate rows, 8-15 the up rows of the same
+// eight columns.
+
+constexpr int mxs_waves(int ksplit) { return ksplit < 4 ? 4 : ksplit; }
+
+template <bool FP8, int FM>
+struct MxRing {
+  uint8_t w[16 * 128];
+  uint8_t x[FM * 16 * (FP8 ? 256 : 128)];
+  uint8_t ws[256];                                 // 16 rows x 8, twice
+  uint8_t xs[FM > 1 ? FM * 128 : 256];
+};
+
+template <bool FP8, bool SWIGLU, int KSPLIT, int FM, int STAGES>
+__global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGemmArgs a) {
+  constexpr int WAVES = mxs_waves(KSPLIT);
+  constexpr int RG = WAVES / KSPLIT;               // fragments of 16 weight rows a workgroup
+  constexpr int FC = SWIGLU ? 8 : 16;              // output columns a fragment
+  constexpr int XB = FP8 ? 256 : 128;              // bytes of a token's stage
+  constexpr int CX = FM * 16 * XB / 1024;          // copies of token codes
+  constexpr int COPIES = 2 + CX + 2;               // of a stage
+  using Ring = MxRing<FP8, FM>;
+  __shared__ __attribute__((aligned(1024))) Ring ring[WAVES][STAGES];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, rl = lane & 15;
+  const int cols = SWIGLU ? a.N / 2 : a.N;
+  const int groups = (cols / FC + RG - 1) / RG;
+  const MxTile t = mx_find_tile<16 * FM>(a, blockIdx.x / groups, lane);
+  if (t.e < 0) return;
+  const int kw = wave % KSPLIT;
+  const int c0 = ((blockIdx.x % groups) * RG + wave / KSPLIT) * FC;
+  const bool live = c0 < cols;                     // (columns come in whole fragments)
+  const int K = a.K, nb = K / 32;
+
+  // rows that are not there read row 0; their results are not used
+  auto w_row = [&](int r) {
+    return (uint32_t)(!live ? 0 : SWIGLU ? c0 + (r & 7) + (r >> 3) * cols : c0 + r);
+  };
+  auto x_row = [&](int r) { return (uint32_t)(r < t.rows ? max(mx_src(a, t.row0 + r), 0) : 0); };
+  const i32x4_t wbuf = raw_buffer(a.wc + (size_t)t.e * a.N * (K / 2), (uint32_t)a.N * (uint32_t)(K / 2));
+  const i32x4_t wsbuf = raw_buffer(a.ws + (size_t)t.e * a.N * nb, (uint32_t)a.N * (uint32_t)nb);
+  const i32x4_t xbuf = raw_buffer(a.xc, a.x_bytes), xsbuf = raw_buffer(a.xs, a.xs_bytes);
+  uint32_t wo[2], xo[CX];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = i * 8 + (lane >> 3);
+    wo[i] = w_row(r) * (uint32_t)(K / 2) + 16 * piece4(r, lane & 7);
+  }
+  const uint32_t wso = w_row((lane >> 1) & 15) * (uint32_t)nb + 4 * (lane & 1);
+#pragma unroll
+  for (int i = 0; i < CX; ++i) {
+    const int r = i * (1024 / XB) + lane / (XB / 16);
+    xo[i] = x_row(r) * (uint32_t)(K / (FP8 ? 1 : 2)) + 16 * (FP8 ? piece8(r, lane & 15) : piece4(r, lane & 7));
+  }
+  const uint32_t xso = x_row((lane >> 1) & (16 * FM - 1)) * (uint32_t)nb + 4 * (lane & 1);
+  const uint32_t lds0 = lds_offset(&ring[wave][0]);
+  // (positions behind K in the last stage, other rows' or the buffers'
+  // zeros, are not contracted)
+  auto fetch = [&](int slot, int c) {
+    const uint32_t base = lds0 + slot * (uint32_t)sizeof(Ring), ks = (uint32_t)c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) copy16_to_lds(base + i * 1024, wbuf, wo[i], ks * 128);
+    copy4_to_lds(base + offsetof(Ring, ws), wsbuf, wso, ks * 8);
+#pragma unroll
+    for (int i = 0; i < CX; ++i) copy16_to_lds(base + offsetof(Ring, x) + i * 1024, xbuf, xo[i], ks * XB);
+    copy4_to_lds(base + offsetof(Ring, xs), xsbuf, xso, ks * 8);
+  };
+  f32x4_t acc[FM];
+#pragma unroll
+  for (int g = 0; g < FM; ++g) acc[g] = f32x4_t{0, 0, 0, 0};
+  auto step = [&](const Ring &k, int s) {          // 128 positions
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint32_t sw = *reinterpret_cast<const uint32_t *>(k.ws + rl * 8 + 4 * s) >> (8 * q);
+    const i32x8_t W = as_operand(*reinterpret_cast<const uint4 *>(k.w + rl * 128 + 16 * piece4(rl, 4 * s + q)), zero);
+#pragma unroll
+    for (int g = 0; g < FM; ++g) {
+      const int r = 16 * g + rl;
+      const uint32_t sx = *reinterpret_cast<const uint32_t *>(k.xs + r * 8 + 4 * s) >> (8 * q);
+      i32x8_t X;
+      if constexpr (FP8)
+        X = as_operand(*reinterpret_cast<const uint4 *>(k.x + r * 256 + 16 * piece8(r, 8 * s + q)),
+                       *reinterpret_cast<const uint4 *>(k.x + r * 256 + 16 * piece8(r, 8 * s + 4 + q)));
+      else
+        X = as_operand(*reinterpret_cast<const uint4 *>(k.x + r * 128 + 16 * piece4(r, 4 * s + q)), zero);
+      acc[g] = mfma_mx<FP8, 0>(W, X, acc[g], sw, sx);
+    }
+  };
+  // this wave's stages: kw, kw + KSPLIT, ...
+  const int n = ((K + 255) / 256 - kw + KSPLIT - 1) / KSPLIT;
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i)
+    if (i < n) fetch(i, kw + i * KSPLIT);
+  int slot = 0;
+  for (int i = 0; i < n; ++i) {
+    const int behind = n - 1 - i;                  // stages in flight behind this one
+    if (behind >= STAGES - 1) wait_copies<(STAGES - 1) * COPIES>();
+    else if (STAGES > 3 && behind == 2) wait_copies<2 * COPIES>();
+    else if (STAGES > 2 && behind == 1) wait_copies<COPIES>();
+    else wait_copies<0>();
+    const int c = kw + i * KSPLIT;
+    step(ring[wave][slot], 0);
+    if (K - 256 * c > 128) step(ring[wave][slot], 1);
+    // the slot's reads are done before it is written again
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (i + STAGES < n) fetch(slot, c + STAGES * KSPLIT);
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
+  }
+  mx_stream_finish<SWIGLU, KSPLIT, FM>(a, t, acc, &ring[0][0], c0, cols, live, wave, lane);
+}
+
+// ------------------------------------------------------------------ direct kernel (any K)
+//
+// Rows of K % 128 != 0 have scale bytes at any alignment and end inside an
+// MFMA step.  The waves are those of the streaming kernel, with operands
+// straight from global memory in chunks of 256 positions, the next one in
+// flight, and codes behind K zero.  The order of the positions is free as
+// long as both operands agree: MFMA block j of step s is the chunk's block 2j
+// + s, so a lane's codes are 32 contiguous bytes and its scales two.
+
+template <bool FP8, int FM>
+struct MxChunk {
+  uint4 w[2];
+  uint4 x[FM][FP8 ? 4 : 2];
+  uint32_t sw, sx[FM];
+};
+
+// One lane's rows: offsets (32 bits: an expert's codes and the activations'
+// stay under 4 GiB) from the bases of the expert and of the activations.
+template <int FM>
+struct MxLane {
+  const uint8_t *w, *ws, *x, *xs;
+  uint32_t wo, wso, xo[FM], xso[FM];
+};
+
+// Scale bytes 2j, 2j + 1 of a chunk for lane group j; rows need no alignment.
+__device__ __forceinline__ uint32_t load_scales2(const uint8_t *p) {
+  uint16_t v;
+  __builtin_memcpy(&v, p, 2);
+  return v;
+}
+
+// Chunk c of the lane's rows; `left` blocks of it lie inside K (8: all).
+__device__ __forceinline__ uint4 load16(const uint8_t *base, uint32_t off) {
+  return *reinterpret_cast<const uint4 *>(base + off);
+}
+
+template <bool FP8, int FM>
+__device__ __forceinline__ void load_chunk(MxChunk<FP8, FM> &k, const MxLane<FM> &p, int c, int q, int left) {
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint32_t cw = 128u * c, cs = 8u * c, cx = (FP8 ? 256u : 128u) * c;
+  if (left >= 8) {
+    k.w[0] = load16(p.w, p.wo + cw + 32 * q);
+    k.w[1] = load16(p.w, p.wo + cw + 32 * q + 16);
+    k.sw = load_scales2(p.ws + (p.wso + cs + 2 * q));
+#pragma unroll
+    for (int g = 0; g < FM; ++g) {
+      if constexpr (FP8) {
+        // bytes [16 (q % 2), +16) of blocks 2 (q / 2) + s and 4 + 2 (q / 2) + s
+        const uint32_t o = p.xo[g] + cx + 64 * (q >> 1) + 16 * (q & 1);
+        k.x[g][0] = load16(p.x, o);
+        k.x[g][1] = load16(p.x, o + 128);
+        k.x[g][2] = load16(p.x, o + 32);
+        k.x[g][3] = load16(p.x, o + 160);
+      } else {
+        k.x[g][0] = load16(p.x, p.xo[g] + cx + 32 * q);
+        k.x[g][1] = load16(p.x, p.xo[g] + cx + 32 * q + 16);
+      }
+      k.sx[g] = load_scales2(p.xs + (p.xso[g] + cs + 2 * q));
+    }
+    return;
+  }
+  k.sw = 0;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int b = 2 * q + s;
+    k.w[s] = b < left ? load16(p.w, p.wo + cw + 16 * b) : zero;
+    if (b < left) k.sw |= (uint32_t)p.ws[p.wso + cs + b] << (8 * s);
+  }
+#pragma unroll
+  for (int g = 0; g < FM; ++g) {
+    k.sx[g] = 0;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int b = 2 * q + s;
+      if (b < left) k.sx[g] |= (uint32_t)p.xs[p.xso[g] + cs + b] << (8 * s);
+      if constexpr (FP8) {
+        const int b0 = 2 * (q >> 1) + s, b1 = b0 + 4;
+        const uint32_t o = p.xo[g] + cx + 16 * (q & 1);
+        k.x[g][2 * s] = b0 < left ? load16(p.x, o + 32 * b0) : zero;
+        k.x[g][2 * s + 1] = b1 < left ? load16(p.x, o + 32 * b1) : zero;
+      } else {
+        k.x[g][s] = b < left ? load16(p.x, p.xo[g] + cx + 16 * b) : zero;
+      }
+    }
+  }
+}
+
+template <bool FP8, int FM>
+__device__ __forceinline__ void contract_chunk(f32x4_t (&acc)[FM], const MxChunk<FP8, FM> &k) {
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int g = 0; g < FM; ++g) {
+      const i32x8_t X = FP8 ? as_operand(k.x[g][2 * s], k.x[g][FP8 ? 2 * s + 1 : 0]) : as_operand(k.x[g][s], zero);
+      acc[g] = s == 0 ? mfma_mx<FP8, 0>(as_operand(k.w[0], zero), X, acc[g], k.sw, k.sx[g])
+                      : mfma_mx<FP8, 1>(as_operand(k.w[1], zero), X, acc[g], k.sw, k.sx[g]);
+    }
+}
+
+template <bool FP8, bool SWIGLU, int KSPLIT, int FM>
+__global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_direct_kernel(MxGemmArgs a) {
+  constexpr int WAVES = mxs_waves(KSPLIT);
+  constexpr int RG = WAVES / KSPLIT;              // fragments of 16 weight rows a workgroup
+  constexpr int FC = SWIGLU ? 8 : 16;              // output columns a fragment
+  __shared__ f32x4_t part[KSPLIT > 1 ? WAVES * FM * 64 : 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, rl = lane & 15;
+  const int cols = SWIGLU ? a.N / 2 : a.N;
+  const int groups = (cols / FC + RG - 1) / RG;
+  const MxTile t = mx_find_tile<16 * FM>(a, blockIdx.x / groups, lane);
+  if (t.e < 0) return;
+  const int kw = wave % KSPLIT;
+  const int c0 = ((blockIdx.x % groups) * RG + wave / KSPLIT) * FC;
+  const bool live = c0 < cols;                     // (columns come in whole fragments)
+  const int nb = a.K / 32;
+  int n = live ? c0 + rl : 0;
+  if constexpr (SWIGLU) n = live ? c0 + (rl & 7) + (rl >> 3) * cols : 0;
+  MxLane<FM> p;
+  p.w = a.wc + (size_t)t.e * a.N * (a.K / 2);
+  p.ws = a.ws + (size_t)t.e * a.N * nb;
+  p.x = a.xc;
+  p.xs = a.xs;
+  p.wo = (uint32_t)n * (uint32_t)(a.K / 2);
+  p.wso = (uint32_t)n * (uint32_t)nb;
+#pragma unroll
+  for (int g = 0; g < FM; ++g) {
+    // rows that are not there read row 0; their results are not used
+    const int r = 16 * g + rl;
+    const uint32_t src = r < t.rows ? max(mx_src(a, t.row0 + r), 0) : 0;
+    p.xo[g] = src * (uint32_t)(a.K / (FP8 ? 1 : 2));
+    p.xso[g] = src * (uint32_t)nb;
+  }
+  f32x4_t acc[FM];
+#pragma unroll
+  for (int g = 0; g < FM; ++g) acc[g] = f32x4_t{0, 0, 0, 0};
+  const int chunks = (nb + 7) / 8;
+  MxChunk<FP8, FM> A, B;
+  int c = kw;
+  if (c < chunks) load_chunk(A, p, c, q, nb - 8 * c);
+  for (; c < chunks; c += 2 * KSPLIT) {
+    const int c1 = c + KSPLIT, c2 = c + 2 * KSPLIT;
+    if (c1 < chunks) load_chunk(B, p, c1, q, nb - 8 * c1);
+    contract_chunk(acc, A);
+    if (c1 >= chunks) break;
+    if (c2 < chunks) load_chunk(A, p, c2, q, nb - 8 * c2);
+    contract_chunk(acc, B);
+  }
+  mx_stream_finish<SWIGLU, KSPLIT, FM>(a, t, acc, part, c0, cols, live, wave, lane);
+}
+
+// ------------------------------------------------------------------ LDS-tiled kernel
+//
+// A workgroup of 8 waves computes BN weight rows x BM tokens.  Stages of 256
+// positions of both operands go from global memory to LDS without passing
+// through registers, two stages in turn: while one is contracted the next is
+// in flight.  (The copies are written as asm without register results, so
+// the compiler's wait counts know nothing of them; the only waits for them
+// are the one asm statement and the barrier at the head of each stage, and
+// the reads of LDS stay ordinary loads that the compiler schedules.)
+//
+// LDS rows are as in memory, 16-byte chunks of a row permuted by its row
+// number so that the 16 rows that read one chunk position together touch all
+// 64 banks once: chunk c of row r sits at c ^ ((r >> 1) & 7) in the 128-byte
+// rows of E2M1 codes and at c ^ (r & 15) in the 256-byte rows of E4M3 ones.
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// 32 x 64 by 64 x 32: lane l holds row l % 32 and, with h = l / 32, the
+// positions [32h, 32h + 32) of the 64 (E2M1) or [16h, +16) and [32 + 16h, +16)
+// (E4M3); its results are features 8 (i / 4) + 4 h + i % 4 of token l % 32.
+// The scales are byte SEL of their registers.
+template <bool FP8, int SEL>
+__device__ __forceinline__ f32x16_t mfma_mx32(i32x8_t w, i32x8_t x, f32x16_t c, uint32_t sw, uint32_t sx) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, MX_E2M1, FP8 ? MX_E4M3 : MX_E2M1, SEL,
+                                                         (int)sw, SEL, (int)sx);
 }
 
 constexpr int MXT_WAVES = 8, MXT_THREADS = MXT_WAVES * 64;
@@ -414,20 +686,50 @@ __global__ __launch_bounds__(MXT_THREADS, 2) void mx_tiled_kernel(MxGemmArgs a) 
   }
 }
 
+// Upper bound of the token tiles of BM rows: an expert with rows has at most
+// one partial tile.
+static long long mx_tiles(const MxGemmArgs &a, int bm) {
+  return ((long long)a.M + (long long)std::min(a.E, a.M) * (bm - 1)) / bm;
+}
+
+template <bool FP8, bool SWIGLU, int KSPLIT, int FM>
+static void launch_stream(const MxGemmArgs &a, hipStream_t stream) {
+  const int frags = a.N / 16, rg = mxs_waves(KSPLIT) / KSPLIT;
+  const long long tiles = mx_tiles(a, 16 * FM);
+  const dim3 grid((unsigned)(tiles * ((frags + rg - 1) / rg))), block(mxs_waves(KSPLIT) * 64);
+  constexpr int STAGES = KSPLIT >= 8 ? 3 : 2;
+  if (a.K % 128 == 0)
+    hipLaunchKernelGGL((mx_stream_kernel<FP8, SWIGLU, KSPLIT, FM, STAGES>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((mx_direct_kernel<FP8, SWIGLU, KSPLIT, FM>), grid, block, 0, stream, a);
+}
+
+template <bool FP8, bool SWIGLU, int FM>
+static void launch_stream_split(const MxGemmArgs &a, hipStream_t stream) {
+  const long long tiles = mx_tiles(a, 16 * FM);
+  const long long frags = tiles * (a.N / 16);
+  const int cus = device_cu_count();
+  if constexpr (FM == 1)
+    if (frags <= 2ll * cus && a.K >= 2048) return launch_stream<FP8, SWIGLU, 8, FM>(a, stream);
+  if (frags <= 4ll * cus && a.K >= 1024) launch_stream<FP8, SWIGLU, 4, FM>(a, stream);
+  else if (frags <= 8ll * cus && a.K >= 512) launch_stream<FP8, SWIGLU, 2, FM>(a, stream);
+  else launch_stream<FP8, SWIGLU, 1, FM>(a, stream);
+}
+
 template <bool FP8, bool SWIGLU>
 static moesq_status_t launch_mx(const MxGemmArgs &a, hipStream_t stream) {
   const int cols = SWIGLU ? a.N / 2 : a.N;
-  if (!a.far && a.K % 128 == 0 && (long long)a.M >= 32ll * a.E) {
+  if (a.K % 128 == 0 && (long long)a.M >= 32ll * a.E) {
     constexpr int WN = FP8 ? 4 : 2, FN = FP8 ? 2 : 4, FM = 2;
     constexpr int BM = 8 / WN * FM * 32, BC = WN * FN * 32 / (SWIGLU ? 2 : 1);
-    const long long tt = (long long)a.M / BM + std::min(a.E, a.M);
+    const long long tt = mx_tiles(a, BM);
     hipLaunchKernelGGL((mx_tiled_kernel<FP8, SWIGLU, WN, FN, FM>), dim3((unsigned)(tt * ((cols + BC - 1) / BC))),
                        dim3(MXT_THREADS), 0, stream, a);
-    return launch_status("moesq_mx_gemm");
+  } else if ((long long)a.M <= 16ll * a.E) {
+    launch_stream_split<FP8, SWIGLU, 1>(a, stream);
+  } else {
+    launch_stream_split<FP8, SWIGLU, 2>(a, stream);
   }
-  const long long tiles = (long long)a.M / 16 + std::min(a.E, a.M);
-  const dim3 grid((unsigned)tiles, (unsigned)((cols / 16 + MXG_WAVES - 1) / MXG_WAVES));
-  hipLaunchKernelGGL((mx_gemm_kernel<FP8, SWIGLU>), grid, dim3(MXG_WAVES * 64), 0, stream, a);
   return launch_status("moesq_mx_gemm");
 }
 
@@ -468,18 +770,18 @@ extern "C" moesq_status_t moesq_mx_gemm(const moesq_mx_t *x, const int32_t *perm
     return fail(MOESQ_ERR_NULL, who + ": expert_offsets may be NULL only with E == 1");
   if (x->rows != (perm ? T : M))
     return fail(MOESQ_ERR_SHAPE, who + ": activation rows must be T with a gather permutation, else M");
+  const bool f8 = x->format == MOESQ_ROWS_MXFP8;
+  const long long xb = (long long)x->rows * (x->K / (f8 ? 1 : 2));
+  if (xb >= (1ll << 32) || (long long)N * (w->K / 2) >= (1ll << 32))
+    return fail(MOESQ_ERR_SHAPE, who + ": the activations' codes and one expert's must stay under 4 GiB");
   if (M == 0) return MOESQ_OK;
   if (!x->codes || !x->scales || !w->codes || !w->scales || !y)
     return fail(MOESQ_ERR_NULL, who + ": NULL codes, scales or output rows");
   if (((uintptr_t)x->codes | (uintptr_t)w->codes | (uintptr_t)y) & 15)
     return fail(MOESQ_ERR_ARG, who + ": codes and y must be 16-byte aligned");
   MxGemmArgs a{x->codes, x->scales, w->codes, w->scales, perm, expert_offsets, y,
-               k,        M,         E,        N,         w->K, flat, false, 0, 0};
-  const bool f8 = x->format == MOESQ_ROWS_MXFP8;
-  const long long xb = (long long)x->rows * (x->K / (f8 ? 1 : 2));
-  a.far = xb >= (1ll << 32) || (long long)N * (w->K / 2) >= (1ll << 32);
-  a.x_bytes = (uint32_t)xb;
-  a.xs_bytes = (uint32_t)((long long)x->rows * (x->K / 32));
+               k,        M,         E,        N,         w->K, flat, (uint32_t)xb,
+               (uint32_t)((long long)x->rows * (x->K / 32))};
   if (epilogue == MOESQ_EPI_SWIGLU)
     return f8 ? launch_mx<true, true>(a, stream) : launch_mx<false, true>(a, stream);
   return f8 ? launch_mx<true, false>(a, stream) : launch_mx<false, false>(a, stream);

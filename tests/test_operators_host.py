@@ -198,6 +198,8 @@ def test_mx_gemm_rejects(m):
     assert call(perm=0x10, T=4, k=0) == m.ERR_SHAPE
     assert call(perm=0x10, T=2, k=2) == m.ERR_SHAPE               # x has M rows, not T
     assert call(perm=0x10, T=4, off=None, E=1) == m.ERR_NULL
+    assert call(w=dict(rows=8 << 16, K=1 << 17), x=dict(K=1 << 17)) == m.ERR_SHAPE    # an expert of 4 GiB
+    assert call(x=dict(rows=1 << 20, K=4096), w=dict(K=4096), M=1 << 20) == m.ERR_SHAPE
     assert call(off=None) == m.ERR_NULL                           # several experts without offsets
     assert call(y=None) == m.ERR_NULL and call(x=dict(scales=None)) == m.ERR_NULL
     assert call(w=dict(codes=0x1008)) == m.ERR_ARG and call(y=0x18) == m.ERR_ARG
