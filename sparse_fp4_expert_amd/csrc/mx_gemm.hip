@@ -155,7 +155,7 @@ __device__ __forceinline__ void wait_copies() {   // all but the last N have lan
 // fragments.
 template <bool SWIGLU, int KSPLIT, int FM>
 __device__ __forceinline__ void mx_stream_finish(const MxGemmArgs &a, const MxTile &t, f32x4_t (&acc)[FM], void *lds,
-                                                 int c0, int cols, bool live, int wave, int lane) {
+                                                 int c0, int cols, int wave, int lane) {
   const int q = lane >> 4, rl = lane & 15, kw = wave % KSPLIT;
   f32x4_t *part = static_cast<f32x4_t *>(lds);     // [waves][FM][64]
   if constexpr (KSPLIT > 1) {
@@ -163,7 +163,6 @@ __device__ __forceinline__ void mx_stream_finish(const MxGemmArgs &a, const MxTi
 #pragma unroll
     for (int g = 0; g < FM; ++g) part[(wave * FM + g) * 64 + lane] = acc[g];
     __syncthreads();
-    if (kw >= FM) return;
   }
 #pragma unroll
   for (int g = 0; g < FM; ++g) {
@@ -182,7 +181,7 @@ __device__ __forceinline__ void mx_stream_finish(const MxGemmArgs &a, const MxTi
       for (int i = 0; i < 4; ++i) v[i] = silu_f32(v[i]) * up[i];
     }
     const int r = 16 * g + rl;
-    if (!live || r >= t.rows || (SWIGLU && q >= 2)) continue;
+    if (c0 >= cols || r >= t.rows || (SWIGLU && q >= 2)) continue;
     const int dst = mx_dst(a, t.row0 + r);
     if (dst < 0) continue;
     const bool ok = mx_src(a, t.row0 + r) >= 0;
@@ -200,12 +199,12 @@ __device__ __forceinline__ int piece8(int r, int c) { return c ^ (r & 15); }
 
 // ------------------------------------------------------------------ streaming kernel (K % 128 == 0)
 //
-// Few rows: bound by the stream of weights.  A wave contracts 16 weight rows
-// with FM fragments of 16 tokens in stages of 256 positions, copied to a ring
-// of its own in LDS: an MFMA operand takes 16 bytes of each of 16 rows, which
+// Few rows: bound by the stream of weights.  A wave contracts FN fragments of
+// 16 weight rows with FM of 16 tokens in stages of 256 positions, copied to a
+// ring of its own in LDS: an MFMA operand takes 16 bytes of each of 16 rows, which
 // as a direct load is 64 separate pieces for the address unit (a quarter of
 // its rate), while a copy takes whole lines.  No wave waits for another but
-// for the final sum: KSPLIT waves of a workgroup share 16 rows, each with its
+// for the final sum: KSPLIT waves of a workgroup share their rows, each with its
 // own stages, and add their sums in LDS in a fixed order.
 //
 // SwiGLU: rows 0-7 of a fragment are gate rows, 8-15 the up rows of the same
@@ -213,109 +212,132 @@ __device__ __forceinline__ int piece8(int r, int c) { return c ^ (r & 15); }
 
 constexpr int mxs_waves(int ksplit) { return ksplit < 4 ? 4 : ksplit; }
 
-template <bool FP8, int FM>
+template <bool FP8, int FN, int FM>
 struct MxRing {
-  uint8_t w[16 * 128];
+  uint8_t w[FN * 16 * 128];
   uint8_t x[FM * 16 * (FP8 ? 256 : 128)];
-  uint8_t ws[256];                                 // 16 rows x 8, twice
-  uint8_t xs[FM > 1 ? FM * 128 : 256];
+  uint8_t ws[256];                                 // rows x 8, 16 rows twice
+  uint8_t xs[256];
 };
 
-template <bool FP8, bool SWIGLU, int KSPLIT, int FM, int STAGES>
+template <bool FP8, bool SWIGLU, int KSPLIT, int FN, int FM>
 __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGemmArgs a) {
   constexpr int WAVES = mxs_waves(KSPLIT);
-  constexpr int RG = WAVES / KSPLIT;               // fragments of 16 weight rows a workgroup
+  constexpr int RG = WAVES / KSPLIT;               // row groups of FN fragments a workgroup
   constexpr int FC = SWIGLU ? 8 : 16;              // output columns a fragment
+  static_assert(FN <= 2 && FM <= 2, "one scale copy each");
   constexpr int XB = FP8 ? 256 : 128;              // bytes of a token's stage
-  constexpr int CX = FM * 16 * XB / 1024;          // copies of token codes
-  constexpr int COPIES = 2 + CX + 2;               // of a stage
-  using Ring = MxRing<FP8, FM>;
-  __shared__ __attribute__((aligned(1024))) Ring ring[WAVES][STAGES];
+  constexpr int CW = FN * 2 + 1;                       // copies of a stage's weights and their scales
+  constexpr int CX = FM * 16 * XB / 1024 + 1;      // copies of its tokens and theirs
+  using Ring = MxRing<FP8, FN, FM>;
+  __shared__ __attribute__((aligned(1024))) Ring ring[WAVES][2];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, rl = lane & 15;
   const int cols = SWIGLU ? a.N / 2 : a.N;
-  const int groups = (cols / FC + RG - 1) / RG;
+  const int groups = (cols / FC + RG * FN - 1) / (RG * FN);
   const MxTile t = mx_find_tile<16 * FM>(a, blockIdx.x / groups, lane);
   if (t.e < 0) return;
   const int kw = wave % KSPLIT;
-  const int c0 = ((blockIdx.x % groups) * RG + wave / KSPLIT) * FC;
-  const bool live = c0 < cols;                     // (columns come in whole fragments)
+  const int c0 = ((blockIdx.x % groups) * RG + wave / KSPLIT) * FN * FC;
   const int K = a.K, nb = K / 32;
+  // this wave's stages: kw, kw + KSPLIT, ...
+  const int n = ((K + 255) / 256 - kw + KSPLIT - 1) / KSPLIT;
+  const uint32_t lds0 = lds_offset(&ring[wave][0]);
 
-  // rows that are not there read row 0; their results are not used
-  auto w_row = [&](int r) {
-    return (uint32_t)(!live ? 0 : SWIGLU ? c0 + (r & 7) + (r >> 3) * cols : c0 + r);
-  };
-  auto x_row = [&](int r) { return (uint32_t)(r < t.rows ? max(mx_src(a, t.row0 + r), 0) : 0); };
+  // (rows that are not there read row 0, and their results are not used;
+  // positions behind K in the last stage, other rows' or the buffers' zeros,
+  // are not contracted)
   const i32x4_t wbuf = raw_buffer(a.wc + (size_t)t.e * a.N * (K / 2), (uint32_t)a.N * (uint32_t)(K / 2));
   const i32x4_t wsbuf = raw_buffer(a.ws + (size_t)t.e * a.N * nb, (uint32_t)a.N * (uint32_t)nb);
-  const i32x4_t xbuf = raw_buffer(a.xc, a.x_bytes), xsbuf = raw_buffer(a.xs, a.xs_bytes);
-  uint32_t wo[2], xo[CX];
+  auto w_row = [&](int r) {
+    // (columns come in whole fragments)
+    const int c = c0 + (r >> 4) * FC + (SWIGLU ? r & 7 : r & 15);
+    return (uint32_t)(c >= cols ? 0 : SWIGLU ? c + ((r >> 3) & 1) * cols : c);
+  };
+  uint32_t wo[CW - 1];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < CW - 1; ++i) {
     const int r = i * 8 + (lane >> 3);
     wo[i] = w_row(r) * (uint32_t)(K / 2) + 16 * piece4(r, lane & 7);
   }
-  const uint32_t wso = w_row((lane >> 1) & 15) * (uint32_t)nb + 4 * (lane & 1);
+  const uint32_t wso = w_row((lane >> 1) & (16 * FN - 1)) * (uint32_t)nb + 4 * (lane & 1);
+  auto fetch_w = [&](int slot, int c) {
+    const uint32_t base = lds0 + slot * (uint32_t)sizeof(Ring);
 #pragma unroll
-  for (int i = 0; i < CX; ++i) {
+    for (int i = 0; i < CW - 1; ++i) copy16_to_lds(base + i * 1024, wbuf, wo[i], (uint32_t)c * 128);
+    copy4_to_lds(base + offsetof(Ring, ws), wsbuf, wso, (uint32_t)c * 8);
+  };
+  // the first weights are under way before the tokens' rows are looked up
+  if (n > 0) fetch_w(0, kw);
+  if (n > 1) fetch_w(1, kw + KSPLIT);
+
+  const i32x4_t xbuf = raw_buffer(a.xc, a.x_bytes), xsbuf = raw_buffer(a.xs, a.xs_bytes);
+  auto x_row = [&](int r) { return (uint32_t)(r < t.rows ? max(mx_src(a, t.row0 + r), 0) : 0); };
+  uint32_t xo[CX - 1];
+#pragma unroll
+  for (int i = 0; i < CX - 1; ++i) {
     const int r = i * (1024 / XB) + lane / (XB / 16);
     xo[i] = x_row(r) * (uint32_t)(K / (FP8 ? 1 : 2)) + 16 * (FP8 ? piece8(r, lane & 15) : piece4(r, lane & 7));
   }
   const uint32_t xso = x_row((lane >> 1) & (16 * FM - 1)) * (uint32_t)nb + 4 * (lane & 1);
-  const uint32_t lds0 = lds_offset(&ring[wave][0]);
-  // (positions behind K in the last stage, other rows' or the buffers'
-  // zeros, are not contracted)
-  auto fetch = [&](int slot, int c) {
-    const uint32_t base = lds0 + slot * (uint32_t)sizeof(Ring), ks = (uint32_t)c;
+  auto fetch_x = [&](int slot, int c) {
+    const uint32_t base = lds0 + slot * (uint32_t)sizeof(Ring);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) copy16_to_lds(base + i * 1024, wbuf, wo[i], ks * 128);
-    copy4_to_lds(base + offsetof(Ring, ws), wsbuf, wso, ks * 8);
-#pragma unroll
-    for (int i = 0; i < CX; ++i) copy16_to_lds(base + offsetof(Ring, x) + i * 1024, xbuf, xo[i], ks * XB);
-    copy4_to_lds(base + offsetof(Ring, xs), xsbuf, xso, ks * 8);
+    for (int i = 0; i < CX - 1; ++i)
+      copy16_to_lds(base + offsetof(Ring, x) + i * 1024, xbuf, xo[i], (uint32_t)c * XB);
+    copy4_to_lds(base + offsetof(Ring, xs), xsbuf, xso, (uint32_t)c * 8);
   };
-  f32x4_t acc[FM];
+  if (n > 0) fetch_x(0, kw);
+  if (n > 1) fetch_x(1, kw + KSPLIT);
+
+  f32x4_t acc[FN][FM];
 #pragma unroll
-  for (int g = 0; g < FM; ++g) acc[g] = f32x4_t{0, 0, 0, 0};
+  for (int f = 0; f < FN; ++f)
+#pragma unroll
+    for (int g = 0; g < FM; ++g) acc[f][g] = f32x4_t{0, 0, 0, 0};
   auto step = [&](const Ring &k, int s) {          // 128 positions
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint32_t sw = *reinterpret_cast<const uint32_t *>(k.ws + rl * 8 + 4 * s) >> (8 * q);
-    const i32x8_t W = as_operand(*reinterpret_cast<const uint4 *>(k.w + rl * 128 + 16 * piece4(rl, 4 * s + q)), zero);
+    i32x8_t X[FM];
+    uint32_t sx[FM];
 #pragma unroll
     for (int g = 0; g < FM; ++g) {
       const int r = 16 * g + rl;
-      const uint32_t sx = *reinterpret_cast<const uint32_t *>(k.xs + r * 8 + 4 * s) >> (8 * q);
-      i32x8_t X;
+      sx[g] = *reinterpret_cast<const uint32_t *>(k.xs + r * 8 + 4 * s) >> (8 * q);
       if constexpr (FP8)
-        X = as_operand(*reinterpret_cast<const uint4 *>(k.x + r * 256 + 16 * piece8(r, 8 * s + q)),
-                       *reinterpret_cast<const uint4 *>(k.x + r * 256 + 16 * piece8(r, 8 * s + 4 + q)));
+        X[g] = as_operand(*reinterpret_cast<const uint4 *>(k.x + r * 256 + 16 * piece8(r, 8 * s + q)),
+                          *reinterpret_cast<const uint4 *>(k.x + r * 256 + 16 * piece8(r, 8 * s + 4 + q)));
       else
-        X = as_operand(*reinterpret_cast<const uint4 *>(k.x + r * 128 + 16 * piece4(r, 4 * s + q)), zero);
-      acc[g] = mfma_mx<FP8, 0>(W, X, acc[g], sw, sx);
+        X[g] = as_operand(*reinterpret_cast<const uint4 *>(k.x + r * 128 + 16 * piece4(r, 4 * s + q)), zero);
+    }
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+      const int r = 16 * f + rl;
+      const uint32_t sw = *reinterpret_cast<const uint32_t *>(k.ws + r * 8 + 4 * s) >> (8 * q);
+      const i32x8_t W = as_operand(*reinterpret_cast<const uint4 *>(k.w + r * 128 + 16 * piece4(r, 4 * s + q)), zero);
+#pragma unroll
+      for (int g = 0; g < FM; ++g) acc[f][g] = mfma_mx<FP8, 0>(W, X[g], acc[f][g], sw, sx[g]);
     }
   };
-  // this wave's stages: kw, kw + KSPLIT, ...
-  const int n = ((K + 255) / 256 - kw + KSPLIT - 1) / KSPLIT;
-#pragma unroll
-  for (int i = 0; i < STAGES; ++i)
-    if (i < n) fetch(i, kw + i * KSPLIT);
-  int slot = 0;
   for (int i = 0; i < n; ++i) {
-    const int behind = n - 1 - i;                  // stages in flight behind this one
-    if (behind >= STAGES - 1) wait_copies<(STAGES - 1) * COPIES>();
-    else if (STAGES > 3 && behind == 2) wait_copies<2 * COPIES>();
-    else if (STAGES > 2 && behind == 1) wait_copies<COPIES>();
-    else wait_copies<0>();
+    // copies in flight behind this stage's: the tokens of stage 1 (at first),
+    // a whole stage, or none
+    if (i + 1 == n) wait_copies<0>();
+    else if (i == 0) wait_copies<CX>();
+    else wait_copies<CW + CX>();
     const int c = kw + i * KSPLIT;
-    step(ring[wave][slot], 0);
-    if (K - 256 * c > 128) step(ring[wave][slot], 1);
+    const Ring &k = ring[wave][i & 1];
+    step(k, 0);
+    if (K - 256 * c > 128) step(k, 1);
     // the slot's reads are done before it is written again
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (i + STAGES < n) fetch(slot, c + STAGES * KSPLIT);
-    slot = slot + 1 == STAGES ? 0 : slot + 1;
+    if (i + 2 < n) {
+      fetch_w(i & 1, c + 2 * KSPLIT);
+      fetch_x(i & 1, c + 2 * KSPLIT);
+    }
   }
-  mx_stream_finish<SWIGLU, KSPLIT, FM>(a, t, acc, &ring[0][0], c0, cols, live, wave, lane);
+#pragma unroll
+  for (int f = 0; f < FN; ++f)
+    mx_stream_finish<SWIGLU, KSPLIT, FM>(a, t, acc[f], &ring[0][0], c0 + f * FC, cols, wave, lane);
 }
 
 // ------------------------------------------------------------------ direct kernel (any K)
@@ -466,7 +488,7 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_direct_kernel(MxGem
     if (c2 < chunks) load_chunk(A, p, c2, q, nb - 8 * c2);
     contract_chunk(acc, B);
   }
-  mx_stream_finish<SWIGLU, KSPLIT, FM>(a, t, acc, part, c0, cols, live, wave, lane);
+  mx_stream_finish<SWIGLU, KSPLIT, FM>(a, t, acc, part, c0, cols, wave, lane);
 }
 
 // ------------------------------------------------------------------ LDS-tiled kernel
@@ -692,28 +714,39 @@ static long long mx_tiles(const MxGemmArgs &a, int bm) {
   return ((long long)a.M + (long long)std::min(a.E, a.M) * (bm - 1)) / bm;
 }
 
-template <bool FP8, bool SWIGLU, int KSPLIT, int FM>
+template <bool FP8, bool SWIGLU, int KSPLIT, int FN, int FM>
 static void launch_stream(const MxGemmArgs &a, hipStream_t stream) {
-  const int frags = a.N / 16, rg = mxs_waves(KSPLIT) / KSPLIT;
-  const long long tiles = mx_tiles(a, 16 * FM);
-  const dim3 grid((unsigned)(tiles * ((frags + rg - 1) / rg))), block(mxs_waves(KSPLIT) * 64);
-  constexpr int STAGES = KSPLIT >= 8 ? 3 : 2;
-  if (a.K % 128 == 0)
-    hipLaunchKernelGGL((mx_stream_kernel<FP8, SWIGLU, KSPLIT, FM, STAGES>), grid, block, 0, stream, a);
+  const int frags = a.N / 16;
+  const bool copies = a.K % 128 == 0;
+  const int rg = mxs_waves(KSPLIT) / KSPLIT * (copies ? FN : 1);
+  const dim3 grid((unsigned)(mx_tiles(a, 16 * FM) * ((frags + rg - 1) / rg))), block(mxs_waves(KSPLIT) * 64);
+  if (copies)
+    hipLaunchKernelGGL((mx_stream_kernel<FP8, SWIGLU, KSPLIT, FN, FM>), grid, block, 0, stream, a);
   else
     hipLaunchKernelGGL((mx_direct_kernel<FP8, SWIGLU, KSPLIT, FM>), grid, block, 0, stream, a);
 }
 
+// How the weight rows (`frags` fragments of 16, counting every token tile
+// there may be) are spread.  Each wave's ring keeps 4 KB (FN = 1) or 8 KB of
+// weights in flight, so the stream needs some 2000 waves: few fragments are
+// split over K, many take two fragments a wave, which halves the copies of
+// tokens.  Measured, us for KSPLIT / FN:
+//   256 fragments (16 x 4096 x 7168 FP8)    8/1 7.3  4/2 8.6  2/2 14.3  1/2 24.3
+//   1024 (16 x 16384 x 4096 FP8)            8/1 16.8 4/2 11.2 2/2 11.8  1/2 16.3
+//   1536 of up to 4096 (48 experts FP8)     8/1 42.1 4/2 21.1 2/2 20.1  1/2 19.7
+//   6912 of up to 12288 (128 experts FP8)   8/1 152  4/2 56.5 2/2 40.6  1/2 32.8
+//   4064 of up to 12288 (384 experts, K 7168 FP4)    4/2 57.4 2/2 47.0  1/2 59.3
 template <bool FP8, bool SWIGLU, int FM>
 static void launch_stream_split(const MxGemmArgs &a, hipStream_t stream) {
-  const long long tiles = mx_tiles(a, 16 * FM);
-  const long long frags = tiles * (a.N / 16);
+  const long long frags = mx_tiles(a, 16 * FM) * (a.N / 16);
   const int cus = device_cu_count();
-  if constexpr (FM == 1)
-    if (frags <= 2ll * cus && a.K >= 2048) return launch_stream<FP8, SWIGLU, 8, FM>(a, stream);
-  if (frags <= 4ll * cus && a.K >= 1024) launch_stream<FP8, SWIGLU, 4, FM>(a, stream);
-  else if (frags <= 8ll * cus && a.K >= 512) launch_stream<FP8, SWIGLU, 2, FM>(a, stream);
-  else launch_stream<FP8, SWIGLU, 1, FM>(a, stream);
+  if (frags <= cus && a.K >= 2048) {
+    if constexpr (FM == 1) return launch_stream<FP8, SWIGLU, 8, 1, FM>(a, stream);
+    return launch_stream<FP8, SWIGLU, 4, 1, FM>(a, stream);
+  }
+  if (frags <= 4ll * cus && a.K >= 1024) launch_stream<FP8, SWIGLU, 4, 2, FM>(a, stream);
+  else if ((frags <= 16ll * cus && a.K >= 512) || a.K >= 4096) launch_stream<FP8, SWIGLU, 2, 2, FM>(a, stream);
+  else launch_stream<FP8, SWIGLU, 1, 2, FM>(a, stream);
 }
 
 template <bool FP8, bool SWIGLU>
