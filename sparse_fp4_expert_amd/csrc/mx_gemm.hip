@@ -30,6 +30,7 @@ struct MxGemmArgs {
   uint16_t *y;
   int k, M, E, N, K;
   int flat;
+  bool wide_scales;            // every row's scales on 16-byte boundaries
   uint32_t x_bytes, xs_bytes;  // of all activation rows
 };
 
@@ -90,6 +91,19 @@ __device__ __forceinline__ MxTile mx_find_tile(const MxGemmArgs &a, int t, int l
   return MxTile{-1, 0, 0};
 }
 
+// All token tiles of up to BM rows; as mx_find_tile.
+template <int BM>
+__device__ __forceinline__ int mx_count_tiles(const MxGemmArgs &a, int lane) {
+  if (!a.offsets) return (a.M + BM - 1) / BM;
+  int mine = 0;
+#pragma unroll FIND_BATCH
+  for (int e = lane; e < a.E; e += 64) {
+    const int2 r = mx_rows_of(a, e);
+    mine += r.y > r.x ? (r.y - r.x + BM - 1) / BM : 0;
+  }
+  return __shfl(wave_incl_scan(mine, lane), 63, 64);
+}
+
 // Source row of routed row r; -1: a zero row.
 __device__ __forceinline__ int mx_src(const MxGemmArgs &a, int r) {
   if (!a.perm) return r;
@@ -136,12 +150,12 @@ __device__ __forceinline__ uint32_t lds_offset(const void *p) {
 // 16 (or 4) bytes a lane from a buffer to LDS at lds + 16 (4) * lane.
 __device__ __forceinline__ void copy16_to_lds(uint32_t lds, i32x4_t buf, uint32_t voff, uint32_t soff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
-               "s"(buf), "s"(soff)
+               "s"(buf), "s"(__builtin_amdgcn_readfirstlane((int)soff))
                : "memory");
 }
 __device__ __forceinline__ void copy4_to_lds(uint32_t lds, i32x4_t buf, uint32_t voff, uint32_t soff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
-               "s"(buf), "s"(soff)
+               "s"(buf), "s"(__builtin_amdgcn_readfirstlane((int)soff))
                : "memory");
 }
 
@@ -491,20 +505,18 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_direct_kernel(MxGem
   mx_stream_finish<SWIGLU, KSPLIT, FM>(a, t, acc, part, c0, cols, wave, lane);
 }
 
-// ------------------------------------------------------------------ LDS-tiled kernel
+// ------------------------------------------------------------------ tiled kernel (K % 128 == 0)
 //
 // A workgroup of 8 waves computes BN weight rows x BM tokens.  Stages of 256
-// positions of both operands go from global memory to LDS without passing
-// through registers, two stages in turn: while one is contracted the next is
-// in flight.  (The copies are written as asm without register results, so
-// the compiler's wait counts know nothing of them; the only waits for them
-// are the one asm statement and the barrier at the head of each stage, and
-// the reads of LDS stay ordinary loads that the compiler schedules.)
-//
-// LDS rows are as in memory, 16-byte chunks of a row permuted by its row
-// number so that the 16 rows that read one chunk position together touch all
-// 64 banks once: chunk c of row r sits at c ^ ((r >> 1) & 7) in the 128-byte
-// rows of E2M1 codes and at c ^ (r & 15) in the 256-byte rows of E4M3 ones.
+// positions of both operands are copied to LDS, two in turn, and contracted
+// in four MFMA steps.  A copy takes whole 128-byte lines (64-byte pieces of
+// twice the rows measured 547 ns for 32 KB a CU instead of 329), and a
+// wave's copies are spread between its MFMAs: a run of them would block the
+// wave until the address unit has taken them.  The operands of a step are
+// read from LDS while the step before it is on the matrix units.  The one
+// barrier of a stage is in the middle of its last step, behind the stage's
+// reads: it hands the stage's buffer to the copies of the stage after the
+// next and says that the next has landed.
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
@@ -519,41 +531,49 @@ __device__ __forceinline__ f32x16_t mfma_mx32(i32x8_t w, i32x8_t x, f32x16_t c, 
 }
 
 constexpr int MXT_WAVES = 8, MXT_THREADS = MXT_WAVES * 64;
-constexpr int MXT_KS = 256;                       // positions a stage
 
 template <bool FP8, int BN, int BM>
-struct MxStage {
-  uint8_t w[BN * 128];
-  uint8_t x[BM * (FP8 ? 256 : 128)];
-  uint8_t ws[BN * 8];
-  uint8_t xs[BM * 8];
+struct MxTileLds {
+  struct {
+    uint8_t w[BN * 128];
+    uint8_t x[BM * (FP8 ? 256 : 128)];
+  } stage[2];
+  uint8_t scales[2][(BN + BM) * 16];               // of 512 positions (two stages)
+  uint8_t unused[(BN + BM) * 16];
 };
 
 // WN waves over the weight rows (FN fragments of 32 each), 8 / WN over the
 // tokens (FM fragments of 32 each).
-template <bool FP8, bool SWIGLU, int WN, int FN, int FM>
+template <bool FP8, bool SWIGLU, bool WIDE, int WN, int FN, int FM>
 __global__ __launch_bounds__(MXT_THREADS, 2) void mx_tiled_kernel(MxGemmArgs a) {
   constexpr int WM = MXT_WAVES / WN;
   constexpr int BN = WN * FN * 32, BM = WM * FM * 32;
-  using Stage = MxStage<FP8, BN, BM>;
-  __shared__ __attribute__((aligned(1024))) Stage lds[2];
+  using Lds = MxTileLds<FP8, BN, BM>;
+  __shared__ __attribute__((aligned(1024))) Lds lds;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cols = SWIGLU ? a.N / 2 : a.N;
   constexpr int BC = SWIGLU ? BN / 2 : BN;         // output columns of a tile
   const int nt = (cols + BC - 1) / BC;
-  const int tile = blockIdx.x / nt, c0 = (blockIdx.x % nt) * BC;
+  // The workgroups of one XCD (every eighth) take a run of tiles, token tiles
+  // in fours and those before weight tiles, so the 32 that run at a time
+  // share 4 x 8 panels in its L2.
+  const int mt = mx_count_tiles<BM>(a, lane), items = mt * nt, run = (items + 7) >> 3;
+  const int item = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= run || item >= items) return;
+  const int first = item / (4 * nt) * 4, in = item - first * nt, four = min(4, mt - first);
+  const int tile = first + in % four, c0 = in / four * BC;
   const MxTile t = mx_find_tile<BM>(a, tile, lane);
   if (t.e < 0) return;
-  const int K = a.K, nb = K / 32;
+  const int K = a.K, nb = K / 32, stages = (K + 255) / 256;
 
   // Weight row of row r of the tile.  SwiGLU: the first half of a wave's
   // rows are gate rows, the second half the up rows of the same columns.
   auto w_row = [&](int r) {
     int n;
     if constexpr (SWIGLU) {
-      constexpr int H = FN * 16;                  // columns of a wave
+      constexpr int H = FN * 16;                   // columns of a wave
       const int in = r % (2 * H), c = c0 + (r / (2 * H)) * H + in % H;
       n = min(c, cols - 1) + (in >= H ? cols : 0);
     } else {
@@ -561,61 +581,94 @@ __global__ __launch_bounds__(MXT_THREADS, 2) void mx_tiled_kernel(MxGemmArgs a) 
     }
     return (uint32_t)n;
   };
-  auto x_row = [&](int r) {
-    const int s = r < t.rows ? mx_src(a, t.row0 + r) : -1;
-    return (uint32_t)max(s, 0);
-  };
+  // (rows that are not there read row 0, and their results are not used)
+  auto x_row = [&](int r) { return (uint32_t)(r < t.rows ? max(mx_src(a, t.row0 + r), 0) : 0); };
   const i32x4_t wbuf = raw_buffer(a.wc + (size_t)t.e * a.N * (K / 2), (uint32_t)a.N * (uint32_t)(K / 2));
   const i32x4_t wsbuf = raw_buffer(a.ws + (size_t)t.e * a.N * nb, (uint32_t)a.N * (uint32_t)nb);
   const i32x4_t xbuf = raw_buffer(a.xc, a.x_bytes);
   const i32x4_t xsbuf = raw_buffer(a.xs, a.xs_bytes);
 
-  // This lane's source offsets of its copies: CW + CX of 16 bytes, a wave
-  // 1 KB each, and SW + SX of 4 bytes (scales).
-  constexpr int XB = FP8 ? 256 : 128, XK = FP8 ? 1 : 2;
-  constexpr int CW = BN * 128 / 1024 / MXT_WAVES, CX = BM * XB / 1024 / MXT_WAVES;
-  constexpr int SD = (BN + BM) * 2;                // scale dwords a stage
-  constexpr int SC = (SD + MXT_THREADS - 1) / MXT_THREADS;
-  static_assert(CW >= 1 && CX >= 1, "every wave copies");
-  uint32_t wo[CW], xo[CX], so[SC];
+  // This lane's source offsets of its copies: CW + CX of 1 KB a wave, and the
+  // scales, 16 bytes a row for two stages.  (What a copy reads behind K, other
+  // rows' bytes or the buffer's zeros, is not contracted.)
+  constexpr int XB = FP8 ? 256 : 128;
+  constexpr int CW = BN * 128 / 1024 / MXT_WAVES, CX = BM * XB / 1024 / MXT_WAVES, COPIES = CW + CX;
+  constexpr int SG = (BN + BM) / 64;               // groups of 64 rows with scales
+  static_assert(CW >= 1 && CX >= 1 && SG <= MXT_WAVES && BN % 64 == 0 && BM % 64 == 0, "whole copies");
+  uint32_t off[COPIES];
 #pragma unroll
   for (int i = 0; i < CW; ++i) {
-    const int r = (i * MXT_WAVES + wave) * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
-    wo[i] = w_row(r) * (uint32_t)(K / 2) + 16 * c;
+    const int r = (i * MXT_WAVES + wave) * 8 + (lane >> 3);
+    off[i] = w_row(r) * (uint32_t)(K / 2) + 16 * piece4(r, lane & 7);
   }
 #pragma unroll
   for (int i = 0; i < CX; ++i) {
     const int r = (i * MXT_WAVES + wave) * (1024 / XB) + lane / (XB / 16);
-    const int c = FP8 ? (lane & 15) ^ (r & 15) : (lane & 7) ^ ((r >> 1) & 7);
-    xo[i] = x_row(r) * (uint32_t)(K / XK) + 16 * c;
+    off[CW + i] = x_row(r) * (uint32_t)(K / (FP8 ? 1 : 2)) + 16 * (FP8 ? piece8(r, lane & 15) : piece4(r, lane & 7));
   }
-  // scale dword d of a stage: row d / 2 of the weights, then of the tokens
+  // Copy i of stage s.  Stages that are not there are copied from buffers of
+  // no bytes (zeros, into a buffer that nobody reads again), so that no
+  // branch comes between the MFMAs.
+  auto copy = [&](int i, int s) {
+    const auto &st = lds.stage[s & 1];
+    i32x4_t buf = i < CW ? wbuf : xbuf;
+    buf[2] = s < stages ? buf[2] : 0;
+    if (i < CW)
+      copy16_to_lds(lds_offset(st.w) + (i * MXT_WAVES + wave) * 1024, buf, off[i], (uint32_t)s * 128);
+    else
+      copy16_to_lds(lds_offset(st.x) + ((i - CW) * MXT_WAVES + wave) * 1024, buf, off[i], (uint32_t)s * XB);
+  };
+  // Scales of stages 2j and 2j + 1, a wave those of 64 rows (waves beyond the
+  // rows copy some again): rows on 16-byte boundaries (WIDE) in one copy,
+  // others in four of 4 bytes.  Not wanted: of no bytes, to a place of no use.
+  const int sr0 = wave % SG * 64;
+  const uint32_t soff = (sr0 < BN ? w_row(sr0 + lane) : x_row(sr0 + lane - BN)) * (uint32_t)nb;
+  uint32_t soff4[WIDE ? 1 : 4];
+  if constexpr (!WIDE) {
 #pragma unroll
-  for (int i = 0; i < SC; ++i) {
-    const int d = (i * MXT_WAVES + wave) * 64 + lane, r = d >> 1;
-    so[i] = (r < BN ? w_row(r) : x_row(min(r - BN, BM - 1))) * (uint32_t)nb + 4 * (d & 1);
+    for (int i = 0; i < 4; ++i)                    // rows 16 i.. of the wave's, four dwords each
+      soff4[i] = (uint32_t)__shfl((int)soff, 16 * i + (lane >> 2), 64) + 4 * (lane & 3);
   }
-  const int stages = (K + MXT_KS - 1) / MXT_KS;
-  auto fetch = [&](int s) {
-    // (positions behind K in the last stage, other rows' or the buffers'
-    // zeros, are not contracted)
-    const uint32_t base = lds_offset(&lds[s & 1]), ks = (uint32_t)s;
+  auto copy_scales = [&](int j, bool wanted) {
+    i32x4_t buf = sr0 < BN ? wsbuf : xsbuf;
+    buf[2] = wanted ? buf[2] : 0;
+    const uint32_t dst = wanted ? lds_offset(lds.scales[j & 1]) + sr0 * 16 : lds_offset(lds.unused) + sr0 * 16;
+    if constexpr (WIDE) {
+      copy16_to_lds(dst, buf, soff, (uint32_t)j * 16);
+    } else {
 #pragma unroll
-    for (int i = 0; i < CW; ++i)
-      copy16_to_lds(base + (i * MXT_WAVES + wave) * 1024, wbuf, wo[i], ks * 128);
-#pragma unroll
-    for (int i = 0; i < CX; ++i)
-      copy16_to_lds(base + BN * 128 + (i * MXT_WAVES + wave) * 1024, xbuf, xo[i], ks * XB);
-#pragma unroll
-    for (int i = 0; i < SC; ++i) {
-      const int first = (i * MXT_WAVES + wave) * 64;      // wave-uniform
-      if (first >= SD) break;
-      copy4_to_lds(base + BN * 128 + BM * XB + first * 4, first < BN * 2 ? wsbuf : xsbuf, so[i], ks * 8);
+      for (int i = 0; i < 4; ++i) copy4_to_lds(dst + i * 256, buf, soff4[i], (uint32_t)j * 16);
     }
   };
 
   const int h = lane >> 5, rl = lane & 31;
   const int wr0 = (wave % WN) * FN * 32 + rl, xr0 = (wave / WN) * FM * 32 + rl;
+  constexpr int XP = FP8 ? 2 : 1, READS = FN + FM * XP, MFMAS = FN * FM;
+  struct Step {
+    uint4 v[READS];                                // FN weight fragments, FM * XP token pieces
+  };
+  auto read = [&](Step &o, int i, int s, int k) {  // operand i of step k (64 positions) of stage s
+    const auto &st = lds.stage[s & 1];
+    if (i < FN) {
+      const int r = wr0 + 32 * i;
+      o.v[i] = *reinterpret_cast<const uint4 *>(st.w + r * 128 + 16 * piece4(r, 2 * k + h));
+    } else {
+      const int r = xr0 + 32 * ((i - FN) / XP);
+      if constexpr (FP8)
+        o.v[i] = *reinterpret_cast<const uint4 *>(st.x + r * 256 + 16 * piece8(r, 4 * k + 2 * ((i - FN) % XP) + h));
+      else
+        o.v[i] = *reinterpret_cast<const uint4 *>(st.x + r * 128 + 16 * piece4(r, 2 * k + h));
+    }
+  };
+  // scales of a stage: eight blocks a row, lane half h starting at block h
+  uint2 sw[FN], sx[FM];
+  auto read_scales = [&](int s) {
+    const uint8_t *sc = lds.scales[(s >> 1) & 1] + 8 * (s & 1);
+#pragma unroll
+    for (int f = 0; f < FN; ++f) sw[f] = *reinterpret_cast<const uint2 *>(sc + (wr0 + 32 * f) * 16);
+#pragma unroll
+    for (int g = 0; g < FM; ++g) sx[g] = *reinterpret_cast<const uint2 *>(sc + (BN + xr0 + 32 * g) * 16);
+  };
   f32x16_t acc[FN][FM];
 #pragma unroll
   for (int f = 0; f < FN; ++f)
@@ -623,59 +676,77 @@ __global__ __launch_bounds__(MXT_THREADS, 2) void mx_tiled_kernel(MxGemmArgs a) 
     for (int g = 0; g < FM; ++g)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[f][g][i] = 0.0f;
-
-  // one half stage: 128 positions, two MFMA steps of 64
-  auto contract = [&](const Stage &st, int half) {
-    // scales of the half's four blocks; lane half h starts at block h
-    uint32_t sw[FN], sx[FM];
-#pragma unroll
-    for (int f = 0; f < FN; ++f)
-      sw[f] = *reinterpret_cast<const uint32_t *>(st.ws + (wr0 + 32 * f) * 8 + 4 * half) >> (8 * h);
-#pragma unroll
-    for (int g = 0; g < FM; ++g)
-      sx[g] = *reinterpret_cast<const uint32_t *>(st.xs + (xr0 + 32 * g) * 8 + 4 * half) >> (8 * h);
-    auto step = [&](auto sel) {
-      constexpr int S = decltype(sel)::value;       // 0 or 2
-      const int c = 4 * half + S + h;               // 32-position chunk of E2M1 rows
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      i32x8_t W[FN], X[FM];
-#pragma unroll
-      for (int f = 0; f < FN; ++f) {
-        const int r = wr0 + 32 * f;
-        W[f] = as_operand(*reinterpret_cast<const uint4 *>(st.w + r * 128 + 16 * (c ^ ((r >> 1) & 7))), zero);
-      }
-#pragma unroll
-      for (int g = 0; g < FM; ++g) {
-        const int r = xr0 + 32 * g;
-        if constexpr (FP8) {
-          const int c8 = 8 * half + 2 * S + h;      // 16-position chunk of E4M3 rows
-          const uint8_t *row = st.x + r * 256;
-          X[g] = as_operand(*reinterpret_cast<const uint4 *>(row + 16 * (c8 ^ (r & 15))),
-                            *reinterpret_cast<const uint4 *>(row + 16 * ((c8 + 2) ^ (r & 15))));
-        } else {
-          X[g] = as_operand(*reinterpret_cast<const uint4 *>(st.x + r * 128 + 16 * (c ^ ((r >> 1) & 7))), zero);
-        }
-      }
-#pragma unroll
-      for (int f = 0; f < FN; ++f)
-#pragma unroll
-        for (int g = 0; g < FM; ++g) acc[f][g] = mfma_mx32<FP8, S>(W[f], X[g], acc[f][g], sw[f], sx[g]);
-    };
-    step(std::integral_constant<int, 0>{});
-    step(std::integral_constant<int, 2>{});
+  // MFMA i of step k
+  auto mfma = [&](const Step &o, int i, auto k) {
+    constexpr int S = 2 * (decltype(k)::value & 1);
+    const int f = i / FM, g = i % FM;
+    const uint32_t w = (decltype(k)::value < 2 ? sw[f].x : sw[f].y) >> (8 * h);
+    const uint32_t x = (decltype(k)::value < 2 ? sx[g].x : sx[g].y) >> (8 * h);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    acc[f][g] = mfma_mx32<FP8, S>(as_operand(o.v[f], zero),
+                                  as_operand(o.v[FN + g * XP], FP8 ? o.v[FN + g * XP + XP - 1] : zero), acc[f][g], w, x);
   };
-
-  fetch(0);
-  for (int s = 0; s < stages; ++s) {
-    // this wave's copies of stage s have landed; behind the barrier all have,
-    // and every wave is done with the other buffer
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  // MFMAs [M0, M1) of step `k`, between them the reads of the operands of
+  // step NK of stage `ns` (NK < 0: none) and copies [C0, C1) of stage `cs`.
+  auto step = [&](const Step &cur, auto k, Step &nxt, auto nk, int ns, auto c0, auto c1, int cs, auto m0, auto m1) {
+    constexpr int M0 = decltype(m0)::value, M1 = decltype(m1)::value, N = M1 - M0;
+    constexpr int C0 = decltype(c0)::value, C1 = decltype(c1)::value, NK = decltype(nk)::value;
+#pragma unroll
+    for (int i = M0; i < M1; ++i) {
+      mfma(cur, i, k);
+      if constexpr (NK >= 0)
+#pragma unroll
+        for (int r = READS * (i - M0) / N; r < READS * (i - M0 + 1) / N; ++r) read(nxt, r, ns, NK);
+#pragma unroll
+      for (int c = C0 + (C1 - C0) * (i - M0) / N; c < C0 + (C1 - C0) * (i - M0 + 1) / N; ++c) copy(c, cs);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  constexpr int HALF = COPIES / 2;                 // copies issued in the first of the two stages that share them
+  constexpr std::integral_constant<int, -1> none{};
+  constexpr std::integral_constant<int, 0> k0{};
+  constexpr std::integral_constant<int, 1> k1{};
+  constexpr std::integral_constant<int, 2> k2{};
+  constexpr std::integral_constant<int, 3> k3{};
+  constexpr std::integral_constant<int, HALF> half{};
+  constexpr std::integral_constant<int, COPIES> copies{};
+  constexpr std::integral_constant<int, MFMAS / 2> mid{};
+  constexpr std::integral_constant<int, MFMAS> end{};
+  // this wave's copies have landed and its reads are done; then every wave's
+  auto arrive = [&] {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (s + 1 < stages) fetch(s + 1);
-    contract(lds[s & 1], 0);
-    if (K - s * MXT_KS > 128) contract(lds[s & 1], 1);
+  };
+
+  copy_scales(0, true);
+#pragma unroll
+  for (int i = 0; i < COPIES; ++i) copy(i, 0);
+  arrive();
+#pragma unroll
+  for (int i = 0; i < HALF; ++i) copy(i, 1);
+  Step A, B;
+#pragma unroll
+  for (int i = 0; i < READS; ++i) read(A, i, 0, 0);
+  read_scales(0);
+  const int full = K / 256;
+  for (int s = 0; s < full; ++s) {
+    step(A, k0, B, k1, s, half, copies, s + 1, k0, end);
+    step(B, k1, A, k2, s, k0, k0, 0, k0, end);
+    step(A, k2, B, k3, s, k0, k0, 0, k0, end);
+    step(B, k3, A, none, 0, k0, k0, 0, k0, mid);
+    arrive();
+    // the buffer of the scales of stages s - 2 and s - 1
+    copy_scales((s >> 1) + 1, (s & 1) == 0 && s + 2 < stages);
+    // (behind the last stage, operands and scales are read for nothing)
+    step(B, k3, A, k0, s + 1, k0, half, s + 2, mid, end);
+    read_scales(s + 1);
   }
+  if (full < stages) {                             // the last 128 positions
+    step(A, k0, B, k1, full, k0, k0, 0, k0, end);
+    step(B, k1, A, none, 0, k0, k0, 0, k0, end);
+  }
+  wait_copies<0>();
 
   // results: four neighbouring features of one token a register group
   constexpr int OF = SWIGLU ? FN / 2 : FN;
@@ -756,8 +827,11 @@ static moesq_status_t launch_mx(const MxGemmArgs &a, hipStream_t stream) {
     constexpr int WN = FP8 ? 4 : 2, FN = FP8 ? 2 : 4, FM = 2;
     constexpr int BM = 8 / WN * FM * 32, BC = WN * FN * 32 / (SWIGLU ? 2 : 1);
     const long long tt = mx_tiles(a, BM);
-    hipLaunchKernelGGL((mx_tiled_kernel<FP8, SWIGLU, WN, FN, FM>), dim3((unsigned)(tt * ((cols + BC - 1) / BC))),
-                       dim3(MXT_THREADS), 0, stream, a);
+    const dim3 grid((unsigned)((tt * ((cols + BC - 1) / BC) + 7) & ~7ll));
+    if (a.wide_scales)
+      hipLaunchKernelGGL((mx_tiled_kernel<FP8, SWIGLU, true, WN, FN, FM>), grid, dim3(MXT_THREADS), 0, stream, a);
+    else
+      hipLaunchKernelGGL((mx_tiled_kernel<FP8, SWIGLU, false, WN, FN, FM>), grid, dim3(MXT_THREADS), 0, stream, a);
   } else if ((long long)a.M <= 16ll * a.E) {
     launch_stream_split<FP8, SWIGLU, 1>(a, stream);
   } else {
@@ -813,7 +887,8 @@ extern "C" moesq_status_t moesq_mx_gemm(const moesq_mx_t *x, const int32_t *perm
   if (((uintptr_t)x->codes | (uintptr_t)w->codes | (uintptr_t)y) & 15)
     return fail(MOESQ_ERR_ARG, who + ": codes and y must be 16-byte aligned");
   MxGemmArgs a{x->codes, x->scales, w->codes, w->scales, perm, expert_offsets, y,
-               k,        M,         E,        N,         w->K, flat, (uint32_t)xb,
+               k,        M,         E,        N,         w->K, flat,
+               w->K % 512 == 0 && !(((uintptr_t)x->scales | (uintptr_t)w->scales) & 15), (uint32_t)xb,
                (uint32_t)((long long)x->rows * (x->K / 32))};
   if (epilogue == MOESQ_EPI_SWIGLU)
     return f8 ? launch_mx<true, true>(a, stream) : launch_mx<false, true>(a, stream);
