@@ -3,10 +3,13 @@
 //   p = softmax(l) or sigmoid(l),  key = l or p + bias,  groups of experts
 //   kept by their best keys,  the k largest keys,  w = p [/ sum] * scale
 //
-// One wave per row; lane i holds the experts i, i + 64, ...  Keys are 64-bit
-// values: a bias brings scores of different experts arbitrarily near one
-// another, and an id that turns on an fp32 rounding would depend on how the
-// sums were ordered.
+// Keys are 64-bit values by definition: a bias brings scores of different
+// experts arbitrarily near one another, and an id that turns on an fp32
+// rounding would depend on how the sums were ordered.  They are computed in
+// fp32 with a bound on their error, and only a row with two keys nearer than
+// that where it matters is done again in 64 bits (about one row in a
+// thousand of random scores; without a bias the keys are the scores
+// themselves, and none).
 #include <cmath>
 
 #include "common.hpp"
@@ -32,10 +35,290 @@ __device__ __forceinline__ float gate_clean(float l) {
   return l != l ? -INFINITY : fminf(l, GATE_BIG);
 }
 
+template <bool BF16>
+__device__ __forceinline__ float gate_logit(const GateArgs &a, int row, int e) {
+  const size_t at = (size_t)row * a.E + e;
+  return gate_clean(BF16 ? __uint_as_float((uint32_t)((const uint16_t *)a.logits)[at] << 16)
+                         : ((const float *)a.logits)[at]);
+}
+
+// ---- reductions over the wave by lane permutations of the vector units
+// (a few cycles a step; shuffles through LDS take over a hundred)
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float(dpp<CTRL, ROWS>(__float_as_uint(v)));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double v) {
+  return __hiloint2double((int)dpp<CTRL, ROWS>((uint32_t)__double2hiint(v)),
+                          (int)dpp<CTRL, ROWS>((uint32_t)__double2loint(v)));
+}
+__device__ __forceinline__ uint32_t lane63(uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 63); }
+__device__ __forceinline__ float lane63(float v) { return __uint_as_float(lane63(__float_as_uint(v))); }
+__device__ __forceinline__ double lane63(double v) {
+  return __hiloint2double((int)lane63((uint32_t)__double2hiint(v)), (int)lane63((uint32_t)__double2loint(v)));
+}
+__device__ __forceinline__ float lane_of(float v, int l) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+__device__ __forceinline__ double lane_of(double v, int l) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), l),
+                          __builtin_amdgcn_readlane(__double2loint(v), l));
+}
+// op over the 64 lanes, the same value in all of them.  A step's lanes
+// outside its rows see their own value again; lane 63 sees every lane's once
+// in each step, so sums are right there (rows first: rotations by 8, 4, 2
+// and 1 double the lanes seen).
+template <typename T, typename Op>
+__device__ __forceinline__ T wave_reduce(T v, Op op) {
+  v = op(v, dpp<0x128, 0xf>(v));                   // row_ror:8 of 16 lanes
+  v = op(v, dpp<0x124, 0xf>(v));
+  v = op(v, dpp<0x122, 0xf>(v));
+  v = op(v, dpp<0x121, 0xf>(v));
+  const T up = dpp<0x142, 0xa>(v);                 // lane 15 of a row to the next row
+  v = (threadIdx.x & 16) ? op(v, up) : v;
+  const T half = dpp<0x143, 0xc>(v);               // lane 31 to the upper half
+  v = (threadIdx.x & 32) ? op(v, half) : v;
+  return lane63(v);
+}
+__device__ __forceinline__ double max_f64(double a, double b) {
+  double r;   // (no NaN comes here; fmax() would quiet its operands first)
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ float wave_max(float v) {
+  return wave_reduce(v, [](float x, float y) { return fmaxf(x, y); });
+}
+__device__ __forceinline__ double wave_max(double v) {
+  return wave_reduce(v, [](double x, double y) { return max_f64(x, y); });
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  return wave_reduce(v, [](double x, double y) { return x + y; });
+}
+__device__ __forceinline__ uint32_t wave_min(uint32_t v) {
+  return wave_reduce(v, [](uint32_t x, uint32_t y) { return min(x, y); });
+}
+template <int N>
+__device__ __forceinline__ double max_of(const double (&d)[N]) {
+  double m[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) m[i] = d[i];
+#pragma unroll
+  for (int w = 1; w < N; w *= 2)
+#pragma unroll
+    for (int i = 0; i + w < N; i += 2 * w) m[i] = max_f64(m[i], m[i + w]);
+  return m[0];
+}
+
+// An order-preserving integer of an fp32 key; 0 is below every one.
+__device__ __forceinline__ uint32_t gate_order(float key) {
+  const uint32_t b = __float_as_uint(key);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float gate_key(uint32_t u) {
+  return __uint_as_float(u ^ ((uint32_t)((int32_t)~u >> 31) | 0x80000000u));
+}
+
+// Largest of 64 integers: each step one instruction.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  auto step = [](uint32_t x, int o) { return max(x, (uint32_t)o); };
+  v = step(v, __builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, true));
+  v = step(v, __builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, true));
+  v = step(v, __builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, true));
+  v = step(v, __builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, true));
+  v = step(v, __builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false));
+  v = step(v, __builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false));
+  return lane63(v);
+}
+
+// How far a biased fp32 key may be from its 64-bit value: sigmoid(l) and
+// exp(l - top) / sum are computed with an argument off by at most 2^-23 of
+// itself, and |x| e^x <= 0.37 and |x| sigmoid'(x) <= 0.28, so that costs at
+// most 2^-24 of 1; the hardware's exp2 and reciprocal, the sum (in 64 bits)
+// and the addition of the bias a few 2^-24 of the score or key.  2^-21 +
+// |key| 2^-22 is more than twice all of it.  Keys nearer to one another than
+// the sum of their bounds are decided in 64 bits.
+__device__ __forceinline__ float gate_bound(float key) { return 0x1p-21f + fabsf(key) * 0x1p-22f; }
+__device__ __forceinline__ float gate_bound(double) { return 0.0f; }
+
+// The groups that stay, as a bit each at group * lanes, for keys (or, with
+// TOP2 and no bias, scores) `sk` of the row's E experts in LDS; `lanes` lanes
+// share a group.  `sure` becomes false when the border of the selection lies
+// within the keys' bounds.
+template <typename F>
+__device__ __forceinline__ uint64_t gate_groups(const GateArgs &a, const F *sk, int lane, int lanes, bool bounded,
+                                                bool &sure) {
+  const int G = a.g.n_group, per = a.E / G, g = lane / lanes;
+  const bool top2 = a.g.group_score == MOESQ_GROUP_TOP2;
+  F m1 = -INFINITY, m2 = -INFINITY;
+  if (g < G) {
+#pragma unroll 4
+    for (int i = lane % lanes; i < per; i += lanes) {
+      const F v = sk[g * per + i];
+      const F lo = m1 < v ? m1 : v;
+      m2 = lo > m2 ? lo : m2;
+      m1 = v > m1 ? v : m1;
+    }
+  }
+  auto merge = [&](F o1, F o2) {                   // two largest of two lanes' two largest
+    const F lo = m1 < o1 ? m1 : o1, hi2 = m2 > o2 ? m2 : o2;
+    m1 = m1 > o1 ? m1 : o1;
+    m2 = lo > hi2 ? lo : hi2;
+  };
+  // neighbours, pairs, then (lanes already alike) mirrored halves of 8 and 16
+  if (lanes > 1) merge(dpp<0xb1, 0xf>(m1), dpp<0xb1, 0xf>(m2));
+  if (lanes > 2) merge(dpp<0x4e, 0xf>(m1), dpp<0x4e, 0xf>(m2));
+  if (lanes > 4) merge(dpp<0x141, 0xf>(m1), dpp<0x141, 0xf>(m2));
+  if (lanes > 8) merge(dpp<0x140, 0xf>(m1), dpp<0x140, 0xf>(m2));
+  if (lanes > 16) merge(__shfl_xor(m1, 16, 64), __shfl_xor(m2, 16, 64));
+  const bool two = top2 && m2 != (F)-INFINITY;
+  const F gs = two ? m1 + m2 : m1;
+  int ahead = 0;
+  float near = INFINITY;                           // distance of the nearest other group's score
+  for (int o = 0; o < G; ++o) {
+    const F v = lane_of(gs, o * lanes);
+    ahead += v > gs || (v == gs && o < g);
+    if (o != g && (v != (F)-INFINITY || gs != (F)-INFINITY)) near = fminf(near, fabsf((float)(v - gs)));
+  }
+  if (bounded) {
+    float bound = g >= G || gs == (F)-INFINITY
+                      ? 0.0f
+                      : gate_bound(m1) + (two ? gate_bound(m2) : 0.0f) + gate_bound(gs);
+    bound = wave_max(bound);
+    const bool border = g < G && ahead >= a.g.topk_group - 1 && ahead <= a.g.topk_group;
+    if (a.g.topk_group < G && __ballot(border && near <= 2.0f * bound)) sure = false;
+  }
+  return __ballot(g < G && ahead < a.g.topk_group);
+}
+
+// The selection of one row by a wave: lane i holds the experts i, i + 64, ...,
+// their cleaned scores in l; `my_id` of lane j receives the j-th expert, or
+// -1.  F = float: false when the keys are too near to one another to decide
+// in fp32.  F = double: 64-bit keys, always true.
+template <typename F, int EPL>
+__device__ __forceinline__ bool gate_select(const GateArgs &a, const float (&l)[EPL], float top, F *sk, int lane,
+                                            int &my_id) {
+  constexpr bool EXACT = sizeof(F) == 8;
+  const int E = a.E, k = a.g.k, G = a.g.n_group;
+  const bool biased = a.bias != nullptr, top2 = G > 1 && a.g.group_score == MOESQ_GROUP_TOP2;
+  F key[EPL], p[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) key[i] = (F)l[i];
+  if (biased || top2) {
+    if (a.g.score == MOESQ_SCORE_SIGMOID) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if constexpr (EXACT)
+          p[i] = 1.0 / (1.0 + exp(-(double)l[i]));
+        else
+          p[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));
+      }
+    } else {
+      double sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if (l[i] == -INFINITY) p[i] = 0;
+        else if constexpr (EXACT) p[i] = exp((double)l[i] - (double)top);
+        else p[i] = __expf(l[i] - top);
+        sum += (double)p[i];
+      }
+      sum = wave_sum(sum);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if constexpr (EXACT)
+          p[i] = p[i] / (sum > 0.0 ? sum : 1.0);
+        else
+          p[i] *= __builtin_amdgcn_rcpf((float)sum);
+      }
+    }
+    if (biased) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = i * 64 + lane;
+        const float b = e < E ? gate_clean(a.bias[e]) : -INFINITY;
+        key[i] = l[i] == -INFINITY || b == -INFINITY ? (F)-INFINITY : p[i] + (F)b;
+      }
+    }
+  }
+  bool sure = true;
+  if (G > 1) {
+    const int per = E / G;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = i * 64 + lane;
+      if (e < E) sk[e] = top2 && !biased && l[i] != -INFINITY ? p[i] : key[i];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int lanes = 64 >> (G > 1 ? 32 - __builtin_clz(G - 1) : 0);
+    const uint64_t kept = gate_groups<F>(a, sk, lane, lanes, !EXACT && (biased || top2), sure);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = i * 64 + lane;
+      if (e < E && !((kept >> (e / per * lanes)) & 1)) key[i] = -INFINITY;
+    }
+  }
+  my_id = -1;
+  if constexpr (EXACT) {
+    for (int r = 0; r < k; ++r) {
+      const double best = wave_max(max_of(key));
+      if (best == -INFINITY) break;
+      uint32_t e = 1u << 20;
+#pragma unroll
+      for (int i = EPL - 1; i >= 0; --i) e = key[i] == best ? (uint32_t)(i * 64 + lane) : e;
+      e = wave_min(e);
+      if (lane == r) my_id = (int)e;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) key[i] = (uint32_t)(i * 64 + lane) == e ? -INFINITY : key[i];
+    }
+  } else {
+    uint32_t u[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) u[i] = key[i] == -INFINITY ? 0u : gate_order(key[i]);
+    // lane r's key and the one behind it; with a bias one round more, for the
+    // first that is left
+    uint32_t mine = 0, left = 0;
+    const int rounds = biased ? min(k + 1, E) : k;
+    for (int r = 0; r < rounds; ++r) {
+      uint32_t best = u[0];
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) best = max(best, u[i]);
+      best = wave_max_u32(best);
+      if (best == 0) break;
+      // the lowest expert that holds it, found and cleared by lane masks
+      int e = -1;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const uint64_t at = e < 0 ? __ballot(u[i] == best) : 0;
+        const uint64_t first = at & (0 - at);
+        if (at) e = i * 64 + __builtin_ctzll(at);
+        u[i] = (first >> lane) & 1 ? 0u : u[i];
+      }
+      if (r == k) {
+        left = best;
+        break;
+      }
+      my_id = lane == r ? e : my_id;
+      mine = lane == r ? best : mine;
+    }
+    if (biased) {
+      const uint32_t next = (uint32_t)__shfl_down((int)mine, 1, 64), behind = lane == k - 1 ? left : next;
+      const float x = gate_key(mine), y = gate_key(behind);
+      if (__ballot(mine != 0 && behind != 0 && x - y <= gate_bound(x) + gate_bound(y))) sure = false;
+    }
+  }
+  return sure;
+}
+
 template <int EPL, bool BF16>
 __global__ __launch_bounds__(GATE_THREADS) void gate_kernel(GateArgs a) {
-  __shared__ double s_key[GATE_WAVES][MOESQ_MAX_EXPERTS];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  extern __shared__ __attribute__((aligned(16))) double s_key[];     // [waves][E] with groups
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = blockIdx.x * GATE_WAVES + wave;
   if (row >= a.T) return;   // the whole wave leaves together
   const int E = a.E, k = a.g.k;
@@ -52,107 +335,37 @@ __global__ __launch_bounds__(GATE_THREADS) void gate_kernel(GateArgs a) {
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = i * 64 + lane;
-    l[i] = -INFINITY;
-    if (e < E) {
-      const size_t at = (size_t)row * E + e;
-      const float v = BF16 ? __uint_as_float((uint32_t)((const uint16_t *)a.logits)[at] << 16)
-                           : ((const float *)a.logits)[at];
-      l[i] = gate_clean(v);
-    }
+    l[i] = e < E ? gate_logit<BF16>(a, row, e) : -INFINITY;
     top = fmaxf(top, l[i]);
   }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
   const bool sigmoid = a.g.score == MOESQ_SCORE_SIGMOID;
-  double sum = 1.0;
-  auto score = [&](float v) {
-    if (v == -INFINITY) return 0.0;
-    return sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)top) / sum;
-  };
-  if (!sigmoid) {
-    double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (l[i] != -INFINITY) s += exp((double)l[i] - (double)top);
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) s += __shfl_xor(s, d, 64);
-    sum = s;   // 0 only when every expert is masked
-  }
-  const bool top2 = a.g.n_group > 1 && a.g.group_score == MOESQ_GROUP_TOP2;
-  double key[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = i * 64 + lane;
-    key[i] = -INFINITY;
-    if (e >= E || l[i] == -INFINITY) continue;
-    if (a.bias) {
-      const float b = gate_clean(a.bias[e]);
-      if (b != -INFINITY) key[i] = score(l[i]) + (double)b;
-    } else {
-      key[i] = (double)l[i];
-    }
-  }
-  if (a.g.n_group > 1) {
-    const int per = E / a.g.n_group;
-    double *sk = s_key[wave];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = i * 64 + lane;
-      if (e < E)
-        sk[e] = top2 && !a.bias && key[i] != -INFINITY ? score(l[i]) : key[i];
-    }
+  if (!sigmoid) top = wave_max(top);
+  double *sk = s_key + wave * E;
+  int my_id;
+  if (!gate_select<float, EPL>(a, l, top, reinterpret_cast<float *>(sk), lane, my_id)) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    __threadfence_block();
-    double gs = -INFINITY;   // this lane's group
-    if (lane < a.g.n_group) {
-      double m1 = -INFINITY, m2 = -INFINITY;
-      for (int j = 0; j < per; ++j) {
-        const double v = sk[lane * per + j];
-        if (v > m1) { m2 = m1; m1 = v; } else if (v > m2) { m2 = v; }
-      }
-      gs = top2 && m2 != -INFINITY ? m1 + m2 : m1;
-    }
-    int ahead = 0;
-    for (int o = 0; o < a.g.n_group; ++o) {
-      const double v = __shfl(gs, o, 64);
-      ahead += v > gs || (v == gs && o < lane);
-    }
-    const uint64_t kept = __ballot(lane < a.g.n_group && ahead < a.g.topk_group);
+    gate_select<double, EPL>(a, l, top, sk, lane, my_id);
+  }
+  // weights in 64 bits
+  const float mine = my_id >= 0 ? gate_logit<BF16>(a, row, my_id) : -INFINITY;
+  double w = 0.0;
+  if (sigmoid) {
+    if (my_id >= 0) w = 1.0 / (1.0 + exp(-(double)mine));
+  } else {
+    if (my_id >= 0) w = exp((double)mine - (double)top);
+    if (!a.g.renormalize) {
+      double s = 0.0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = i * 64 + lane;
-      if (e < E && !((kept >> (e / per)) & 1)) key[i] = -INFINITY;
+      for (int i = 0; i < EPL; ++i)
+        if (l[i] != -INFINITY) s += exp((double)l[i] - (double)top);
+      s = wave_sum(s);
+      w /= s > 0.0 ? s : 1.0;
     }
   }
-  int my_id = -1;
-  float my_l = -INFINITY;
-  for (int j = 0; j < k; ++j) {
-    double best = -INFINITY;
-    int at = -1;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (key[i] > best) { best = key[i]; at = i * 64 + lane; }
-    int id = best == -INFINITY ? 1 << 30 : at;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-      const double v = __shfl_xor(best, d, 64);
-      const int o = __shfl_xor(id, d, 64);
-      if (v > best || (v == best && o < id)) { best = v; id = o; }
-    }
-    if (id == 1 << 30) break;
-    float lv = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (i * 64 + lane == id) { key[i] = -INFINITY; lv = l[i]; }
-    lv = __shfl(lv, id & 63, 64);
-    if (lane == j) { my_id = id; my_l = lv; }
-  }
-  double w = score(my_l);
   if (a.g.renormalize) {
-    double t = w;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) t += __shfl_xor(t, d, 64);
-    w = t > 0.0 ? w / t : 0.0;
+    const double s = wave_sum(w);
+    w = s > 0.0 ? w / s : 0.0;
   }
   if (lane < k) {
     a.ids[out] = my_id;
@@ -163,11 +376,14 @@ __global__ __launch_bounds__(GATE_THREADS) void gate_kernel(GateArgs a) {
 template <bool BF16>
 static void launch_gate(const GateArgs &a, hipStream_t stream) {
   const dim3 grid((unsigned)((a.T + GATE_WAVES - 1) / GATE_WAVES)), block(GATE_THREADS);
+  const size_t lds = a.g.n_group > 1 ? (size_t)GATE_WAVES * a.E * sizeof(double) : 0;
   const int epl = (a.E + 63) / 64;
-  if (epl <= 2) hipLaunchKernelGGL((gate_kernel<2, BF16>), grid, block, 0, stream, a);
-  else if (epl <= 4) hipLaunchKernelGGL((gate_kernel<4, BF16>), grid, block, 0, stream, a);
-  else if (epl <= 8) hipLaunchKernelGGL((gate_kernel<8, BF16>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((gate_kernel<16, BF16>), grid, block, 0, stream, a);
+  if (epl <= 1) hipLaunchKernelGGL((gate_kernel<1, BF16>), grid, block, lds, stream, a);
+  else if (epl <= 2) hipLaunchKernelGGL((gate_kernel<2, BF16>), grid, block, lds, stream, a);
+  else if (epl <= 4) hipLaunchKernelGGL((gate_kernel<4, BF16>), grid, block, lds, stream, a);
+  else if (epl <= 6) hipLaunchKernelGGL((gate_kernel<6, BF16>), grid, block, lds, stream, a);
+  else if (epl <= 8) hipLaunchKernelGGL((gate_kernel<8, BF16>), grid, block, lds, stream, a);
+  else hipLaunchKernelGGL((gate_kernel<16, BF16>), grid, block, lds, stream, a);
 }
 
 }  // namespace moesq
