@@ -12,8 +12,8 @@ importing this module without it raises ImportError.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -252,6 +252,7 @@ class Gate:
         self.k = int(k)
         self.desc = GateDesc(self.k, score, n_group, topk_group, group_score, int(bool(renormalize)),
                              scale)
+        self.ref = ctypes.byref(self.desc)
 
 
 class Mx:
@@ -262,17 +263,27 @@ class Mx:
     def __init__(self, codes, scales, format: int):
         if format not in (ROWS_MXFP4, ROWS_MXFP8):
             raise ValueError("format must be ROWS_MXFP4 or ROWS_MXFP8")
-        self.shape = tuple(codes.shape[:-1])
-        self.K = int(codes.shape[-1]) * (2 if format == ROWS_MXFP4 else 1)
-        if tuple(scales.shape) != self.shape + (self.K // 32,) or self.K % 32:
-            raise ValueError(f"scales has shape {tuple(scales.shape)}, expected "
-                             f"{self.shape + (self.K // 32,)} (K = {self.K}, a multiple of 32)")
-        self.rows = 1
-        for n in self.shape:
-            self.rows *= int(n)
-        self.codes, self.scales, self.format = codes, scales, format
-        self.desc = MxDesc(_ptr(codes, torch.uint8, "codes", True),
-                           _ptr(scales, torch.uint8, "scales", True), self.rows, self.K, format)
+        shape = tuple(codes.shape[:-1])
+        K = int(codes.shape[-1]) * (2 if format == ROWS_MXFP4 else 1)
+        if K % 32 or tuple(scales.shape) != shape + (K // 32,):
+            raise ValueError(f"scales has shape {tuple(scales.shape)}, expected {shape + (K // 32,)} "
+                             f"(K = {K}, a multiple of 32)")
+        self._set(codes, scales, format, shape, K)
+
+    def _set(self, codes, scales, format, shape, K):
+        self.codes, self.scales, self.format, self.shape, self.K = codes, scales, format, shape, K
+        self.rows = math.prod(shape)
+        self._desc = None
+        return self
+
+    def _described(self):
+        """(descriptor, device), checked and made at the first use."""
+        if self._desc is None:
+            dev, (codes, scales) = _pointers(
+                (self.codes, torch.uint8, self.rows * self.K // (2 if self.format == ROWS_MXFP4 else 1), "codes"),
+                (self.scales, torch.uint8, self.rows * self.K // 32, "scales"))
+            self._desc = ctypes.byref(MxDesc(codes, scales, self.rows, self.K, self.format)), dev
+        return self._desc
 
     @property
     def nbytes(self) -> int:
@@ -281,34 +292,68 @@ class Mx:
     @staticmethod
     def empty(shape, K: int, format: int, device="cuda"):
         """`shape`: the leading dimensions, (rows,) or (E, N)."""
-        u8 = dict(dtype=torch.uint8, device=device)
-        return Mx(torch.empty(*shape, K // 2 if format == ROWS_MXFP4 else K, **u8),
-                  torch.empty(*shape, K // 32, **u8), format)
+        shape = tuple(shape)
+        codes = torch.empty(shape + (K // 2 if format == ROWS_MXFP4 else K,), dtype=torch.uint8, device=device)
+        scales = torch.empty(shape + (K // 32,), dtype=torch.uint8, device=device)
+        return Mx.__new__(Mx)._set(codes, scales, format, shape, K)
 
 
-def _launch(stream, *tensors):
-    """(device context, raw stream) of a call on these tensors: all on one
-    device, which is made current for the launch; without a `stream` that
-    device's current one.  A stream of another device is refused."""
-    dev = None
-    for t in tensors:
-        if t is None or not t.is_cuda:
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _pointers(*specs):
+    """Checks every (tensor, dtype, elements, name): types, sizes and
+    contiguity first, then that all tensors are on one GPU.  Returns its index
+    (None when no tensor has elements) and the pointers.  A None tensor is
+    passed on as NULL (the C call decides whether it may be), and so is an
+    empty one."""
+    dev, ptrs = None, []
+    for t, dtype, n, name in specs:
+        if t is None:
+            ptrs.append(None)
             continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.numel() != n:
+            raise ValueError(f"{name} has {t.numel()} elements ({tuple(t.shape)}), "
+                             f"the shape arguments need {n}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if not n:
+            ptrs.append(None)
+            continue
+        d = t.get_device()
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    if dev is None:
-        return _HERE, _stream(stream)
-    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
-        raise ValueError(f"stream of {stream.device} for tensors on {dev}")
-    here = _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{name} is on another device than the tensors before it")
+        ptrs.append(t.data_ptr())
+    if dev is not None and dev < 0:
+        raise ValueError("the tensors must be on the GPU")
+    return dev, ptrs
+
+
+def _launch(dev, stream, call, *args):
+    """call(*args, raw stream) with GPU `dev` current, and its status checked.
+    Without a `stream` it is that device's current one; a stream of another
+    device is refused."""
+    if dev is None:                       # nothing but empty tensors: nothing will be launched
+        return _check(call(*args, None if stream is None else _stream(stream)))
     if stream is None:
-        return here, torch.cuda.current_stream(dev).cuda_stream
-    return here, _stream(stream)
-
-
-_HERE = contextlib.nullcontext()
+        raw = _raw_stream(dev)
+    else:
+        if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+            raise ValueError(f"stream of {stream.device} for tensors on GPU {dev}")
+        raw = _stream(stream)
+    if dev == _current_device():
+        st = call(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args, raw)
+    if st != OK:
+        _check(st)
 
 
 # ------------------------------------------------------------ C-ABI mirrors
@@ -461,56 +506,55 @@ def _dtype(t, name):
 
 def moesq_gate_topk(logits, T: int, E: int, bias, gate: Gate, n_rows, topk_ids, topk_weights,
                     stream=None):
-    _sizes((logits, T * E, "logits"), (bias, E, "bias"), (n_rows, 1, "n_rows"),
-           (topk_ids, T * gate.k, "topk_ids"), (topk_weights, T * gate.k, "topk_weights"))
-    dtype = _dtype(logits, "logits")
-    args = (_ptr(logits, logits.dtype, "logits"), dtype, T, E, _ptr(bias, torch.float32, "bias", True),
-            ctypes.byref(gate.desc), _ptr(n_rows, torch.int32, "n_rows", True),
-            _ptr(topk_ids, torch.int32, "topk_ids"), _ptr(topk_weights, torch.float32, "topk_weights"))
-    here, st = _launch(stream, logits, bias, n_rows, topk_ids, topk_weights)
-    with here:
-        _check(_gate_topk(*args, st))
+    dtype, n = _dtype(logits, "logits"), T * gate.k
+    f32, i32 = torch.float32, torch.int32
+    dev, (l, b, r, i, w) = _pointers(
+        (logits, logits.dtype, T * E, "logits"), (bias, f32, E, "bias"), (n_rows, i32, 1, "n_rows"),
+        (topk_ids, i32, n, "topk_ids"), (topk_weights, f32, n, "topk_weights"))
+    _launch(dev, stream, _gate_topk, l, dtype, T, E, b, gate.ref, r, i, w)
 
 
-def _rows_buffers(format, rows, K, codes, scales, row_scale=None):
-    """Size checks of quantized-row buffers."""
-    _sizes((codes, rows * K // (1 if format == ROWS_MXFP8 else 2), "codes"),
-           (scales, rows * K // 32, "scales"), (row_scale, rows, "row_scale"))
+def _one_device(dev, *rows):
+    """The descriptors of Mx rows, which have to be on the call's device."""
+    found = []
+    for q in rows:
+        desc, d = q._described()
+        if d is not None and dev is not None and d != dev:
+            raise ValueError("the rows are on another device than the other tensors")
+        found.append(desc)
+    return found
+
+
+def _row_elements(format, rows, K):
+    """Elements of the codes of quantized rows."""
+    return rows * K if format == ROWS_MXFP8 else rows * K // 2
 
 
 def moesq_mx_quantize(x, rows: int, K: int, format: int, codes, scales, stream=None):
-    _sizes((x, rows * K, "x"))
-    _rows_buffers(format, rows, K, codes, scales)
-    dtype = _dtype(x, "x")
-    args = (_ptr(x, x.dtype, "x"), dtype, rows, K, format, _ptr(codes, torch.uint8, "codes"),
-            _ptr(scales, torch.uint8, "scales"))
-    here, st = _launch(stream, x, codes, scales)
-    with here:
-        _check(_mx_quantize(*args, st))
+    dtype, u8 = _dtype(x, "x"), torch.uint8
+    dev, (xp, c, s) = _pointers(
+        (x, x.dtype, rows * K, "x"), (codes, u8, _row_elements(format, rows, K), "codes"),
+        (scales, u8, rows * K // 32, "scales"))
+    _launch(dev, stream, _mx_quantize, xp, dtype, rows, K, format, c, s)
 
 
 def moesq_mx_decode(x: Mx, out, stream=None):
-    _sizes((out, x.rows * x.K, "out"))
-    ptr = _ptr(out, torch.bfloat16, "out")
-    here, st = _launch(stream, x.codes, x.scales, out)
-    with here:
-        _check(_mx_decode(ctypes.byref(x.desc), ptr, st))
+    dev, (o,) = _pointers((out, torch.bfloat16, x.rows * x.K, "out"))
+    desc = _one_device(dev, x)
+    _launch(dev, stream, _mx_decode, desc[0], o)
 
 
 def moesq_rmsnorm(x, residual, weight, T: int, K: int, eps: float, residual_out, y,
                   rows_format: int = ROWS_NONE, codes=None, scales=None, row_scale=None, stream=None):
-    _sizes((x, T * K, "x"), (residual, T * K, "residual"), (weight, K, "weight"),
-           (residual_out, T * K, "residual_out"), (y, T * K, "y"))
-    if rows_format != ROWS_NONE:
-        _rows_buffers(rows_format, T, K, codes, scales, row_scale)
-    bf, u8 = torch.bfloat16, torch.uint8
-    args = (_ptr(x, bf, "x"), _ptr(residual, bf, "residual", True), _ptr(weight, bf, "weight"), T, K, eps,
-            _ptr(residual_out, bf, "residual_out", True), _ptr(y, bf, "y", True), rows_format,
-            _ptr(codes, u8, "codes", True), _ptr(scales, u8, "scales", True),
-            _ptr(row_scale, torch.float32, "row_scale", True))
-    here, st = _launch(stream, x, residual, weight, residual_out, y, codes, scales, row_scale)
-    with here:
-        _check(_rmsnorm(*args, st))
+    bf, u8, n = torch.bfloat16, torch.uint8, T * K
+    if rows_format == ROWS_NONE:
+        codes = scales = row_scale = None
+    dev, (xp, rp, wp, ro, yp, c, s, g) = _pointers(
+        (x, bf, n, "x"), (residual, bf, n, "residual"), (weight, bf, K, "weight"),
+        (residual_out, bf, n, "residual_out"), (y, bf, n, "y"),
+        (codes, u8, _row_elements(rows_format, T, K), "codes"), (scales, u8, n // 32, "scales"),
+        (row_scale, torch.float32, T, "row_scale"))
+    _launch(dev, stream, _rmsnorm, xp, rp, wp, T, K, eps, ro, yp, rows_format, c, s, g)
 
 
 def moesq_mx_gemm(x: Mx, perm, T: int, k: int, expert_offsets, M: int, w: Mx, E: int, epilogue: int,
@@ -518,18 +562,16 @@ def moesq_mx_gemm(x: Mx, perm, T: int, k: int, expert_offsets, M: int, w: Mx, E:
     if E < 1 or w.rows % E:
         raise ValueError(f"weights have {w.rows} rows, not E = {E} matrices")
     N = w.rows // E
-    _sizes((perm, M, "perm"), (expert_offsets, E + 1, "expert_offsets"),
-           (y, M * (N // 2 if (epilogue & ~OUT_FLAT) == EPI_SWIGLU else N), "y"))
     if x.K != w.K:
         raise ValueError(f"activations have K = {x.K}, the weights {w.K}")
     if x.rows != (T if perm is not None else M):
         raise ValueError(f"activations have {x.rows} rows, need {T if perm is not None else M}")
-    args = (ctypes.byref(x.desc), _ptr(perm, torch.int32, "perm", True), T, k,
-            _ptr(expert_offsets, torch.int32, "expert_offsets", True), M, ctypes.byref(w.desc), E,
-            epilogue, _ptr(y, torch.bfloat16, "y"))
-    here, st = _launch(stream, x.codes, x.scales, perm, expert_offsets, w.codes, w.scales, y)
-    with here:
-        _check(_mx_gemm(*args, st))
+    i32 = torch.int32
+    dev, (p, off, yp) = _pointers(
+        (perm, i32, M, "perm"), (expert_offsets, i32, E + 1, "expert_offsets"),
+        (y, torch.bfloat16, M * (N // 2 if (epilogue & ~OUT_FLAT) == EPI_SWIGLU else N), "y"))
+    xd, wd = _one_device(dev, x, w)
+    _launch(dev, stream, _mx_gemm, xd, p, T, k, off, M, wd, E, epilogue, yp)
 
 
 VALIDATE_CHECKS = ("ids", "offsets", "masks", "scales", "global_scales")

@@ -210,9 +210,7 @@ def test_binding_rejects_mismatched_sizes(m):
     z = lambda *s, dt=torch.uint8: torch.zeros(*s, dtype=dt)        # noqa: E731
     f32, bf, i32 = torch.float32, torch.bfloat16, torch.int32
     g = m.Gate(2)
-    import types
-    mx = lambda rows, K, f=1: types.SimpleNamespace(                # noqa: E731
-        rows=rows, K=K, shape=(rows,), codes=z(rows, K // 2), scales=z(rows, K // 32), desc=m.MxDesc())
+    mx = lambda rows, K: m.Mx(z(rows, K // 2), z(rows, K // 32), m.ROWS_MXFP4)      # noqa: E731
     cases = [
         lambda: m.moesq_gate_topk(z(4, 8, dt=f32), 4, 9, None, g, None, z(8, dt=i32), z(8, dt=f32)),
         lambda: m.moesq_gate_topk(z(4, 8, dt=f32), 4, 8, z(7, dt=f32), g, None, z(8, dt=i32), z(8, dt=f32)),
