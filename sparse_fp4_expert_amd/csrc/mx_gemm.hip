@@ -11,6 +11,7 @@
 // operand, tokens the second: a lane's four results are four neighbouring
 // output features of one token.
 #include <stddef.h>
+#include <stdlib.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -507,7 +508,7 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_direct_kernel(MxGem
 
 // ------------------------------------------------------------------ tiled kernel (K % 128 == 0)
 //
-// A workgroup of 8 waves computes BN weight rows x BM tokens.  Stages of 256
+// A workgroup computes BN weight rows x BM tokens.  Stages of 256
 // positions of both operands are copied to LDS, two in turn, and contracted
 // in four MFMA steps.  A copy takes whole 128-byte lines (64-byte pieces of
 // twice the rows measured 547 ns for 32 KB a CU instead of 329), and a
@@ -530,8 +531,6 @@ __device__ __forceinline__ f32x16_t mfma_mx32(i32x8_t w, i32x8_t x, f32x16_t c, 
                                                          (int)sw, SEL, (int)sx);
 }
 
-constexpr int MXT_WAVES = 8, MXT_THREADS = MXT_WAVES * 64;
-
 template <bool FP8, int BN, int BM>
 struct MxTileLds {
   struct {
@@ -542,11 +541,11 @@ struct MxTileLds {
   uint8_t unused[(BN + BM) * 16];
 };
 
-// WN waves over the weight rows (FN fragments of 32 each), 8 / WN over the
-// tokens (FM fragments of 32 each).
-template <bool FP8, bool SWIGLU, bool WIDE, int WN, int FN, int FM>
-__global__ __launch_bounds__(MXT_THREADS, 2) void mx_tiled_kernel(MxGemmArgs a) {
-  constexpr int WM = MXT_WAVES / WN;
+// WN waves over the weight rows (FN fragments of 32 each), WM over the tokens
+// (FM fragments of 32 each).
+template <bool FP8, bool SWIGLU, bool WIDE, int WN, int WM, int FN, int FM>
+__global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled_kernel(MxGemmArgs a) {
+  constexpr int WAVES = WN * WM;
   constexpr int BN = WN * FN * 32, BM = WM * FM * 32;
   using Lds = MxTileLds<FP8, BN, BM>;
   __shared__ __attribute__((aligned(1024))) Lds lds;
@@ -556,92 +555,111 @@ __global__ __launch_bounds__(MXT_THREADS, 2) void mx_tiled_kernel(MxGemmArgs a) 
   const int cols = SWIGLU ? a.N / 2 : a.N;
   constexpr int BC = SWIGLU ? BN / 2 : BN;         // output columns of a tile
   const int nt = (cols + BC - 1) / BC;
-  // The workgroups of one XCD (every eighth) take a run of tiles, token tiles
-  // in fours and those before weight tiles, so the 32 that run at a time
-  // share 4 x 8 panels in its L2.
-  const int mt = mx_count_tiles<BM>(a, lane), items = mt * nt, run = (items + 7) >> 3;
-  const int item = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
-  if ((blockIdx.x >> 3) >= run || item >= items) return;
-  const int first = item / (4 * nt) * 4, in = item - first * nt, four = min(4, mt - first);
-  const int tile = first + in % four, c0 = in / four * BC;
-  const MxTile t = mx_find_tile<BM>(a, tile, lane);
-  if (t.e < 0) return;
   const int K = a.K, nb = K / 32, stages = (K + 255) / 256;
-
-  // Weight row of row r of the tile.  SwiGLU: the first half of a wave's
-  // rows are gate rows, the second half the up rows of the same columns.
-  auto w_row = [&](int r) {
-    int n;
-    if constexpr (SWIGLU) {
-      constexpr int H = FN * 16;                   // columns of a wave
-      const int in = r % (2 * H), c = c0 + (r / (2 * H)) * H + in % H;
-      n = min(c, cols - 1) + (in >= H ? cols : 0);
-    } else {
-      n = min(c0 + r, cols - 1);
-    }
-    return (uint32_t)n;
-  };
-  // (rows that are not there read row 0, and their results are not used)
-  auto x_row = [&](int r) { return (uint32_t)(r < t.rows ? max(mx_src(a, t.row0 + r), 0) : 0); };
-  const i32x4_t wbuf = raw_buffer(a.wc + (size_t)t.e * a.N * (K / 2), (uint32_t)a.N * (uint32_t)(K / 2));
-  const i32x4_t wsbuf = raw_buffer(a.ws + (size_t)t.e * a.N * nb, (uint32_t)a.N * (uint32_t)nb);
-  const i32x4_t xbuf = raw_buffer(a.xc, a.x_bytes);
-  const i32x4_t xsbuf = raw_buffer(a.xs, a.xs_bytes);
-
-  // This lane's source offsets of its copies: CW + CX of 1 KB a wave, and the
-  // scales, 16 bytes a row for two stages.  (What a copy reads behind K, other
-  // rows' bytes or the buffer's zeros, is not contracted.)
+  const int h = lane >> 5, rl = lane & 31;
   constexpr int XB = FP8 ? 256 : 128;
-  constexpr int CW = BN * 128 / 1024 / MXT_WAVES, CX = BM * XB / 1024 / MXT_WAVES, COPIES = CW + CX;
+  constexpr int CW = BN * 128 / 1024 / WAVES, CX = BM * XB / 1024 / WAVES, COPIES = CW + CX;
   constexpr int SG = (BN + BM) / 64;               // groups of 64 rows with scales
-  static_assert(CW >= 1 && CX >= 1 && SG <= MXT_WAVES && BN % 64 == 0 && BM % 64 == 0, "whole copies");
-  uint32_t off[COPIES];
+  static_assert(CW >= 1 && CX >= 1 && SG <= WAVES && BN % 64 == 0 && BM % 64 == 0, "whole copies");
+  const int sr0 = wave % SG * 64;
+
+  // One tile's place and this lane's source offsets of its copies: CW + CX of
+  // 1 KB a wave, and the scales, 16 bytes a row for two stages, a wave those
+  // of 64 rows (waves beyond the rows copy some again): rows on 16-byte
+  // boundaries (WIDE) in one copy, others in four of 4 bytes.
+  struct Item {
+    int e, c0;
+    int dst[FM];                                   // output rows of this lane's tokens; -1: none
+    bool zero[FM];                                 // ... that come out zero
+    uint32_t off[COPIES], soff[WIDE ? 1 : 4];
+  };
+  // The workgroups of one XCD (every eighth) take a run of tiles, token tiles
+  // in fours and those before weight tiles, so that those running at a time
+  // share panels of both operands in its L2; each walks the run by the number
+  // of them.
+  const int mt = __builtin_amdgcn_readfirstlane(mx_count_tiles<BM>(a, lane)), items = mt * nt, run = (items + 7) >> 3;
+  const int last = min(items, ((blockIdx.x & 7) + 1) * run);
+  auto set_up = [&](Item &it, int item) {
+    const int first = item / (4 * nt) * 4, in = item - first * nt, four = min(4, mt - first);
+    const MxTile t = mx_find_tile<BM>(a, first + in % four, lane);
+    it.e = __builtin_amdgcn_readfirstlane(t.e);
+    it.c0 = in / four * BC;
+    const int rows = t.e < 0 ? 0 : t.rows;
+    if (it.e < 0) it.e = 0;                        // (offsets that changed meanwhile: nothing is stored)
+    // Weight row of row r of the tile.  SwiGLU: the first half of a wave's
+    // rows are gate rows, the second half the up rows of the same columns.
+    auto w_row = [&](int r) {
+      int n;
+      if constexpr (SWIGLU) {
+        constexpr int H = FN * 16;                 // columns of a wave
+        const int in = r % (2 * H), c = it.c0 + (r / (2 * H)) * H + in % H;
+        n = min(c, cols - 1) + (in >= H ? cols : 0);
+      } else {
+        n = min(it.c0 + r, cols - 1);
+      }
+      return (uint32_t)n;
+    };
+    // (rows that are not there read row 0, and their results are not used)
+    auto x_row = [&](int r) { return (uint32_t)(r < rows ? max(mx_src(a, t.row0 + r), 0) : 0); };
 #pragma unroll
-  for (int i = 0; i < CW; ++i) {
-    const int r = (i * MXT_WAVES + wave) * 8 + (lane >> 3);
-    off[i] = w_row(r) * (uint32_t)(K / 2) + 16 * piece4(r, lane & 7);
-  }
+    for (int i = 0; i < CW; ++i) {
+      const int r = (i * WAVES + wave) * 8 + (lane >> 3);
+      it.off[i] = w_row(r) * (uint32_t)(K / 2) + 16 * piece4(r, lane & 7);
+    }
 #pragma unroll
-  for (int i = 0; i < CX; ++i) {
-    const int r = (i * MXT_WAVES + wave) * (1024 / XB) + lane / (XB / 16);
-    off[CW + i] = x_row(r) * (uint32_t)(K / (FP8 ? 1 : 2)) + 16 * (FP8 ? piece8(r, lane & 15) : piece4(r, lane & 7));
-  }
+    for (int i = 0; i < CX; ++i) {
+      const int r = (i * WAVES + wave) * (1024 / XB) + lane / (XB / 16);
+      it.off[CW + i] =
+          x_row(r) * (uint32_t)(K / (FP8 ? 1 : 2)) + 16 * (FP8 ? piece8(r, lane & 15) : piece4(r, lane & 7));
+    }
+    const uint32_t so = (sr0 < BN ? w_row(sr0 + lane) : x_row(sr0 + lane - BN)) * (uint32_t)nb;
+    if constexpr (WIDE) {
+      it.soff[0] = so;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)                  // rows 16 i.. of the wave's, four dwords each
+        it.soff[i] = (uint32_t)__shfl((int)so, 16 * i + (lane >> 2), 64) + 4 * (lane & 3);
+    }
+#pragma unroll
+    for (int g = 0; g < FM; ++g) {
+      const int r = (wave / WN) * FM * 32 + 32 * g + rl;
+      it.dst[g] = r < rows ? mx_dst(a, t.row0 + r) : -1;
+      it.zero[g] = r < rows && mx_src(a, t.row0 + r) < 0;
+    }
+  };
+  const i32x4_t xbuf = raw_buffer(a.xc, a.x_bytes), xsbuf = raw_buffer(a.xs, a.xs_bytes);
+  i32x4_t wbuf, wsbuf;
+  auto point = [&](const Item &it) {
+    wbuf = raw_buffer(a.wc + (size_t)it.e * a.N * (K / 2), (uint32_t)a.N * (uint32_t)(K / 2));
+    wsbuf = raw_buffer(a.ws + (size_t)it.e * a.N * nb, (uint32_t)a.N * (uint32_t)nb);
+  };
   // Copy i of stage s.  Stages that are not there are copied from buffers of
-  // no bytes (zeros, into a buffer that nobody reads again), so that no
-  // branch comes between the MFMAs.
+  // no bytes (zeros, into a buffer that nobody reads before its next copy), so
+  // that no branch comes between the MFMAs.  (What a copy reads behind K,
+  // other rows' bytes or the buffer's zeros, is not contracted.)
+  Item cur;
   auto copy = [&](int i, int s) {
     const auto &st = lds.stage[s & 1];
     i32x4_t buf = i < CW ? wbuf : xbuf;
     buf[2] = s < stages ? buf[2] : 0;
     if (i < CW)
-      copy16_to_lds(lds_offset(st.w) + (i * MXT_WAVES + wave) * 1024, buf, off[i], (uint32_t)s * 128);
+      copy16_to_lds(lds_offset(st.w) + (i * WAVES + wave) * 1024, buf, cur.off[i], (uint32_t)s * 128);
     else
-      copy16_to_lds(lds_offset(st.x) + ((i - CW) * MXT_WAVES + wave) * 1024, buf, off[i], (uint32_t)s * XB);
+      copy16_to_lds(lds_offset(st.x) + ((i - CW) * WAVES + wave) * 1024, buf, cur.off[i], (uint32_t)s * XB);
   };
-  // Scales of stages 2j and 2j + 1, a wave those of 64 rows (waves beyond the
-  // rows copy some again): rows on 16-byte boundaries (WIDE) in one copy,
-  // others in four of 4 bytes.  Not wanted: of no bytes, to a place of no use.
-  const int sr0 = wave % SG * 64;
-  const uint32_t soff = (sr0 < BN ? w_row(sr0 + lane) : x_row(sr0 + lane - BN)) * (uint32_t)nb;
-  uint32_t soff4[WIDE ? 1 : 4];
-  if constexpr (!WIDE) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)                    // rows 16 i.. of the wave's, four dwords each
-      soff4[i] = (uint32_t)__shfl((int)soff, 16 * i + (lane >> 2), 64) + 4 * (lane & 3);
-  }
+  // Scales of stages 2j and 2j + 1; not wanted: of no bytes, to a place of no use.
   auto copy_scales = [&](int j, bool wanted) {
     i32x4_t buf = sr0 < BN ? wsbuf : xsbuf;
     buf[2] = wanted ? buf[2] : 0;
     const uint32_t dst = wanted ? lds_offset(lds.scales[j & 1]) + sr0 * 16 : lds_offset(lds.unused) + sr0 * 16;
     if constexpr (WIDE) {
-      copy16_to_lds(dst, buf, soff, (uint32_t)j * 16);
+      copy16_to_lds(dst, buf, cur.soff[0], (uint32_t)j * 16);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) copy4_to_lds(dst + i * 256, buf, soff4[i], (uint32_t)j * 16);
+      for (int i = 0; i < 4; ++i) copy4_to_lds(dst + i * 256, buf, cur.soff[i], (uint32_t)j * 16);
     }
   };
 
-  const int h = lane >> 5, rl = lane & 31;
   const int wr0 = (wave % WN) * FN * 32 + rl, xr0 = (wave / WN) * FM * 32 + rl;
   constexpr int XP = FP8 ? 2 : 1, READS = FN + FM * XP, MFMAS = FN * FM;
   struct Step {
@@ -670,12 +688,6 @@ __global__ __launch_bounds__(MXT_THREADS, 2) void mx_tiled_kernel(MxGemmArgs a) 
     for (int g = 0; g < FM; ++g) sx[g] = *reinterpret_cast<const uint2 *>(sc + (BN + xr0 + 32 * g) * 16);
   };
   f32x16_t acc[FN][FM];
-#pragma unroll
-  for (int f = 0; f < FN; ++f)
-#pragma unroll
-    for (int g = 0; g < FM; ++g)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[f][g][i] = 0.0f;
   // MFMA i of step k
   auto mfma = [&](const Step &o, int i, auto k) {
     constexpr int S = 2 * (decltype(k)::value & 1);
@@ -719,75 +731,100 @@ __global__ __launch_bounds__(MXT_THREADS, 2) void mx_tiled_kernel(MxGemmArgs a) 
     asm volatile("" ::: "memory");
   };
 
-  copy_scales(0, true);
+  int item = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
+  if (item >= last) return;
+  auto start = [&] {                               // the first copies of `cur`
+    point(cur);
+    copy_scales(0, true);
 #pragma unroll
-  for (int i = 0; i < COPIES; ++i) copy(i, 0);
-  arrive();
+    for (int i = 0; i < COPIES; ++i) copy(i, 0);
+  };
+  set_up(cur, item);
+  start();
+  while (true) {
+    // the next tile is looked up while the first copies are in flight, and its
+    // own first copies while this one's results are stored
+    const int next = item + (gridDim.x >> 3);
+    Item nxt;
+    if (next < last) set_up(nxt, next);
 #pragma unroll
-  for (int i = 0; i < HALF; ++i) copy(i, 1);
-  Step A, B;
+    for (int f = 0; f < FN; ++f)
 #pragma unroll
-  for (int i = 0; i < READS; ++i) read(A, i, 0, 0);
-  read_scales(0);
-  const int full = K / 256;
-  for (int s = 0; s < full; ++s) {
-    step(A, k0, B, k1, s, half, copies, s + 1, k0, end);
-    step(B, k1, A, k2, s, k0, k0, 0, k0, end);
-    step(A, k2, B, k3, s, k0, k0, 0, k0, end);
-    step(B, k3, A, none, 0, k0, k0, 0, k0, mid);
+      for (int g = 0; g < FM; ++g)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[f][g][i] = 0.0f;
     arrive();
-    // the buffer of the scales of stages s - 2 and s - 1
-    copy_scales((s >> 1) + 1, (s & 1) == 0 && s + 2 < stages);
-    // (behind the last stage, operands and scales are read for nothing)
-    step(B, k3, A, k0, s + 1, k0, half, s + 2, mid, end);
-    read_scales(s + 1);
-  }
-  if (full < stages) {                             // the last 128 positions
-    step(A, k0, B, k1, full, k0, k0, 0, k0, end);
-    step(B, k1, A, none, 0, k0, k0, 0, k0, end);
+#pragma unroll
+    for (int i = 0; i < HALF; ++i) copy(i, 1);
+    Step A, B;
+#pragma unroll
+    for (int i = 0; i < READS; ++i) read(A, i, 0, 0);
+    read_scales(0);
+    const int full = K / 256;
+    for (int s = 0; s < full; ++s) {
+      step(A, k0, B, k1, s, half, copies, s + 1, k0, end);
+      // to the buffer of the scales of stages s - 2 and s - 1, behind the codes
+      // that are waited for first: 64 rows are 64 lines for the address unit
+      copy_scales((s >> 1) + 1, (s & 1) == 0 && s + 2 < stages);
+      step(B, k1, A, k2, s, k0, k0, 0, k0, end);
+      step(A, k2, B, k3, s, k0, k0, 0, k0, end);
+      step(B, k3, A, none, 0, k0, k0, 0, k0, mid);
+      arrive();
+      // (behind the last stage, operands and scales are read for nothing)
+      step(B, k3, A, k0, s + 1, k0, half, s + 2, mid, end);
+      read_scales(s + 1);
+    }
+    if (full < stages) {                           // the last 128 positions
+      step(A, k0, B, k1, full, k0, k0, 0, k0, end);
+      step(B, k1, A, none, 0, k0, k0, 0, k0, end);
+    }
+    const int c0 = cur.c0;
+    int dst[FM];
+    bool zero[FM];
+#pragma unroll
+    for (int g = 0; g < FM; ++g) dst[g] = cur.dst[g], zero[g] = cur.zero[g];
+    if (next < last) {
+      arrive();                                    // every wave is done with the buffers
+      cur = nxt;
+      start();
+    }
+    // Results.  A lane holds four neighbouring features of a token at a time;
+    // exchanging halves of the wave makes that eight, 16 bytes a store.
+    constexpr int OF = SWIGLU ? FN / 2 : FN;
+#pragma unroll
+    for (int g = 0; g < FM; ++g) {
+      uint16_t *y = a.y + (size_t)max(dst[g], 0) * cols;
+#pragma unroll
+      for (int f = 0; f < OF; ++f)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          uint32_t w[2][2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float u = acc[f][g][4 * (i + q) + j];
+              if constexpr (SWIGLU)
+                v[j] = silu_f32(u) * acc[f + OF][g][4 * (i + q) + j];
+              else
+                v[j] = u;
+            }
+            w[q][0] = pack_bf16x2(v[0], v[1]);
+            w[q][1] = pack_bf16x2(v[2], v[3]);
+          }
+          const auto lo = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+          const auto hi = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+          const int c = c0 + (wave % WN) * OF * 32 + 32 * f + 8 * (i + h);
+          if (dst[g] < 0 || c >= cols) continue;
+          *reinterpret_cast<uint4 *>(y + c) =
+              zero[g] ? make_uint4(0, 0, 0, 0) : make_uint4(lo[0], hi[0], lo[1], hi[1]);
+        }
+    }
+    if (next >= last) break;
+    item = next;
   }
   wait_copies<0>();
-
-  // Results.  A lane holds four neighbouring features of a token at a time:
-  // stored as they are, a 256 x 256 tile took 12 us.  They pass through LDS
-  // to lines of 16 bytes a lane, each wave its own tokens and columns.
-  constexpr int OF = SWIGLU ? FN / 2 : FN, OC = OF * 32, TR = FM * 32;   // columns and tokens of a wave
-  constexpr int STRIDE = OC * 2 + 16, LPR = OC * 2 / 16;
-  static_assert(MXT_WAVES * TR * STRIDE <= (int)sizeof(Lds), "results fit the operands' space");
-  __builtin_amdgcn_s_barrier();                    // every wave has read its last operands
-  asm volatile("" ::: "memory");
-  uint8_t *out = reinterpret_cast<uint8_t *>(&lds) + wave * TR * STRIDE;
-#pragma unroll
-  for (int g = 0; g < FM; ++g) {
-    if ((wave / WN) * TR + 32 * g >= t.rows) break;
-#pragma unroll
-    for (int f = 0; f < OF; ++f)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float u = acc[f][g][4 * i + j];
-          if constexpr (SWIGLU)
-            v[j] = silu_f32(u) * acc[f + OF][g][4 * i + j];
-          else
-            v[j] = u;
-        }
-        *reinterpret_cast<uint2 *>(out + (32 * g + rl) * STRIDE + (32 * f + 8 * i + 4 * h) * 2) =
-            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-      }
-  }
-  const int c = c0 + (wave % WN) * OC + lane % LPR * 8;
-#pragma unroll 4
-  for (int i = 0; i < TR * LPR / 64; ++i) {
-    const int r = i * (64 / LPR) + lane / LPR, row = (wave / WN) * TR + r;
-    if (row >= t.rows || c >= cols) continue;
-    const uint4 v = *reinterpret_cast<const uint4 *>(out + r * STRIDE + lane % LPR * 16);
-    const int dst = mx_dst(a, t.row0 + row);
-    if (dst < 0) continue;
-    *reinterpret_cast<uint4 *>(a.y + (size_t)dst * cols + c) =
-        mx_src(a, t.row0 + row) >= 0 ? v : make_uint4(0, 0, 0, 0);
-  }
 }
 
 // Upper bound of the token tiles of BM rows: an expert with rows has at most
@@ -831,18 +868,32 @@ static void launch_stream_split(const MxGemmArgs &a, hipStream_t stream) {
   else launch_stream<FP8, SWIGLU, 1, 2, FM>(a, stream);
 }
 
+template <bool FP8, bool SWIGLU, int WN, int WM, int FN, int FM>
+static void launch_tiled(const MxGemmArgs &a, hipStream_t stream) {
+  constexpr int BM = WM * FM * 32, BC = WN * FN * 32 / (SWIGLU ? 2 : 1);
+  const long long items = mx_tiles(a, BM) * (((SWIGLU ? a.N / 2 : a.N) + BC - 1) / BC);
+  const int per_cu = sizeof(MxTileLds<FP8, WN * FN * 32, BM>) > 81920 ? 1 : 2;
+  const long long slots = (long long)device_cu_count() * per_cu;
+  const dim3 grid((unsigned)((std::min(items, slots) + 7) & ~7ll)), block(WN * WM * 64);
+  if (a.wide_scales)
+    hipLaunchKernelGGL((mx_tiled_kernel<FP8, SWIGLU, true, WN, WM, FN, FM>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((mx_tiled_kernel<FP8, SWIGLU, false, WN, WM, FN, FM>), grid, block, 0, stream, a);
+}
+
 template <bool FP8, bool SWIGLU>
 static moesq_status_t launch_mx(const MxGemmArgs &a, hipStream_t stream) {
-  const int cols = SWIGLU ? a.N / 2 : a.N;
   if (a.K % 128 == 0 && (long long)a.M >= 32ll * a.E) {
-    constexpr int WN = FP8 ? 4 : 2, FN = FP8 ? 2 : 4, FM = 2;
-    constexpr int BM = 8 / WN * FM * 32, BC = WN * FN * 32 / (SWIGLU ? 2 : 1);
-    const long long tt = mx_tiles(a, BM);
-    const dim3 grid((unsigned)((tt * ((cols + BC - 1) / BC) + 7) & ~7ll));
-    if (a.wide_scales)
-      hipLaunchKernelGGL((mx_tiled_kernel<FP8, SWIGLU, true, WN, FN, FM>), grid, dim3(MXT_THREADS), 0, stream, a);
+#ifdef MXTUNE
+    const int v = getenv("MXV") ? atoi(getenv("MXV")) : 0;
+    if (v == 1) launch_tiled<FP8, SWIGLU, 2, 2, 2, 2>(a, stream);
+    else if (v == 2) launch_tiled<FP8, SWIGLU, 4, 2, 2, 1>(a, stream);
+    else if (v == 3) launch_tiled<FP8, SWIGLU, 4, 2, 2, 2>(a, stream);
+    else if (v == 5) launch_tiled<FP8, SWIGLU, 2, 2, 2, 1>(a, stream);
+    else if constexpr (FP8) launch_tiled<FP8, SWIGLU, 4, 2, 2, 2>(a, stream);
     else
-      hipLaunchKernelGGL((mx_tiled_kernel<FP8, SWIGLU, false, WN, FN, FM>), grid, dim3(MXT_THREADS), 0, stream, a);
+#endif
+    launch_tiled<FP8, SWIGLU, FP8 ? 4 : 2, FP8 ? 2 : 4, FP8 ? 2 : 4, 2>(a, stream);
   } else if ((long long)a.M <= 16ll * a.E) {
     launch_stream_split<FP8, SWIGLU, 1>(a, stream);
   } else {
