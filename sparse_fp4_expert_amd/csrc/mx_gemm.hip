@@ -11,7 +11,6 @@
 // operand, tokens the second: a lane's four results are four neighbouring
 // output features of one token.
 #include <stddef.h>
-#include <stdlib.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -31,7 +30,8 @@ struct MxGemmArgs {
   uint16_t *y;
   int k, M, E, N, K;
   int flat;
-  bool wide_scales;            // every row's scales on 16-byte boundaries
+  bool copies;                 // every row's scales on 4-byte boundaries
+  bool wide_scales;            // ... on 16-byte boundaries
   uint32_t x_bytes, xs_bytes;  // of all activation rows
 };
 
@@ -358,7 +358,7 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGem
 // ------------------------------------------------------------------ direct kernel (any K)
 //
 // Rows of K % 128 != 0 have scale bytes at any alignment and end inside an
-// MFMA step.  The waves are those of the streaming kernel, with operands
+// MFMA step (and a caller's scales may start on any byte).  The waves are those of the streaming kernel, with operands
 // straight from global memory in chunks of 256 positions, the next one in
 // flight, and codes behind K zero.  The order of the positions is free as
 // long as both operands agree: MFMA block j of step s is the chunk's block 2j
@@ -836,10 +836,9 @@ static long long mx_tiles(const MxGemmArgs &a, int bm) {
 template <bool FP8, bool SWIGLU, int KSPLIT, int FN, int FM>
 static void launch_stream(const MxGemmArgs &a, hipStream_t stream) {
   const int frags = a.N / 16;
-  const bool copies = a.K % 128 == 0;
-  const int rg = mxs_waves(KSPLIT) / KSPLIT * (copies ? FN : 1);
+  const int rg = mxs_waves(KSPLIT) / KSPLIT * (a.copies ? FN : 1);
   const dim3 grid((unsigned)(mx_tiles(a, 16 * FM) * ((frags + rg - 1) / rg))), block(mxs_waves(KSPLIT) * 64);
-  if (copies)
+  if (a.copies)
     hipLaunchKernelGGL((mx_stream_kernel<FP8, SWIGLU, KSPLIT, FN, FM>), grid, block, 0, stream, a);
   else
     hipLaunchKernelGGL((mx_direct_kernel<FP8, SWIGLU, KSPLIT, FM>), grid, block, 0, stream, a);
@@ -872,8 +871,9 @@ template <bool FP8, bool SWIGLU, int WN, int WM, int FN, int FM>
 static void launch_tiled(const MxGemmArgs &a, hipStream_t stream) {
   constexpr int BM = WM * FM * 32, BC = WN * FN * 32 / (SWIGLU ? 2 : 1);
   const long long items = mx_tiles(a, BM) * (((SWIGLU ? a.N / 2 : a.N) + BC - 1) / BC);
-  const int per_cu = sizeof(MxTileLds<FP8, WN * FN * 32, BM>) > 81920 ? 1 : 2;
-  const long long slots = (long long)device_cu_count() * per_cu;
+  // as many workgroups as run at a time, each walking over its tiles
+  constexpr int PER_CU = sizeof(MxTileLds<FP8, WN * FN * 32, BM>) > 80 * 1024 ? 1 : 2;
+  const long long slots = (long long)device_cu_count() * PER_CU;
   const dim3 grid((unsigned)((std::min(items, slots) + 7) & ~7ll)), block(WN * WM * 64);
   if (a.wide_scales)
     hipLaunchKernelGGL((mx_tiled_kernel<FP8, SWIGLU, true, WN, WM, FN, FM>), grid, block, 0, stream, a);
@@ -881,23 +881,42 @@ static void launch_tiled(const MxGemmArgs &a, hipStream_t stream) {
     hipLaunchKernelGGL((mx_tiled_kernel<FP8, SWIGLU, false, WN, WM, FN, FM>), grid, block, 0, stream, a);
 }
 
+// The kernel and its tile, from the rows an expert has on average (`avg`; the
+// host does not know more) and the tiles that makes.  Up to 8 rows an expert,
+// or where the smallest tile would leave half the CUs without one, the
+// streaming kernel; then the largest tile that the rows fill and that gives
+// every CU one.  Measured, us:
+//   FP4, 128 experts of 1536 x 2048     stream  128x64  128x128  256x256
+//      8 rows an expert                   30.8    32.6     28.8
+//     16                                  39.9    32.1     36.4
+//     64                                 103.2    53.0     50.2     59.8
+//    128                                 181.1    80.0     69.3     77.5
+//    256 (uneven loads)                            151      127      120
+//   FP8, 48 experts of 4096 x 7168      stream  128x64  256x128
+//     21 rows an expert                  202.3   147.6    153.7
+//     85                                 542.7   254.8    217.7
+//   FP4, dense, 4096 x 7168             stream  128x64  128x128  256x256
+//     64 rows                              7.7    14.7     18.3     39.5
+//    1024                                         29.7     27.8     43.7
+//    2048                                101.0    52.4     40.2     44.3
+//    4096                                191.0   100.1     74.2     61.1
 template <bool FP8, bool SWIGLU>
 static moesq_status_t launch_mx(const MxGemmArgs &a, hipStream_t stream) {
-  if (a.K % 128 == 0 && (long long)a.M >= 32ll * a.E) {
-#ifdef MXTUNE
-    const int v = getenv("MXV") ? atoi(getenv("MXV")) : 0;
-    if (v == 1) launch_tiled<FP8, SWIGLU, 2, 2, 2, 2>(a, stream);
-    else if (v == 2) launch_tiled<FP8, SWIGLU, 4, 2, 2, 1>(a, stream);
-    else if (v == 3) launch_tiled<FP8, SWIGLU, 4, 2, 2, 2>(a, stream);
-    else if (v == 5) launch_tiled<FP8, SWIGLU, 2, 2, 2, 1>(a, stream);
-    else if constexpr (FP8) launch_tiled<FP8, SWIGLU, 4, 2, 2, 2>(a, stream);
-    else
-#endif
-    launch_tiled<FP8, SWIGLU, FP8 ? 4 : 2, FP8 ? 2 : 4, FP8 ? 2 : 4, 2>(a, stream);
-  } else if ((long long)a.M <= 16ll * a.E) {
-    launch_stream_split<FP8, SWIGLU, 1>(a, stream);
+  const int experts = std::min(a.E, a.M), avg = (a.M + experts - 1) / experts;
+  auto tiles = [&](int bn, int bm) {
+    return (long long)experts * ((avg + bm - 1) / bm) * ((a.N + bn - 1) / bn);
+  };
+  const int cus = device_cu_count();
+  if (!a.copies || (long long)a.M <= 8ll * a.E || tiles(128, 64) < cus / 2) {
+    if (avg <= 16) launch_stream_split<FP8, SWIGLU, 1>(a, stream);
+    else launch_stream_split<FP8, SWIGLU, 2>(a, stream);
+  } else if constexpr (FP8) {
+    if (avg > 80 && tiles(256, 128) >= cus) launch_tiled<true, SWIGLU, 4, 2, 2, 2>(a, stream);
+    else launch_tiled<true, SWIGLU, 2, 2, 2, 1>(a, stream);
   } else {
-    launch_stream_split<FP8, SWIGLU, 2>(a, stream);
+    if (avg > 192 && tiles(256, 256) >= cus) launch_tiled<false, SWIGLU, 2, 4, 4, 2>(a, stream);
+    else if (avg > 32 && tiles(128, 128) >= cus) launch_tiled<false, SWIGLU, 2, 2, 2, 2>(a, stream);
+    else launch_tiled<false, SWIGLU, 2, 2, 2, 1>(a, stream);
   }
   return launch_status("moesq_mx_gemm");
 }
@@ -950,6 +969,7 @@ extern "C" moesq_status_t moesq_mx_gemm(const moesq_mx_t *x, const int32_t *perm
     return fail(MOESQ_ERR_ARG, who + ": codes and y must be 16-byte aligned");
   MxGemmArgs a{x->codes, x->scales, w->codes, w->scales, perm, expert_offsets, y,
                k,        M,         E,        N,         w->K, flat,
+               w->K % 128 == 0 && !(((uintptr_t)x->scales | (uintptr_t)w->scales) & 3),
                w->K % 512 == 0 && !(((uintptr_t)x->scales | (uintptr_t)w->scales) & 15), (uint32_t)xb,
                (uint32_t)((long long)x->rows * (x->K / 32))};
   if (epilogue == MOESQ_EPI_SWIGLU)

@@ -181,6 +181,87 @@ def test_grouped(lib, fmt, counts):
                swiglu=len(counts) % 2 == 1)
 
 
+# Enough tiles to reach every tile size: with 256 CUs, 128 x 64 from 128 tiles
+# on, 128 x 128 (FP4) and 256 x 128 (FP8) or 256 x 256 from 256 of their own.
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("T,N", [(250, 4112), (1000, 4128), (2047, 4096), (4090, 4128)])
+@pytest.mark.parametrize("K", [128, 256, 384, 512, 1152])
+def test_dense_tiles(lib, fmt, T, N, K):
+    swiglu = N % 32 == 0 and K % 256 == 0
+    print(f"[mx tiles] {fmt} T={T} N={N} K={K} swiglu={swiglu}", flush=True)
+    check_gemm(lib, np.random.default_rng(T + K), 1, N, K, None, fmt, swiglu, T=T)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("E,mean,N,K", [(64, 9, 256, 384), (40, 20, 528, 128), (70, 40, 544, 512), (40, 100, 1056, 256),
+                                        (33, 250, 2080, 384), (300, 11, 96, 256)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_grouped_tiles(lib, fmt, E, mean, N, K, swiglu):
+    """Uneven loads about a mean: experts without rows, with one, and with
+    several tiles."""
+    if swiglu and N % 32:
+        N += 16
+    rng = np.random.default_rng(E + mean)
+    counts = rng.poisson(mean, E) * rng.integers(0, 3, E)
+    counts[:3] = 0, 1, 3 * mean
+    counts[-1] += max(0, E * mean - counts.sum())       # the mean at least
+    print(f"[mx grouped tiles] {fmt} E={E} mean={mean} N={N} K={K} swiglu={swiglu}", flush=True)
+    check_gemm(lib, rng, E, N, K, [int(c) for c in counts], fmt, swiglu)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("E,T,k,N,K", [(64, 400, 2, 256, 256), (40, 1300, 3, 1056, 384), (32, 2100, 4, 2112, 512)])
+@pytest.mark.parametrize("flat", [False, True])
+def test_gather_tiles(lib, fmt, E, T, k, N, K, flat):
+    rng = np.random.default_rng(E + T)
+    skew = rng.standard_normal(E)
+    ids = np.argsort(-(rng.standard_normal((T, E)) + skew), axis=1)[:, :k].reshape(-1)
+    print(f"[mx gather tiles] {fmt} E={E} T={T} k={k} flat={flat}", flush=True)
+    check_gemm(lib, rng, E, N, K, None, fmt, swiglu=flat, k=k, T=T, flat=flat, ids=ids)
+
+
+def test_tiles_leave_other_rows(lib):
+    """Rows behind the last expert and rows of bad permutation entries, in the
+    tiled kernels."""
+    rng = np.random.default_rng(11)
+    E, T, k, N, K = 64, 700, 2, 512, 256
+    ids = rng.integers(0, E, T * k).astype(np.int32)
+    ids[1300:] = -1
+    w = lib.mx_quantize(torch.randn(E, N, K, device="cuda"))
+    for f in FMT.values():
+        q = lib.mx_quantize(rows_of(rng, T, K).cuda(), f)
+        off, perm, _ = lib.route(torch.from_numpy(ids).cuda(), E, k)
+        perm[1300:] = -1
+        bad = perm.clone()
+        bad[7], bad[900] = T * k, -3
+        y = torch.full((T * k, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        z = y.clone()
+        lib.mx_gemm(q, w, off, perm=perm, k=k, out=y)
+        lib.mx_gemm(q, w, off, perm=bad, k=k, out=z)
+        assert (y[1300:] == 7).all() and (z[1300:] == 7).all() and (z[[7, 900]] == 0).all()
+        y[[7, 900]] = 0
+        assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+def test_unaligned_scales(lib, fmt):
+    """Scales that start on any byte give the same results."""
+    for T, N, K in ((16, 256, 512), (2048, 4096, 512)):
+        x = lib.mx_quantize(torch.randn(T, K, device="cuda").to(torch.bfloat16), FMT[fmt])
+        w = lib.mx_quantize(torch.randn(N, K, device="cuda"))
+        want = lib.mx_gemm(x, w)
+
+        def moved(q, by):
+            s = torch.empty(q.scales.numel() + by, dtype=torch.uint8, device="cuda")
+            s = s[by:].view(q.scales.shape).copy_(q.scales)
+            return lib.Mx(q.codes, s, q.format)
+        for by in (1, 2, 4, 8):
+            got = lib.mx_gemm(moved(x, by), moved(w, by)).double()
+            assert (got - want.double()).norm() <= 2.0 ** -8 * want.double().norm()
+            if by % 4 == 0:
+                assert torch.equal(got, want.double())
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("E,T,k,N,K", [(8, 1, 2, 64, 256), (8, 64, 2, 128, 256), (128, 16, 8, 160, 256),
                                        (5, 333, 3, 96, 416), (3, 700, 2, 288, 640)])
