@@ -30,8 +30,8 @@ struct MxGemmArgs {
   uint16_t *y;
   int k, M, E, N, K;
   int flat;
-  bool copies;                 // every row's scales on 4-byte boundaries
-  bool wide_scales;            // ... on 16-byte boundaries
+  bool aligned, wide;          // every row's scales on 4-byte, 16-byte boundaries
+  uint32_t xs_off, ws_off;     // of the scales from the 4-byte boundary that xs, ws are
   uint32_t x_bytes, xs_bytes;  // of all activation rows
 };
 
@@ -212,7 +212,16 @@ __device__ __forceinline__ void mx_stream_finish(const MxGemmArgs &a, const MxTi
 __device__ __forceinline__ int piece4(int r, int c) { return c ^ ((r >> 1) & 7); }
 __device__ __forceinline__ int piece8(int r, int c) { return c ^ (r & 15); }
 
-// ------------------------------------------------------------------ streaming kernel (K % 128 == 0)
+// Scales in LDS.  A row's scale bytes may start anywhere; copies take 4-byte
+// words from the boundary at or before a stage's first byte, and `sub`, the
+// byte in the word, stays the same from stage to stage.  Four scale bytes
+// from p + sub on:
+__device__ __forceinline__ uint32_t scale_word(const uint8_t *p, uint32_t sub, bool aligned) {
+  const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
+  return aligned ? w[0] : __builtin_amdgcn_alignbyte(w[1], w[0], sub);
+}
+
+// ------------------------------------------------------------------ streaming kernel
 //
 // Few rows: bound by the stream of weights.  A wave contracts FN fragments of
 // 16 weight rows with FM of 16 tokens in stages of 256 positions, copied to a
@@ -227,24 +236,30 @@ __device__ __forceinline__ int piece8(int r, int c) { return c ^ (r & 15); }
 
 constexpr int mxs_waves(int ksplit) { return ksplit < 4 ? 4 : ksplit; }
 
-template <bool FP8, int FN, int FM>
+// 4-byte words of a row's scales for a stage, and the copies of 64 of them
+// for that many fragments of 16 rows.
+constexpr int mxs_words(bool aligned) { return aligned ? 2 : 3; }
+constexpr int mxs_scale_copies(bool aligned, int frags) { return (frags * 16 * mxs_words(aligned) + 63) / 64; }
+
+template <bool FP8, bool ALIGNED, int FN, int FM>
 struct MxRing {
   uint8_t w[FN * 16 * 128];
   uint8_t x[FM * 16 * (FP8 ? 256 : 128)];
-  uint8_t ws[256];                                 // rows x 8, 16 rows twice
-  uint8_t xs[256];
+  uint8_t ws[mxs_scale_copies(ALIGNED, FN) * 256];
+  uint8_t xs[mxs_scale_copies(ALIGNED, FM) * 256];
 };
 
-template <bool FP8, bool SWIGLU, int KSPLIT, int FN, int FM>
+template <bool FP8, bool SWIGLU, bool ALIGNED, int KSPLIT, int FN, int FM>
 __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGemmArgs a) {
   constexpr int WAVES = mxs_waves(KSPLIT);
   constexpr int RG = WAVES / KSPLIT;               // row groups of FN fragments a workgroup
   constexpr int FC = SWIGLU ? 8 : 16;              // output columns a fragment
-  static_assert(FN <= 2 && FM <= 2, "one scale copy each");
   constexpr int XB = FP8 ? 256 : 128;              // bytes of a token's stage
-  constexpr int CW = FN * 2 + 1;                       // copies of a stage's weights and their scales
-  constexpr int CX = FM * 16 * XB / 1024 + 1;      // copies of its tokens and theirs
-  using Ring = MxRing<FP8, FN, FM>;
+  // copies of a stage's weights and of its tokens, without and with the scales
+  constexpr int WC = FN * 2, WS = mxs_scale_copies(ALIGNED, FN), CW = WC + WS;
+  constexpr int XC = FM * 16 * XB / 1024, XS = mxs_scale_copies(ALIGNED, FM), CX = XC + XS;
+  constexpr int WORDS = mxs_words(ALIGNED);
+  using Ring = MxRing<FP8, ALIGNED, FN, FM>;
   __shared__ __attribute__((aligned(1024))) Ring ring[WAVES][2];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, rl = lane & 15;
@@ -261,46 +276,70 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGem
 
   // (rows that are not there read row 0, and their results are not used;
   // positions behind K in the last stage, other rows' or the buffers' zeros,
-  // are not contracted)
+  // are masked)
   const i32x4_t wbuf = raw_buffer(a.wc + (size_t)t.e * a.N * (K / 2), (uint32_t)a.N * (uint32_t)(K / 2));
-  const i32x4_t wsbuf = raw_buffer(a.ws + (size_t)t.e * a.N * nb, (uint32_t)a.N * (uint32_t)nb);
+  const i32x4_t wsbuf = raw_buffer(a.ws + (size_t)t.e * a.N * nb, (a.ws_off + (uint32_t)a.N * (uint32_t)nb + 3) & ~3u);
   auto w_row = [&](int r) {
     // (columns come in whole fragments)
     const int c = c0 + (r >> 4) * FC + (SWIGLU ? r & 7 : r & 15);
     return (uint32_t)(c >= cols ? 0 : SWIGLU ? c + ((r >> 3) & 1) * cols : c);
   };
-  uint32_t wo[CW - 1];
+  uint32_t wo[WC], wso[WS];
 #pragma unroll
-  for (int i = 0; i < CW - 1; ++i) {
+  for (int i = 0; i < WC; ++i) {
     const int r = i * 8 + (lane >> 3);
     wo[i] = w_row(r) * (uint32_t)(K / 2) + 16 * piece4(r, lane & 7);
   }
-  const uint32_t wso = w_row((lane >> 1) & (16 * FN - 1)) * (uint32_t)nb + 4 * (lane & 1);
+  // word d of a stage's scales: word d % WORDS of row d / WORDS
+  auto scale_at = [&](int i, int rows, int &row, int &word) {
+    const int d = i * 64 + lane;
+    row = min(d / WORDS, rows - 1);
+    word = d % WORDS;
+  };
+#pragma unroll
+  for (int i = 0; i < WS; ++i) {
+    int r, word;
+    scale_at(i, 16 * FN, r, word);
+    wso[i] = ((w_row(r) * (uint32_t)nb + a.ws_off) & ~3u) + 4 * word;
+  }
   auto fetch_w = [&](int slot, int c) {
     const uint32_t base = lds0 + slot * (uint32_t)sizeof(Ring);
 #pragma unroll
-    for (int i = 0; i < CW - 1; ++i) copy16_to_lds(base + i * 1024, wbuf, wo[i], (uint32_t)c * 128);
-    copy4_to_lds(base + offsetof(Ring, ws), wsbuf, wso, (uint32_t)c * 8);
+    for (int i = 0; i < WC; ++i) copy16_to_lds(base + i * 1024, wbuf, wo[i], (uint32_t)c * 128);
+#pragma unroll
+    for (int i = 0; i < WS; ++i) copy4_to_lds(base + offsetof(Ring, ws) + i * 256, wsbuf, wso[i], (uint32_t)c * 8);
   };
   // the first weights are under way before the tokens' rows are looked up
   if (n > 0) fetch_w(0, kw);
   if (n > 1) fetch_w(1, kw + KSPLIT);
 
-  const i32x4_t xbuf = raw_buffer(a.xc, a.x_bytes), xsbuf = raw_buffer(a.xs, a.xs_bytes);
+  const i32x4_t xbuf = raw_buffer(a.xc, a.x_bytes), xsbuf = raw_buffer(a.xs, (a.xs_off + a.xs_bytes + 3) & ~3u);
   auto x_row = [&](int r) { return (uint32_t)(r < t.rows ? max(mx_src(a, t.row0 + r), 0) : 0); };
-  uint32_t xo[CX - 1];
+  uint32_t xo[XC], xso[XS];
 #pragma unroll
-  for (int i = 0; i < CX - 1; ++i) {
+  for (int i = 0; i < XC; ++i) {
     const int r = i * (1024 / XB) + lane / (XB / 16);
     xo[i] = x_row(r) * (uint32_t)(K / (FP8 ? 1 : 2)) + 16 * (FP8 ? piece8(r, lane & 15) : piece4(r, lane & 7));
   }
-  const uint32_t xso = x_row((lane >> 1) & (16 * FM - 1)) * (uint32_t)nb + 4 * (lane & 1);
+#pragma unroll
+  for (int i = 0; i < XS; ++i) {
+    int r, word;
+    scale_at(i, 16 * FM, r, word);
+    xso[i] = ((x_row(r) * (uint32_t)nb + a.xs_off) & ~3u) + 4 * word;
+  }
+  // the byte in its word at which a row's scales start
+  uint32_t wsub[FN], xsub[FM];
+#pragma unroll
+  for (int f = 0; f < FN; ++f) wsub[f] = ALIGNED ? 0 : w_row(16 * f + rl) * (uint32_t)nb + a.ws_off;
+#pragma unroll
+  for (int g = 0; g < FM; ++g) xsub[g] = ALIGNED ? 0 : x_row(16 * g + rl) * (uint32_t)nb + a.xs_off;
   auto fetch_x = [&](int slot, int c) {
     const uint32_t base = lds0 + slot * (uint32_t)sizeof(Ring);
 #pragma unroll
-    for (int i = 0; i < CX - 1; ++i)
+    for (int i = 0; i < XC; ++i)
       copy16_to_lds(base + offsetof(Ring, x) + i * 1024, xbuf, xo[i], (uint32_t)c * XB);
-    copy4_to_lds(base + offsetof(Ring, xs), xsbuf, xso, (uint32_t)c * 8);
+#pragma unroll
+    for (int i = 0; i < XS; ++i) copy4_to_lds(base + offsetof(Ring, xs) + i * 256, xsbuf, xso[i], (uint32_t)c * 8);
   };
   if (n > 0) fetch_x(0, kw);
   if (n > 1) fetch_x(1, kw + KSPLIT);
@@ -310,25 +349,34 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGem
   for (int f = 0; f < FN; ++f)
 #pragma unroll
     for (int g = 0; g < FM; ++g) acc[f][g] = f32x4_t{0, 0, 0, 0};
-  auto step = [&](const Ring &k, int s) {          // 128 positions
+  // 128 positions, of which the first `left` blocks of the stage are there
+  auto step = [&](const Ring &k, int s, int left) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
+    auto there = [&](int block, uint4 v) { return ALIGNED || block < left ? v : zero; };
+    auto scale = [&](const uint8_t *p, uint32_t sub) {
+      const uint32_t v = scale_word(p + 4 * s, sub, ALIGNED) >> (8 * q);
+      return ALIGNED || 4 * s + q < left ? v : 0u;
+    };
     i32x8_t X[FM];
     uint32_t sx[FM];
 #pragma unroll
     for (int g = 0; g < FM; ++g) {
       const int r = 16 * g + rl;
-      sx[g] = *reinterpret_cast<const uint32_t *>(k.xs + r * 8 + 4 * s) >> (8 * q);
+      sx[g] = scale(k.xs + r * 4 * WORDS, xsub[g]);
       if constexpr (FP8)
-        X[g] = as_operand(*reinterpret_cast<const uint4 *>(k.x + r * 256 + 16 * piece8(r, 8 * s + q)),
-                          *reinterpret_cast<const uint4 *>(k.x + r * 256 + 16 * piece8(r, 8 * s + 4 + q)));
+        X[g] = as_operand(
+            there(4 * s + (q >> 1), *reinterpret_cast<const uint4 *>(k.x + r * 256 + 16 * piece8(r, 8 * s + q))),
+            there(4 * s + 2 + (q >> 1), *reinterpret_cast<const uint4 *>(k.x + r * 256 + 16 * piece8(r, 8 * s + 4 + q))));
       else
-        X[g] = as_operand(*reinterpret_cast<const uint4 *>(k.x + r * 128 + 16 * piece4(r, 4 * s + q)), zero);
+        X[g] = as_operand(
+            there(4 * s + q, *reinterpret_cast<const uint4 *>(k.x + r * 128 + 16 * piece4(r, 4 * s + q))), zero);
     }
 #pragma unroll
     for (int f = 0; f < FN; ++f) {
       const int r = 16 * f + rl;
-      const uint32_t sw = *reinterpret_cast<const uint32_t *>(k.ws + r * 8 + 4 * s) >> (8 * q);
-      const i32x8_t W = as_operand(*reinterpret_cast<const uint4 *>(k.w + r * 128 + 16 * piece4(r, 4 * s + q)), zero);
+      const uint32_t sw = scale(k.ws + r * 4 * WORDS, wsub[f]);
+      const i32x8_t W = as_operand(
+          there(4 * s + q, *reinterpret_cast<const uint4 *>(k.w + r * 128 + 16 * piece4(r, 4 * s + q))), zero);
 #pragma unroll
       for (int g = 0; g < FM; ++g) acc[f][g] = mfma_mx<FP8, 0>(W, X[g], acc[f][g], sw, sx[g]);
     }
@@ -341,8 +389,8 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGem
     else wait_copies<CW + CX>();
     const int c = kw + i * KSPLIT;
     const Ring &k = ring[wave][i & 1];
-    step(k, 0);
-    if (K - 256 * c > 128) step(k, 1);
+    step(k, 0, nb - 8 * c);
+    if (nb - 8 * c > 4) step(k, 1, nb - 8 * c);
     // the slot's reads are done before it is written again
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     if (i + 2 < n) {
@@ -355,158 +403,7 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGem
     mx_stream_finish<SWIGLU, KSPLIT, FM>(a, t, acc[f], &ring[0][0], c0 + f * FC, cols, wave, lane);
 }
 
-// ------------------------------------------------------------------ direct kernel (any K)
-//
-// Rows of K % 128 != 0 have scale bytes at any alignment and end inside an
-// MFMA step (and a caller's scales may start on any byte).  The waves are those of the streaming kernel, with operands
-// straight from global memory in chunks of 256 positions, the next one in
-// flight, and codes behind K zero.  The order of the positions is free as
-// long as both operands agree: MFMA block j of step s is the chunk's block 2j
-// + s, so a lane's codes are 32 contiguous bytes and its scales two.
-
-template <bool FP8, int FM>
-struct MxChunk {
-  uint4 w[2];
-  uint4 x[FM][FP8 ? 4 : 2];
-  uint32_t sw, sx[FM];
-};
-
-// One lane's rows: offsets (32 bits: an expert's codes and the activations'
-// stay under 4 GiB) from the bases of the expert and of the activations.
-template <int FM>
-struct MxLane {
-  const uint8_t *w, *ws, *x, *xs;
-  uint32_t wo, wso, xo[FM], xso[FM];
-};
-
-// Scale bytes 2j, 2j + 1 of a chunk for lane group j; rows need no alignment.
-__device__ __forceinline__ uint32_t load_scales2(const uint8_t *p) {
-  uint16_t v;
-  __builtin_memcpy(&v, p, 2);
-  return v;
-}
-
-// Chunk c of the lane's rows; `left` blocks of it lie inside K (8: all).
-__device__ __forceinline__ uint4 load16(const uint8_t *base, uint32_t off) {
-  return *reinterpret_cast<const uint4 *>(base + off);
-}
-
-template <bool FP8, int FM>
-__device__ __forceinline__ void load_chunk(MxChunk<FP8, FM> &k, const MxLane<FM> &p, int c, int q, int left) {
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const uint32_t cw = 128u * c, cs = 8u * c, cx = (FP8 ? 256u : 128u) * c;
-  if (left >= 8) {
-    k.w[0] = load16(p.w, p.wo + cw + 32 * q);
-    k.w[1] = load16(p.w, p.wo + cw + 32 * q + 16);
-    k.sw = load_scales2(p.ws + (p.wso + cs + 2 * q));
-#pragma unroll
-    for (int g = 0; g < FM; ++g) {
-      if constexpr (FP8) {
-        // bytes [16 (q % 2), +16) of blocks 2 (q / 2) + s and 4 + 2 (q / 2) + s
-        const uint32_t o = p.xo[g] + cx + 64 * (q >> 1) + 16 * (q & 1);
-        k.x[g][0] = load16(p.x, o);
-        k.x[g][1] = load16(p.x, o + 128);
-        k.x[g][2] = load16(p.x, o + 32);
-        k.x[g][3] = load16(p.x, o + 160);
-      } else {
-        k.x[g][0] = load16(p.x, p.xo[g] + cx + 32 * q);
-        k.x[g][1] = load16(p.x, p.xo[g] + cx + 32 * q + 16);
-      }
-      k.sx[g] = load_scales2(p.xs + (p.xso[g] + cs + 2 * q));
-    }
-    return;
-  }
-  k.sw = 0;
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int b = 2 * q + s;
-    k.w[s] = b < left ? load16(p.w, p.wo + cw + 16 * b) : zero;
-    if (b < left) k.sw |= (uint32_t)p.ws[p.wso + cs + b] << (8 * s);
-  }
-#pragma unroll
-  for (int g = 0; g < FM; ++g) {
-    k.sx[g] = 0;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int b = 2 * q + s;
-      if (b < left) k.sx[g] |= (uint32_t)p.xs[p.xso[g] + cs + b] << (8 * s);
-      if constexpr (FP8) {
-        const int b0 = 2 * (q >> 1) + s, b1 = b0 + 4;
-        const uint32_t o = p.xo[g] + cx + 16 * (q & 1);
-        k.x[g][2 * s] = b0 < left ? load16(p.x, o + 32 * b0) : zero;
-        k.x[g][2 * s + 1] = b1 < left ? load16(p.x, o + 32 * b1) : zero;
-      } else {
-        k.x[g][s] = b < left ? load16(p.x, p.xo[g] + cx + 16 * b) : zero;
-      }
-    }
-  }
-}
-
-template <bool FP8, int FM>
-__device__ __forceinline__ void contract_chunk(f32x4_t (&acc)[FM], const MxChunk<FP8, FM> &k) {
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int g = 0; g < FM; ++g) {
-      const i32x8_t X = FP8 ? as_operand(k.x[g][2 * s], k.x[g][FP8 ? 2 * s + 1 : 0]) : as_operand(k.x[g][s], zero);
-      acc[g] = s == 0 ? mfma_mx<FP8, 0>(as_operand(k.w[0], zero), X, acc[g], k.sw, k.sx[g])
-                      : mfma_mx<FP8, 1>(as_operand(k.w[1], zero), X, acc[g], k.sw, k.sx[g]);
-    }
-}
-
-template <bool FP8, bool SWIGLU, int KSPLIT, int FM>
-__global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_direct_kernel(MxGemmArgs a) {
-  constexpr int WAVES = mxs_waves(KSPLIT);
-  constexpr int RG = WAVES / KSPLIT;              // fragments of 16 weight rows a workgroup
-  constexpr int FC = SWIGLU ? 8 : 16;              // output columns a fragment
-  __shared__ f32x4_t part[KSPLIT > 1 ? WAVES * FM * 64 : 1];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int q = lane >> 4, rl = lane & 15;
-  const int cols = SWIGLU ? a.N / 2 : a.N;
-  const int groups = (cols / FC + RG - 1) / RG;
-  const MxTile t = mx_find_tile<16 * FM>(a, blockIdx.x / groups, lane);
-  if (t.e < 0) return;
-  const int kw = wave % KSPLIT;
-  const int c0 = ((blockIdx.x % groups) * RG + wave / KSPLIT) * FC;
-  const bool live = c0 < cols;                     // (columns come in whole fragments)
-  const int nb = a.K / 32;
-  int n = live ? c0 + rl : 0;
-  if constexpr (SWIGLU) n = live ? c0 + (rl & 7) + (rl >> 3) * cols : 0;
-  MxLane<FM> p;
-  p.w = a.wc + (size_t)t.e * a.N * (a.K / 2);
-  p.ws = a.ws + (size_t)t.e * a.N * nb;
-  p.x = a.xc;
-  p.xs = a.xs;
-  p.wo = (uint32_t)n * (uint32_t)(a.K / 2);
-  p.wso = (uint32_t)n * (uint32_t)nb;
-#pragma unroll
-  for (int g = 0; g < FM; ++g) {
-    // rows that are not there read row 0; their results are not used
-    const int r = 16 * g + rl;
-    const uint32_t src = r < t.rows ? max(mx_src(a, t.row0 + r), 0) : 0;
-    p.xo[g] = src * (uint32_t)(a.K / (FP8 ? 1 : 2));
-    p.xso[g] = src * (uint32_t)nb;
-  }
-  f32x4_t acc[FM];
-#pragma unroll
-  for (int g = 0; g < FM; ++g) acc[g] = f32x4_t{0, 0, 0, 0};
-  const int chunks = (nb + 7) / 8;
-  MxChunk<FP8, FM> A, B;
-  int c = kw;
-  if (c < chunks) load_chunk(A, p, c, q, nb - 8 * c);
-  for (; c < chunks; c += 2 * KSPLIT) {
-    const int c1 = c + KSPLIT, c2 = c + 2 * KSPLIT;
-    if (c1 < chunks) load_chunk(B, p, c1, q, nb - 8 * c1);
-    contract_chunk(acc, A);
-    if (c1 >= chunks) break;
-    if (c2 < chunks) load_chunk(A, p, c2, q, nb - 8 * c2);
-    contract_chunk(acc, B);
-  }
-  mx_stream_finish<SWIGLU, KSPLIT, FM>(a, t, acc, part, c0, cols, wave, lane);
-}
-
-// ------------------------------------------------------------------ tiled kernel (K % 128 == 0)
+// ------------------------------------------------------------------ tiled kernel
 //
 // A workgroup computes BN weight rows x BM tokens.  Stages of 256
 // positions of both operands are copied to LDS, two in turn, and contracted
@@ -531,14 +428,18 @@ __device__ __forceinline__ f32x16_t mfma_mx32(i32x8_t w, i32x8_t x, f32x16_t c, 
                                                          (int)sw, SEL, (int)sx);
 }
 
-template <bool FP8, int BN, int BM>
+// Bytes of LDS for a row's scales of two stages: 16, or with them anywhere in
+// their first word (not WIDE) 20.
+constexpr int mxt_scale_bytes(bool wide) { return wide ? 16 : 20; }
+
+template <bool FP8, bool WIDE, int BN, int BM>
 struct MxTileLds {
   struct {
     uint8_t w[BN * 128];
     uint8_t x[BM * (FP8 ? 256 : 128)];
   } stage[2];
-  uint8_t scales[2][(BN + BM) * 16];               // of 512 positions (two stages)
-  uint8_t unused[(BN + BM) * 16];
+  uint8_t scales[2][(BN + BM) * mxt_scale_bytes(WIDE)];
+  uint8_t unused[(BN + BM) * mxt_scale_bytes(WIDE)];
 };
 
 // WN waves over the weight rows (FN fragments of 32 each), WM over the tokens
@@ -547,7 +448,8 @@ template <bool FP8, bool SWIGLU, bool WIDE, int WN, int WM, int FN, int FM>
 __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled_kernel(MxGemmArgs a) {
   constexpr int WAVES = WN * WM;
   constexpr int BN = WN * FN * 32, BM = WM * FM * 32;
-  using Lds = MxTileLds<FP8, BN, BM>;
+  using Lds = MxTileLds<FP8, WIDE, BN, BM>;
+  constexpr int SB = mxt_scale_bytes(WIDE);
   __shared__ __attribute__((aligned(1024))) Lds lds;
 
   const int lane = threadIdx.x & 63;
@@ -557,6 +459,7 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled_kernel(MxGemmArgs a)
   const int nt = (cols + BC - 1) / BC;
   const int K = a.K, nb = K / 32, stages = (K + 255) / 256;
   const int h = lane >> 5, rl = lane & 31;
+  const int wr0 = (wave % WN) * FN * 32 + rl, xr0 = (wave / WN) * FM * 32 + rl;
   constexpr int XB = FP8 ? 256 : 128;
   constexpr int CW = BN * 128 / 1024 / WAVES, CX = BM * XB / 1024 / WAVES, COPIES = CW + CX;
   constexpr int SG = (BN + BM) / 64;               // groups of 64 rows with scales
@@ -566,12 +469,13 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled_kernel(MxGemmArgs a)
   // One tile's place and this lane's source offsets of its copies: CW + CX of
   // 1 KB a wave, and the scales, 16 bytes a row for two stages, a wave those
   // of 64 rows (waves beyond the rows copy some again): rows on 16-byte
-  // boundaries (WIDE) in one copy, others in four of 4 bytes.
+  // boundaries (WIDE) in one copy, others in five of 4 bytes.
   struct Item {
     int e, c0;
     int dst[FM];                                   // output rows of this lane's tokens; -1: none
     bool zero[FM];                                 // ... that come out zero
-    uint32_t off[COPIES], soff[WIDE ? 1 : 4];
+    uint32_t off[COPIES], soff[WIDE ? 1 : 5];
+    uint32_t wsub[WIDE ? 1 : FN], xsub[WIDE ? 1 : FM];   // see scale_word
   };
   // The workgroups of one XCD (every eighth) take a run of tiles, token tiles
   // in fours and those before weight tiles, so that those running at a time
@@ -612,13 +516,20 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled_kernel(MxGemmArgs a)
       it.off[CW + i] =
           x_row(r) * (uint32_t)(K / (FP8 ? 1 : 2)) + 16 * (FP8 ? piece8(r, lane & 15) : piece4(r, lane & 7));
     }
-    const uint32_t so = (sr0 < BN ? w_row(sr0 + lane) : x_row(sr0 + lane - BN)) * (uint32_t)nb;
+    const uint32_t so = sr0 < BN ? w_row(sr0 + lane) * (uint32_t)nb + a.ws_off
+                                 : x_row(sr0 + lane - BN) * (uint32_t)nb + a.xs_off;
     if constexpr (WIDE) {
       it.soff[0] = so;
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)                  // rows 16 i.. of the wave's, four dwords each
-        it.soff[i] = (uint32_t)__shfl((int)so, 16 * i + (lane >> 2), 64) + 4 * (lane & 3);
+      for (int i = 0; i < 5; ++i) {                // word d % 5 of row d / 5 of the wave's
+        const int d = 64 * i + lane;
+        it.soff[i] = ((uint32_t)__shfl((int)so, d / 5, 64) & ~3u) + 4 * (d % 5);
+      }
+#pragma unroll
+      for (int f = 0; f < FN; ++f) it.wsub[f] = w_row(wr0 + 32 * f) * (uint32_t)nb + a.ws_off;
+#pragma unroll
+      for (int g = 0; g < FM; ++g) it.xsub[g] = x_row(xr0 + 32 * g) * (uint32_t)nb + a.xs_off;
     }
 #pragma unroll
     for (int g = 0; g < FM; ++g) {
@@ -627,11 +538,12 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled_kernel(MxGemmArgs a)
       it.zero[g] = r < rows && mx_src(a, t.row0 + r) < 0;
     }
   };
-  const i32x4_t xbuf = raw_buffer(a.xc, a.x_bytes), xsbuf = raw_buffer(a.xs, a.xs_bytes);
+  const i32x4_t xbuf = raw_buffer(a.xc, a.x_bytes);
+  const i32x4_t xsbuf = raw_buffer(a.xs, (a.xs_off + a.xs_bytes + 3) & ~3u);
   i32x4_t wbuf, wsbuf;
   auto point = [&](const Item &it) {
     wbuf = raw_buffer(a.wc + (size_t)it.e * a.N * (K / 2), (uint32_t)a.N * (uint32_t)(K / 2));
-    wsbuf = raw_buffer(a.ws + (size_t)it.e * a.N * nb, (uint32_t)a.N * (uint32_t)nb);
+    wsbuf = raw_buffer(a.ws + (size_t)it.e * a.N * nb, (a.ws_off + (uint32_t)a.N * (uint32_t)nb + 3) & ~3u);
   };
   // Copy i of stage s.  Stages that are not there are copied from buffers of
   // no bytes (zeros, into a buffer that nobody reads before its next copy), so
@@ -651,16 +563,15 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled_kernel(MxGemmArgs a)
   auto copy_scales = [&](int j, bool wanted) {
     i32x4_t buf = sr0 < BN ? wsbuf : xsbuf;
     buf[2] = wanted ? buf[2] : 0;
-    const uint32_t dst = wanted ? lds_offset(lds.scales[j & 1]) + sr0 * 16 : lds_offset(lds.unused) + sr0 * 16;
+    const uint32_t dst = (wanted ? lds_offset(lds.scales[j & 1]) : lds_offset(lds.unused)) + sr0 * SB;
     if constexpr (WIDE) {
       copy16_to_lds(dst, buf, cur.soff[0], (uint32_t)j * 16);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) copy4_to_lds(dst + i * 256, buf, cur.soff[i], (uint32_t)j * 16);
+      for (int i = 0; i < 5; ++i) copy4_to_lds(dst + i * 256, buf, cur.soff[i], (uint32_t)j * 16);
     }
   };
 
-  const int wr0 = (wave % WN) * FN * 32 + rl, xr0 = (wave / WN) * FM * 32 + rl;
   constexpr int XP = FP8 ? 2 : 1, READS = FN + FM * XP, MFMAS = FN * FM;
   struct Step {
     uint4 v[READS];                                // FN weight fragments, FM * XP token pieces
@@ -682,10 +593,14 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled_kernel(MxGemmArgs a)
   uint2 sw[FN], sx[FM];
   auto read_scales = [&](int s) {
     const uint8_t *sc = lds.scales[(s >> 1) & 1] + 8 * (s & 1);
+    auto get = [&](const uint8_t *p, uint32_t sub) {
+      if constexpr (WIDE) return *reinterpret_cast<const uint2 *>(p);
+      return make_uint2(scale_word(p, sub, false), scale_word(p + 4, sub, false));
+    };
 #pragma unroll
-    for (int f = 0; f < FN; ++f) sw[f] = *reinterpret_cast<const uint2 *>(sc + (wr0 + 32 * f) * 16);
+    for (int f = 0; f < FN; ++f) sw[f] = get(sc + (wr0 + 32 * f) * SB, cur.wsub[WIDE ? 0 : f]);
 #pragma unroll
-    for (int g = 0; g < FM; ++g) sx[g] = *reinterpret_cast<const uint2 *>(sc + (BN + xr0 + 32 * g) * 16);
+    for (int g = 0; g < FM; ++g) sx[g] = get(sc + (BN + xr0 + 32 * g) * SB, cur.xsub[WIDE ? 0 : g]);
   };
   f32x16_t acc[FN][FM];
   // MFMA i of step k
@@ -774,9 +689,37 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled_kernel(MxGemmArgs a)
       step(B, k3, A, k0, s + 1, k0, half, s + 2, mid, end);
       read_scales(s + 1);
     }
-    if (full < stages) {                           // the last 128 positions
-      step(A, k0, B, k1, full, k0, k0, 0, k0, end);
-      step(B, k1, A, none, 0, k0, k0, 0, k0, end);
+    if constexpr (!WIDE) {
+      // The last stage of K % 256 positions: blocks behind K are masked, their
+      // scales too (an 0xFF among them is not this row's).
+      const int left = nb - 8 * full;
+      auto rest = [&](auto k) {
+        constexpr int KS = decltype(k)::value;
+        if (2 * KS >= left) return;
+        Step T;
+#pragma unroll
+        for (int i = 0; i < READS; ++i) read(T, i, full, KS);
+        if (2 * KS + 1 == left) {
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < READS; ++i) {
+            // an E4M3 lane's second piece, any other's whole upper half
+            const bool second = FP8 && i >= FN ? (i - FN) % XP == 1 : h == 1;
+            if (second) T.v[i] = zero;
+          }
+          const uint32_t keep = h ? 0u : ~0u;
+#pragma unroll
+          for (int f = 0; f < FN; ++f) (KS < 2 ? sw[f].x : sw[f].y) &= keep;
+#pragma unroll
+          for (int g = 0; g < FM; ++g) (KS < 2 ? sx[g].x : sx[g].y) &= keep;
+        }
+#pragma unroll
+        for (int i = 0; i < MFMAS; ++i) mfma(T, i, k);
+      };
+      rest(k0);
+      rest(k1);
+      rest(k2);
+      rest(k3);
     }
     const int c0 = cur.c0;
     int dst[FM];
@@ -835,13 +778,12 @@ static long long mx_tiles(const MxGemmArgs &a, int bm) {
 
 template <bool FP8, bool SWIGLU, int KSPLIT, int FN, int FM>
 static void launch_stream(const MxGemmArgs &a, hipStream_t stream) {
-  const int frags = a.N / 16;
-  const int rg = mxs_waves(KSPLIT) / KSPLIT * (a.copies ? FN : 1);
+  const int frags = a.N / 16, rg = mxs_waves(KSPLIT) / KSPLIT * FN;
   const dim3 grid((unsigned)(mx_tiles(a, 16 * FM) * ((frags + rg - 1) / rg))), block(mxs_waves(KSPLIT) * 64);
-  if (a.copies)
-    hipLaunchKernelGGL((mx_stream_kernel<FP8, SWIGLU, KSPLIT, FN, FM>), grid, block, 0, stream, a);
+  if (a.aligned)
+    hipLaunchKernelGGL((mx_stream_kernel<FP8, SWIGLU, true, KSPLIT, FN, FM>), grid, block, 0, stream, a);
   else
-    hipLaunchKernelGGL((mx_direct_kernel<FP8, SWIGLU, KSPLIT, FM>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((mx_stream_kernel<FP8, SWIGLU, false, KSPLIT, FN, FM>), grid, block, 0, stream, a);
 }
 
 // How the weight rows (`frags` fragments of 16, counting every token tile
@@ -872,10 +814,10 @@ static void launch_tiled(const MxGemmArgs &a, hipStream_t stream) {
   constexpr int BM = WM * FM * 32, BC = WN * FN * 32 / (SWIGLU ? 2 : 1);
   const long long items = mx_tiles(a, BM) * (((SWIGLU ? a.N / 2 : a.N) + BC - 1) / BC);
   // as many workgroups as run at a time, each walking over its tiles
-  constexpr int PER_CU = sizeof(MxTileLds<FP8, WN * FN * 32, BM>) > 80 * 1024 ? 1 : 2;
+  constexpr int PER_CU = sizeof(MxTileLds<FP8, false, WN * FN * 32, BM>) > 80 * 1024 ? 1 : 2;
   const long long slots = (long long)device_cu_count() * PER_CU;
   const dim3 grid((unsigned)((std::min(items, slots) + 7) & ~7ll)), block(WN * WM * 64);
-  if (a.wide_scales)
+  if (a.wide)
     hipLaunchKernelGGL((mx_tiled_kernel<FP8, SWIGLU, true, WN, WM, FN, FM>), grid, block, 0, stream, a);
   else
     hipLaunchKernelGGL((mx_tiled_kernel<FP8, SWIGLU, false, WN, WM, FN, FM>), grid, block, 0, stream, a);
@@ -907,7 +849,7 @@ static moesq_status_t launch_mx(const MxGemmArgs &a, hipStream_t stream) {
     return (long long)experts * ((avg + bm - 1) / bm) * ((a.N + bn - 1) / bn);
   };
   const int cus = device_cu_count();
-  if (!a.copies || (long long)a.M <= 8ll * a.E || tiles(128, 64) < cus / 2) {
+  if ((long long)a.M <= 8ll * a.E || tiles(128, 64) < cus / 2) {
     if (avg <= 16) launch_stream_split<FP8, SWIGLU, 1>(a, stream);
     else launch_stream_split<FP8, SWIGLU, 2>(a, stream);
   } else if constexpr (FP8) {
@@ -967,11 +909,15 @@ extern "C" moesq_status_t moesq_mx_gemm(const moesq_mx_t *x, const int32_t *perm
     return fail(MOESQ_ERR_NULL, who + ": NULL codes, scales or output rows");
   if (((uintptr_t)x->codes | (uintptr_t)w->codes | (uintptr_t)y) & 15)
     return fail(MOESQ_ERR_ARG, who + ": codes and y must be 16-byte aligned");
-  MxGemmArgs a{x->codes, x->scales, w->codes, w->scales, perm, expert_offsets, y,
-               k,        M,         E,        N,         w->K, flat,
-               w->K % 128 == 0 && !(((uintptr_t)x->scales | (uintptr_t)w->scales) & 3),
-               w->K % 512 == 0 && !(((uintptr_t)x->scales | (uintptr_t)w->scales) & 15), (uint32_t)xb,
-               (uint32_t)((long long)x->rows * (x->K / 32))};
+  const uint32_t xs_off = (uintptr_t)x->scales & 3, ws_off = (uintptr_t)w->scales & 3;
+  MxGemmArgs a{x->codes, x->scales - xs_off, w->codes, w->scales - ws_off, perm, expert_offsets, y,
+               k,        M,                  E,        N,                  w->K, flat};
+  a.aligned = w->K % 128 == 0 && !(xs_off | ws_off);
+  a.wide = w->K % 512 == 0 && !(((uintptr_t)x->scales | (uintptr_t)w->scales) & 15);
+  a.xs_off = xs_off;
+  a.ws_off = ws_off;
+  a.x_bytes = (uint32_t)xb;
+  a.xs_bytes = (uint32_t)((long long)x->rows * (x->K / 32));
   if (epilogue == MOESQ_EPI_SWIGLU)
     return f8 ? launch_mx<true, true>(a, stream) : launch_mx<false, true>(a, stream);
   return f8 ? launch_mx<true, false>(a, stream) : launch_mx<false, false>(a, stream);

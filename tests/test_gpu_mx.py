@@ -185,7 +185,7 @@ def test_grouped(lib, fmt, counts):
 # on, 128 x 128 (FP4) and 256 x 128 (FP8) or 256 x 256 from 256 of their own.
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("T,N", [(250, 4112), (1000, 4128), (2047, 4096), (4090, 4128)])
-@pytest.mark.parametrize("K", [128, 256, 384, 512, 1152])
+@pytest.mark.parametrize("K", [32, 128, 160, 224, 256, 288, 384, 512, 736, 1152])
 def test_dense_tiles(lib, fmt, T, N, K):
     swiglu = N % 32 == 0 and K % 256 == 0
     print(f"[mx tiles] {fmt} T={T} N={N} K={K} swiglu={swiglu}", flush=True)
@@ -194,7 +194,8 @@ def test_dense_tiles(lib, fmt, T, N, K):
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("E,mean,N,K", [(64, 9, 256, 384), (40, 20, 528, 128), (70, 40, 544, 512), (40, 100, 1056, 256),
-                                        (33, 250, 2080, 384), (300, 11, 96, 256)])
+                                        (33, 250, 2080, 384), (300, 11, 96, 256),
+                                        (50, 90, 800, 96), (35, 210, 2048, 352)])
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_grouped_tiles(lib, fmt, E, mean, N, K, swiglu):
     """Uneven loads about a mean: experts without rows, with one, and with
@@ -325,6 +326,24 @@ def test_nan_scale_reaches_its_rows_only(lib, fmt):
     bad = torch.zeros(40, dtype=torch.bool, device="cuda")
     bad[[7, 39]] = True
     assert y[bad].isnan().all() and torch.equal(y[~bad], good[~bad])
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("T,N", [(9, 64), (40, 64), (300, 4096), (1100, 4096), (2050, 4096)])
+@pytest.mark.parametrize("K", [32, 96, 160, 352])
+def test_what_lies_behind_a_row(lib, fmt, T, N, K):
+    """Where K ends inside a stage the kernels read on into the next rows:
+    NaN scales and codes there do not reach a result, of tokens or weights."""
+    x = torch.randn(T, K, device="cuda").to(torch.bfloat16)
+    w = 0.02 * torch.randn(N, K, device="cuda")
+    good = lib.mx_gemm(lib.mx_quantize(x, FMT[fmt]), lib.mx_quantize(w))
+    assert good.isfinite().all()
+    x[1::2], w[1::2] = float("nan"), float("inf")
+    xq, wq = lib.mx_quantize(x, FMT[fmt]), lib.mx_quantize(w)
+    xq.codes[1::2], wq.codes[1::2] = 0x7f, 0x77
+    y = lib.mx_gemm(xq, wq)
+    assert torch.equal(y[::2, ::2], good[::2, ::2])
+    assert y[1::2].isnan().all() and y[:, 1::2].isnan().all()
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
