@@ -26,6 +26,7 @@ struct GateArgs {
   int32_t *ids;
   float *weights;
   int T, E;
+  uint32_t per_inv;   // e * per_inv >> 20 is e / (experts of a group), for e < 1024
   moesq_gate_t g;
 };
 
@@ -247,7 +248,6 @@ __device__ __forceinline__ bool gate_select(const GateArgs &a, const float (&l)[
   }
   bool sure = true;
   if (G > 1) {
-    const int per = E / G;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const int e = i * 64 + lane;
@@ -260,7 +260,7 @@ __device__ __forceinline__ bool gate_select(const GateArgs &a, const float (&l)[
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const int e = i * 64 + lane;
-      if (e < E && !((kept >> (e / per * lanes)) & 1)) key[i] = -INFINITY;
+      if (e < E && !((kept >> (((uint32_t)e * a.per_inv >> 20) * lanes)) & 1)) key[i] = -INFINITY;
     }
   }
   my_id = -1;
@@ -290,15 +290,18 @@ __device__ __forceinline__ bool gate_select(const GateArgs &a, const float (&l)[
       for (int i = 1; i < EPL; ++i) best = max(best, u[i]);
       best = wave_max_u32(best);
       if (best == 0) break;
-      // the lowest expert that holds it, found and cleared by lane masks
-      int e = -1;
+      // the lowest expert that holds it
+      uint64_t at = 0;
+      int base = 0;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const uint64_t at = e < 0 ? __ballot(u[i] == best) : 0;
-        const uint64_t first = at & (0 - at);
-        if (at) e = i * 64 + __builtin_ctzll(at);
-        u[i] = (first >> lane) & 1 ? 0u : u[i];
+      for (int i = EPL - 1; i >= 0; --i) {
+        const uint64_t here = __ballot(u[i] == best);
+        at = here ? here : at;
+        base = here ? i * 64 : base;
       }
+      const int e = base + __builtin_ctzll(at);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) u[i] = lane == e - i * 64 ? 0u : u[i];
       if (r == k) {
         left = best;
         break;
@@ -425,7 +428,8 @@ extern "C" moesq_status_t moesq_gate_topk(const void *logits, int32_t dtype, int
   if (!logits || !topk_ids || !topk_weights) return fail(MOESQ_ERR_NULL, who + ": NULL buffer");
   if ((uintptr_t)logits & (dtype == MOESQ_F32 ? 3 : 1))
     return fail(MOESQ_ERR_ARG, who + ": logits not aligned to their type");
-  GateArgs a{logits, bias, n_rows, topk_ids, topk_weights, T, E, *gate};
+  // floor(2^20 / per) + 1 is off by less than per, and e * per < 2^20
+  GateArgs a{logits, bias, n_rows, topk_ids, topk_weights, T, E, (1u << 20) / (uint32_t)(E / gate->n_group) + 1, *gate};
   if (dtype == MOESQ_F32) launch_gate<false>(a, stream);
   else launch_gate<true>(a, stream);
   return launch_status("moesq_gate_topk");
