@@ -194,7 +194,8 @@ def test_mx_gemm_rejects(m):
     assert call(w=dict(K=48), x=dict(K=48)) == m.ERR_SHAPE
     assert call(x=dict(K=64)) == m.ERR_SHAPE
     assert call(M=-1) == m.ERR_SHAPE and call(M=5) == m.ERR_SHAPE
-    assert call(perm=0x10, T=1 << 28, k=5, M=5 << 28, x=dict(rows=1 << 28, K=32), w=dict(K=32)) == m.ERR_SHAPE
+    wide = dict(perm=0x10, T=(1 << 28) - 1, k=5, M=5 * ((1 << 28) - 1))
+    assert call(x=dict(rows=wide["T"], K=32, format=1), w=dict(K=32), **wide) == m.ERR_SHAPE
     assert call(perm=0x10, T=2, k=1) == m.ERR_SHAPE               # M != T*k
     assert call(perm=0x10, T=4, k=0) == m.ERR_SHAPE
     assert call(perm=0x10, T=2, k=2) == m.ERR_SHAPE               # x has M rows, not T
