@@ -854,19 +854,25 @@ static void launch_tiled(const MxGemmArgs &a, hipStream_t stream) {
 // streaming kernel; then the largest tile that the rows fill and that gives
 // every CU one.  Measured, us:
 //   FP4, 128 experts of 1536 x 2048     stream  128x64  128x128  256x256
-//      8 rows an expert                   30.8    32.6     28.8
-//     16                                  39.9    32.1     36.4
-//     64                                 103.2    53.0     50.2     59.8
-//    128                                 181.1    80.0     69.3     77.5
-//    256 (uneven loads)                            151      127      120
+//      8 rows an expert                   35.7    38.0     40.3     44.7
+//     16                                  49.7    38.3     40.8     45.6
+//     64                                  95.1    51.9     45.6     49.3
+//    128                                 152.2    75.0     63.4     58.1
+//    128 (uneven loads)                            80.3     68.9     75.6
+//    192                                 211.5   102.0     79.8     66.6
+//    256 (uneven loads)                           137.7    107.7     97.5
 //   FP8, 48 experts of 4096 x 7168      stream  128x64  256x128
-//     21 rows an expert                  202.3   147.6    153.7
-//     85                                 542.7   254.8    217.7
+//      8 rows an expert                  161.3   151.5    157.2
+//     21                                 231.5   158.5    158.8
+//     48                                 385.1   174.0    165.4
+//     85                                 546.1   254.4    185.2
+//    170 (uneven loads)                          429.7    317.2
 //   FP4, dense, 4096 x 7168             stream  128x64  128x128  256x256
-//     64 rows                              7.7    14.7     18.3     39.5
-//    1024                                         29.7     27.8     43.7
-//    2048                                101.0    52.4     40.2     44.3
-//    4096                                191.0   100.1     74.2     61.1
+//     64 rows                              7.5    16.3     18.2     28.1
+//    256                                  17.3    18.0     20.5     40.5
+//   1024                                  56.2    30.4     29.9     44.9
+//   2048                                  99.7    53.2     40.8     46.6
+//   4096                                          100.5    74.7     61.7
 template <bool FP8, bool SWIGLU>
 static moesq_status_t launch_mx(const MxGemmArgs &a, hipStream_t stream) {
   const int experts = std::min(a.E, a.M), avg = (a.M + experts - 1) / experts;
@@ -878,10 +884,10 @@ static moesq_status_t launch_mx(const MxGemmArgs &a, hipStream_t stream) {
     if (avg <= 16) launch_stream_split<FP8, SWIGLU, 1>(a, stream);
     else launch_stream_split<FP8, SWIGLU, 2>(a, stream);
   } else if constexpr (FP8) {
-    if (avg > 80 && tiles(256, 128) >= cus) launch_tiled<true, SWIGLU, 4, 2, 2, 2>(a, stream);
+    if (avg > 32 && tiles(256, 128) >= cus) launch_tiled<true, SWIGLU, 4, 2, 2, 2>(a, stream);
     else launch_tiled<true, SWIGLU, 2, 2, 2, 1>(a, stream);
   } else {
-    if (avg > 192 && tiles(256, 256) >= cus) launch_tiled<false, SWIGLU, 2, 4, 4, 2>(a, stream);
+    if (avg > 160 && tiles(256, 256) >= cus) launch_tiled<false, SWIGLU, 2, 4, 4, 2>(a, stream);
     else if (avg > 32 && tiles(128, 128) >= cus) launch_tiled<false, SWIGLU, 2, 2, 2, 2>(a, stream);
     else launch_tiled<false, SWIGLU, 2, 2, 2, 1>(a, stream);
   }
