@@ -9,15 +9,18 @@
 // below an fp32 step, so r is the correctly rounded fp32 value but for rows
 // next to a rounding border, whatever the order of the sum: the quantized
 // rows, whose scales turn on single bits of y, then do not depend on it.
-// (64-bit multiply-adds run at the fp32 rate on this chip; the kernel is a
-// stream, 5 to 9 bytes an element, bound by HBM.)
+// (64-bit multiply-adds run at the fp32 rate on this chip.)
+//
+// Bound by HBM: x and residual in, their sum out, and the rows, 6.5 to 9 bytes
+// an element.  Measured: 96 us for 8192 x 7168 with a residual and MXFP8 rows
+// (530 MB: 5.5 TB/s; a large copy reaches 5.0), 5.1 us for 64 x 7168, 2.8 us
+// for one row of 2048 (both the latency of a launch, a load, a reduction and
+// a store).
+#include "dpp.hpp"
 #include "encode.hpp"
 #include "mx.hpp"
 
 namespace moesq {
-
-constexpr int RN_THREADS = 256;
-constexpr int RN_WAVES = RN_THREADS / 64;
 
 struct RmsNormArgs {
   const uint4 *x, *residual, *weight;
@@ -28,26 +31,28 @@ struct RmsNormArgs {
   double eps;
 };
 
-// Sum of v over the workgroup, in every thread.
+// Sum and maximum of v over the WAVES of the workgroup, in every thread.
+template <int WAVES>
 __device__ __forceinline__ double block_sum(double v, double *part) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+  v = wave_sum(v);
+  if (WAVES == 1) return v;
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
   double t = 0.0;
 #pragma unroll
-  for (int w = 0; w < RN_WAVES; ++w) t += part[w];
+  for (int w = 0; w < WAVES; ++w) t += part[w];
   return t;
 }
 
+template <int WAVES>
 __device__ __forceinline__ float block_max(float v, float *part) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  v = wave_max(v);
+  if (WAVES == 1) return v;
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
   float t = 0.0f;
 #pragma unroll
-  for (int w = 0; w < RN_WAVES; ++w) t = fmaxf(t, part[w]);
+  for (int w = 0; w < WAVES; ++w) t = fmaxf(t, part[w]);
   return t;
 }
 
@@ -74,43 +79,53 @@ __device__ __forceinline__ void nvfp4_store_unit(const float (&v)[8], float g, s
   if ((unit & 3) == 0) scales[unit >> 2] = (uint8_t)sc;
 }
 
-// NU units a thread (K up to 2048 * NU); NU == 0: rows of any length, read a
-// second time for the scaling (s from residual_out when there is one).
-template <int NU, int ROWS>
-__global__ __launch_bounds__(RN_THREADS) void rmsnorm_kernel(RmsNormArgs a) {
-  __shared__ double psum[RN_WAVES];
-  __shared__ float pmax[RN_WAVES];
+// NU units a thread (K up to 8 * THREADS * NU); NU == 0: rows of any length,
+// read a second time for the scaling (s from residual_out when there is one).
+template <int THREADS, int NU, int ROWS>
+__global__ __launch_bounds__(THREADS) void rmsnorm_kernel(RmsNormArgs a) {
+  constexpr int WAVES = THREADS / 64;
+  __shared__ double psum[WAVES];
+  __shared__ float pmax[WAVES];
   constexpr int N = NU ? NU : 1, UNROLL = N;
   const int tid = threadIdx.x, units = a.units;
   const size_t base = (size_t)blockIdx.x * units;
-  const int iters = NU ? NU : (units + RN_THREADS - 1) / RN_THREADS;
+  const int iters = NU ? NU : (units + THREADS - 1) / THREADS;
 
-  uint4 s[N];
+  // All loads first: behind a store to residual_out, which may be x's or
+  // residual's buffer, the next unit's would wait (64 x 7168: 6.5 us so, 5.7 this way).
+  // Threads without a unit read the last one and count it as zeros.
+  uint4 s[N], d[N], wt[N];
+  auto load = [&](int i, int u) {
+    u = min(u, units - 1);
+    s[i] = a.x[base + u];
+    if (a.residual) d[i] = a.residual[base + u];
+  };
+  if constexpr (NU > 0) {
+#pragma unroll
+    for (int i = 0; i < NU; ++i) load(i, i * THREADS + tid);
+#pragma unroll
+    for (int i = 0; i < NU; ++i) wt[i] = a.weight[min(i * THREADS + tid, units - 1)];
+  }
   double ss = 0.0;
 #pragma unroll UNROLL
   for (int i = 0; i < iters; ++i) {
-    const int u = i * RN_THREADS + tid;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (u < units) {
-      v = a.x[base + u];
-      if (a.residual) {
-        const uint4 d = a.residual[base + u];
-        v = make_uint4(add_bf16x2(v.x, d.x), add_bf16x2(v.y, d.y), add_bf16x2(v.z, d.z),
-                       add_bf16x2(v.w, d.w));
-        a.residual_out[base + u] = v;
-      }
+    const int u = i * THREADS + tid, at = NU ? i : 0;
+    if constexpr (NU == 0) load(0, u);
+    if (a.residual) {
+      s[at] = make_uint4(add_bf16x2(s[at].x, d[at].x), add_bf16x2(s[at].y, d[at].y), add_bf16x2(s[at].z, d[at].z),
+                         add_bf16x2(s[at].w, d[at].w));
+      if (u < units) a.residual_out[base + u] = s[at];
     }
     float f[8];
-    unpack_bf16x8(v, f);
+    unpack_bf16x8(u < units ? s[at] : make_uint4(0, 0, 0, 0), f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = fma((double)f[j], (double)f[j], ss);
-    if constexpr (NU > 0) s[i] = v;
   }
-  const float r = (float)(1.0 / sqrt(block_sum(ss, psum) / (8.0 * units) + a.eps));
+  const float r = (float)(1.0 / sqrt(block_sum<WAVES>(ss, psum) / (8.0 * units) + a.eps));
 
   auto norm = [&](int i, int u) {
     const uint4 v = NU ? s[NU ? i : 0] : (a.residual ? a.residual_out[base + u] : a.x[base + u]);
-    const uint4 w = a.weight[u];
+    const uint4 w = NU ? wt[NU ? i : 0] : a.weight[u];
     return make_uint4(norm_bf16x2(v.x, w.x, r), norm_bf16x2(v.y, w.y, r), norm_bf16x2(v.z, w.z, r),
                       norm_bf16x2(v.w, w.w, r));
   };
@@ -120,7 +135,7 @@ __global__ __launch_bounds__(RN_THREADS) void rmsnorm_kernel(RmsNormArgs a) {
     float m = 0.0f;
 #pragma unroll UNROLL
     for (int i = 0; i < iters; ++i) {
-      const int u = i * RN_THREADS + tid;
+      const int u = i * THREADS + tid;
       if (u < units) {
         float f[8];
         const uint4 y = norm(i, u);
@@ -129,14 +144,14 @@ __global__ __launch_bounds__(RN_THREADS) void rmsnorm_kernel(RmsNormArgs a) {
         for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
       }
     }
-    const float amax = block_max(m, pmax);
+    const float amax = block_max<WAVES>(m, pmax);
     g = amax > 0.0f ? __fdiv_rn(amax, 2688.0f) : 1.0f;
     if (tid == 0) a.row_scale[blockIdx.x] = g;
   }
 
 #pragma unroll UNROLL
   for (int i = 0; i < iters; ++i) {
-    const int u = i * RN_THREADS + tid;
+    const int u = i * THREADS + tid;
     // a block's four units are four neighbouring lanes and units % 4 == 0
     // with quantized rows, so they leave together
     if (u >= units) break;
@@ -153,21 +168,21 @@ __global__ __launch_bounds__(RN_THREADS) void rmsnorm_kernel(RmsNormArgs a) {
   }
 }
 
-template <int NU>
+template <int THREADS, int NU>
 static void launch_rows(const RmsNormArgs &a, int T, int rows_format, hipStream_t stream) {
-  const dim3 grid((unsigned)T), block(RN_THREADS);
+  const dim3 grid((unsigned)T), block(THREADS);
   switch (rows_format) {
     case MOESQ_ROWS_MXFP4:
-      hipLaunchKernelGGL((rmsnorm_kernel<NU, MOESQ_ROWS_MXFP4>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((rmsnorm_kernel<THREADS, NU, MOESQ_ROWS_MXFP4>), grid, block, 0, stream, a);
       break;
     case MOESQ_ROWS_MXFP8:
-      hipLaunchKernelGGL((rmsnorm_kernel<NU, MOESQ_ROWS_MXFP8>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((rmsnorm_kernel<THREADS, NU, MOESQ_ROWS_MXFP8>), grid, block, 0, stream, a);
       break;
     case MOESQ_ROWS_NVFP4:
-      hipLaunchKernelGGL((rmsnorm_kernel<NU, MOESQ_ROWS_NVFP4>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((rmsnorm_kernel<THREADS, NU, MOESQ_ROWS_NVFP4>), grid, block, 0, stream, a);
       break;
     default:
-      hipLaunchKernelGGL((rmsnorm_kernel<NU, MOESQ_ROWS_NONE>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((rmsnorm_kernel<THREADS, NU, MOESQ_ROWS_NONE>), grid, block, 0, stream, a);
   }
 }
 
@@ -213,10 +228,22 @@ extern "C" moesq_status_t moesq_rmsnorm(const uint16_t *x, const uint16_t *resid
   a.row_scale = row_scale;
   a.units = K / 8;
   a.eps = eps;
-  if (K <= 2048) launch_rows<1>(a, T, rows_format, stream);
-  else if (K <= 4096) launch_rows<2>(a, T, rows_format, stream);
-  else if (K <= 8192) launch_rows<4>(a, T, rows_format, stream);
-  else if (K <= 16384) launch_rows<8>(a, T, rows_format, stream);
-  else launch_rows<0>(a, T, rows_format, stream);
+  // Threads a row: as few as hold it in one or two units each (a long row, in
+  // four).  Measured, us, threads / units a thread:
+  //   65536 x 256      64/1 29.3  64/2 38.6   256/1 77.9
+  //   4096 x 768       64/2 5.6   128/1 5.6   256/1 6.8
+  //   64 x 2048        64/4 5.1   128/2 4.1   256/1 3.5   512/1 3.6
+  //   8192 x 4096     128/4 38.4  256/2 37.8  512/1 39.8
+  //   64 x 7168       256/4 5.7   512/2 5.1  1024/1 5.2
+  //   8192 x 7168     256/4 103   512/2 95.7 1024/1 97.4
+  //   1024 x 16384    256/8 26.7  512/4 25.2 1024/2 26.4
+  //   64 x 20480      256/any 14.3  1024/any 9.4
+  if (K <= 512) launch_rows<64, 1>(a, T, rows_format, stream);
+  else if (K <= 1024) launch_rows<128, 1>(a, T, rows_format, stream);
+  else if (K <= 2048) launch_rows<256, 1>(a, T, rows_format, stream);
+  else if (K <= 4096) launch_rows<256, 2>(a, T, rows_format, stream);
+  else if (K <= 8192) launch_rows<512, 2>(a, T, rows_format, stream);
+  else if (K <= 16384) launch_rows<512, 4>(a, T, rows_format, stream);
+  else launch_rows<1024, 0>(a, T, rows_format, stream);
   return launch_status("moesq_rmsnorm");
 }

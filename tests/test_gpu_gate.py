@@ -108,6 +108,19 @@ def test_masked_infinite_and_nan(lib):
     run(lib, l, 8, bias=np.full(48, -np.inf), score="softmax")
 
 
+def test_group_sums_below_fp32_range(lib):
+    """TOP2 group scores of finite biases, the sums of which fp32 does not hold."""
+    l = np.random.default_rng(5).standard_normal((6, 12)).astype(np.float32)
+    bias = np.repeat(np.float32([-3e38, -2e38, -2.5e38]), 4)
+    for kept in (1, 2):
+        ids, _ = run(lib, l, 3, bias=bias, score="sigmoid", n_group=3, topk_group=kept, group_score="top2")
+        assert (ids.reshape(6, 3) // 4 == 1).all()
+    bias[5:8] = np.finfo(np.float32).min
+    run(lib, l, 6, bias=bias, score="softmax", n_group=3, topk_group=2, group_score="top2")
+    run(lib, l, 6, bias=np.full(12, np.finfo(np.float32).max), score="sigmoid", n_group=3, topk_group=2,
+        group_score="top2")
+
+
 @pytest.mark.parametrize("n_rows", [-1, 0, 1, 5, 9, 100])
 def test_padded_rows(lib, n_rows):
     rng = np.random.default_rng(5)

@@ -11,7 +11,7 @@ import oracle
 
 pytestmark = pytest.mark.gpu
 
-SHAPES = [(1, 8), (1, 32), (3, 24), (2, 96), (5, 2048), (1, 2056), (17, 4096), (4, 4128), (64, 7168),
+SHAPES = [(1, 8), (1, 32), (3, 24), (2, 96), (5, 512), (7, 544), (3, 1024), (2, 1056), (5, 2048), (1, 2056), (17, 4096), (4, 4128), (64, 7168),
           (2, 8192), (3, 8200), (2, 16384), (2, 16416), (3, 20480)]
 
 
