@@ -237,6 +237,11 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t *p, uint32_t sub, b
 // for the final sum: KSPLIT waves of a workgroup share their rows, each with its
 // own stages, and add their sums in LDS in a fixed order.
 //
+// Measured: 16 rows of FP8 x 4096 x 7168 5.3 us (15.8 MB, 2.5 us of it a
+// launch); 16 tokens on 8 of 128 experts of 1536 x 2048 FP4, some 70 of them
+// with rows, 15.3 us; 1024 rows on those, all of them with rows, 36 us (214 MB
+// of weights: 6.0 TB/s, part of it from the last-level cache).
+//
 // SwiGLU: rows 0-7 of a fragment are gate rows, 8-15 the up rows of the same
 // eight columns.
 
@@ -421,6 +426,15 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGem
 // barrier of a stage is in the middle of its last step, behind the stage's
 // reads: it hands the stage's buffer to the copies of the stage after the
 // next and says that the next has landed.
+//
+// Measured: 8192 x 4096 x 7168 FP4 118 us, 4.1 PFLOP/s; its MFMAs alone,
+// without copies and reads of LDS, take 100 us on the same codes: the clock
+// falls to 2.0 GHz, and on codes of zero, with everything in place, the whole
+// kernel takes 96.  FP8 202 us (162 on zeros).  On 48 experts with uneven
+// loads, 8192 rows of FP8 in all, 320 to 350 us: a quarter more MFMAs than
+// dense for tiles that are partly empty, six rounds of tiles where five would
+// hold them, and 704 MB of weights from HBM.  A prefetch of the weights' lines
+// to the L2 two to six stages ahead made this 6 to 14 % slower.
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
