@@ -12,6 +12,7 @@ importing this module without it raises ImportError.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -258,7 +259,8 @@ class Gate:
 class Mx:
     """Device tensors of microscaled rows: scales uint8 [..., K/32] (E8M0) and
     codes uint8 [..., K/2] (ROWS_MXFP4) or [..., K] (ROWS_MXFP8).  Activations
-    are [rows, ...]; MXFP4 weights [E, N, ...], or [N, ...] for one matrix."""
+    are [rows, ...]; MXFP4 weights [E, N, ...], or [N, ...] for one matrix.
+    Their contents may change, the tensors stay the ones it was made with."""
 
     def __init__(self, codes, scales, format: int):
         if format not in (ROWS_MXFP4, ROWS_MXFP8):
@@ -279,6 +281,7 @@ class Mx:
     def _described(self):
         """(descriptor, device), checked and made at the first use."""
         if self._desc is None:
+            _count(self.rows, "rows")
             dev, (codes, scales) = _pointers(
                 (self.codes, torch.uint8, self.rows * self.K // (2 if self.format == ROWS_MXFP4 else 1), "codes"),
                 (self.scales, torch.uint8, self.rows * self.K // 32, "scales"))
@@ -333,6 +336,21 @@ def _pointers(*specs):
     if dev is not None and dev < 0:
         raise ValueError("the tensors must be on the GPU")
     return dev, ptrs
+
+
+def _count(n, name):
+    """The library counts rows in 32 bits."""
+    if n >= 1 << 31:
+        raise ValueError(f"{name} must be below 2^31, got {n}")
+
+
+_as_is = contextlib.nullcontext()
+
+
+def _allocating(stream):
+    """Memory for a call's results comes from the stream that writes them: a
+    block of the current stream may still be in use there."""
+    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else _as_is
 
 
 def _launch(dev, stream, call, *args):
@@ -507,6 +525,7 @@ def _dtype(t, name):
 def moesq_gate_topk(logits, T: int, E: int, bias, gate: Gate, n_rows, topk_ids, topk_weights,
                     stream=None):
     dtype, n = _dtype(logits, "logits"), T * gate.k
+    _count(T, "T")
     f32, i32 = torch.float32, torch.int32
     dev, (l, b, r, i, w) = _pointers(
         (logits, logits.dtype, T * E, "logits"), (bias, f32, E, "bias"), (n_rows, i32, 1, "n_rows"),
@@ -532,6 +551,7 @@ def _row_elements(format, rows, K):
 
 def moesq_mx_quantize(x, rows: int, K: int, format: int, codes, scales, stream=None):
     dtype, u8 = _dtype(x, "x"), torch.uint8
+    _count(rows, "rows")
     dev, (xp, c, s) = _pointers(
         (x, x.dtype, rows * K, "x"), (codes, u8, _row_elements(format, rows, K), "codes"),
         (scales, u8, rows * K // 32, "scales"))
@@ -547,6 +567,7 @@ def moesq_mx_decode(x: Mx, out, stream=None):
 def moesq_rmsnorm(x, residual, weight, T: int, K: int, eps: float, residual_out, y,
                   rows_format: int = ROWS_NONE, codes=None, scales=None, row_scale=None, stream=None):
     bf, u8, n = torch.bfloat16, torch.uint8, T * K
+    _count(T, "T")
     if rows_format == ROWS_NONE:
         codes = scales = row_scale = None
     dev, (xp, rp, wp, ro, yp, c, s, g) = _pointers(
@@ -567,6 +588,7 @@ def moesq_mx_gemm(x: Mx, perm, T: int, k: int, expert_offsets, M: int, w: Mx, E:
     if x.rows != (T if perm is not None else M):
         raise ValueError(f"activations have {x.rows} rows, need {T if perm is not None else M}")
     i32 = torch.int32
+    _count(M, "M")
     dev, (p, off, yp) = _pointers(
         (perm, i32, M, "perm"), (expert_offsets, i32, E + 1, "expert_offsets"),
         (y, torch.bfloat16, M * (N // 2 if (epilogue & ~OUT_FLAT) == EPI_SWIGLU else N), "y"))
@@ -746,8 +768,9 @@ def gate_topk(logits, gate: Gate, bias=None, n_rows=None, stream=None):
     if logits.dim() != 2:
         raise ValueError(f"logits must be [T, E], got {tuple(logits.shape)}")
     T, E = logits.shape
-    ids = torch.empty(T * gate.k, dtype=torch.int32, device=logits.device)
-    weights = torch.empty(T * gate.k, dtype=torch.float32, device=logits.device)
+    with _allocating(stream):
+        ids = torch.empty(T * gate.k, dtype=torch.int32, device=logits.device)
+        weights = torch.empty(T * gate.k, dtype=torch.float32, device=logits.device)
     moesq_gate_topk(logits, T, E, bias, gate, n_rows, ids, weights, stream)
     return ids, weights
 
@@ -760,14 +783,16 @@ def mx_quantize(x, format: int = ROWS_MXFP4, stream=None) -> Mx:
     _dtype(x, "x")
     if format not in (ROWS_MXFP4, ROWS_MXFP8) or K % 32:
         raise ValueError(f"need an MX format and K % 32 == 0, got format {format}, K = {K}")
-    q = Mx.empty(x.shape[:-1], K, format, device=x.device)
+    with _allocating(stream):
+        q = Mx.empty(x.shape[:-1], K, format, device=x.device)
     moesq_mx_quantize(x, q.rows, K, format, q.codes, q.scales, stream)
     return q
 
 
 def mx_decode(x: Mx, stream=None):
     """The bfloat16 values that MX rows stand for, [..., K]."""
-    out = torch.empty(*x.shape, x.K, dtype=torch.bfloat16, device=x.codes.device)
+    with _allocating(stream):
+        out = torch.empty(*x.shape, x.K, dtype=torch.bfloat16, device=x.codes.device)
     moesq_mx_decode(x, out, stream)
     return out
 
@@ -782,14 +807,15 @@ def rmsnorm(x, weight, eps: float = 1e-6, residual=None, y: bool = True, rows: i
         raise ValueError(f"x must be [T, K], got {tuple(x.shape)}")
     T, K = x.shape
     rows = rows or ROWS_NONE
-    out = torch.empty_like(x) if y else None
-    res = torch.empty_like(x) if residual is not None else None
     q, codes, scales, row_scale = None, None, None, None
-    if rows in (ROWS_MXFP4, ROWS_MXFP8):
-        q = Mx.empty((T,), K, rows, device=x.device)
-    elif rows == ROWS_NVFP4:
-        q = Act4.empty(T, K, device=x.device)
-        row_scale = q.row_scale
+    with _allocating(stream):
+        out = torch.empty_like(x) if y else None
+        res = torch.empty_like(x) if residual is not None else None
+        if rows in (ROWS_MXFP4, ROWS_MXFP8):
+            q = Mx.empty((T,), K, rows, device=x.device)
+        elif rows == ROWS_NVFP4:
+            q = Act4.empty(T, K, device=x.device)
+            row_scale = q.row_scale
     if q is not None:
         codes, scales = q.codes, q.scales
     moesq_rmsnorm(x, residual, weight, T, K, eps, res, out, rows, codes, scales, row_scale, stream)
@@ -807,7 +833,8 @@ def mx_gemm(x: Mx, w: Mx, expert_offsets=None, perm=None, k: int = 1, epilogue: 
     M = x.rows * k if perm is not None else x.rows
     n_out = N // 2 if (epilogue & ~OUT_FLAT) == EPI_SWIGLU else N
     if out is None:
-        out = torch.empty(M, n_out, dtype=torch.bfloat16, device=x.codes.device)
+        with _allocating(stream):
+            out = torch.empty(M, n_out, dtype=torch.bfloat16, device=x.codes.device)
     elif tuple(out.shape) != (M, n_out):
         raise ValueError(f"out must be [{M}, {n_out}], got {tuple(out.shape)}")
     moesq_mx_gemm(x, perm, x.rows if perm is not None else 0, k, expert_offsets, M, w, E, epilogue, out,

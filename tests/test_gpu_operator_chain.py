@@ -151,3 +151,29 @@ def test_stream_argument(lib):
     v = lib.mx_decode(q, stream=s)
     torch.cuda.synchronize()
     assert (y == 1).all() and (v == 1).all()
+
+
+def test_results_of_a_side_stream_spare_pending_reads(lib):
+    """A block that the current stream has freed but still reads must not become
+    the result of a call on another stream."""
+    s = torch.cuda.Stream()
+    x = torch.randn(4096, 2048, device="cuda").to(torch.bfloat16)
+    w = torch.ones(2048, device="cuda", dtype=torch.bfloat16)
+    logits = torch.randn(4096, 128, device="cuda")
+    mxw = lib.mx_quantize(torch.randn(2048, 2048, device="cuda"))
+    mxx = lib.mx_quantize(x)
+    gate = lib.Gate(8)
+    calls = (lambda: lib.mx_quantize(x, stream=s), lambda: lib.mx_decode(mxx, stream=s),
+             lambda: lib.rmsnorm(x, w, rows=lib.ROWS_MXFP8, stream=s),
+             lambda: lib.gate_topk(logits, gate, stream=s), lambda: lib.mx_gemm(mxx, mxw, stream=s))
+    torch.cuda.synchronize()
+    for i, call in enumerate(calls):
+        blocks = [torch.full((n,), 7, dtype=torch.uint8, device="cuda")
+                  for n in (4096 * 4096, 4096 * 2048, 4096 * 1024, 4096 * 64, 4096 * 32) for _ in range(2)]
+        torch.cuda._sleep(20_000_000)
+        copies = [b.clone() for b in blocks]
+        del blocks
+        kept = call()
+        torch.cuda.synchronize()
+        assert all(bool((c == 7).all()) for c in copies), i
+        del kept, copies

@@ -252,3 +252,18 @@ def test_binding_rejects_mismatched_sizes(m):
         m.gate_topk(z(4, 8, dt=torch.float16), g)
     with pytest.raises(TypeError):
         m.mx_quantize(z(2, 64, dt=torch.float64))
+
+
+def test_binding_rejects_counts_beyond_32_bits(m):
+    """A wrapped count would leave rows out without an error."""
+    z = lambda *s, dt=torch.uint8: torch.zeros(*s, dtype=dt)        # noqa: E731
+    bf, big = torch.bfloat16, (1 << 32) + 4
+    q = m.Mx.empty((1,), 32, m.ROWS_MXFP4, device="cpu")
+    many = m.Mx.__new__(m.Mx)._set(q.codes, q.scales, m.ROWS_MXFP4, (big,), 32)
+    for case in (lambda: m.moesq_gate_topk(z(4, dt=bf), big, 1, None, m.Gate(1), None, None, None),
+                 lambda: m.moesq_mx_quantize(z(32, dt=bf), big, 32, 1, None, None),
+                 lambda: m.moesq_rmsnorm(z(8, dt=bf), None, z(8, dt=bf), big, 8, 1e-6, None, z(8, dt=bf)),
+                 lambda: m.moesq_mx_gemm(q, z(4, dt=torch.int32), 1, big, z(2, dt=torch.int32), big, q, 1, 0, None),
+                 lambda: many._described()):
+        with pytest.raises(ValueError, match="2\\^31"):
+            case()
