@@ -15,11 +15,11 @@
 // at once (8192 rows are 32 waves a CU), and a round of the selection is a
 // maximum in a lane, six lane permutations and a ballot.  Bound by these
 // rounds' instructions, not by the scores (13 MB of 8192 x 384, 2.6 us of
-// HBM).  Measured, k = 8: 11.1 us for 8192 x 384 by softmax, 16.7 by sigmoid
-// with a bias, 19.6 to 23.3 with 4 of 8 groups too (up to 5 of them the one
-// row in 64 bits that ends last; that code as loops over LDS, a third of the
-// instructions to fetch, took as long); 5.4 for 4096 x 128; 4.3 for 16 x 128,
-// of which a launch is 2.5.
+// HBM): about 1000 vector instructions a row, 15 us of them.  Measured, k = 8:
+// 11.0 us for 8192 x 384 by softmax, 15.6 by sigmoid with a bias, 20.4 with 4
+// of 8 groups too (up to 5 of them the one row in 64 bits that ends last; that
+// code as loops over LDS, a third of the instructions to fetch, took as long);
+// 5.4 for 4096 x 128; 4.3 for 16 x 128, of which a launch is 2.5.
 #include <cmath>
 
 #include "dpp.hpp"
@@ -128,13 +128,22 @@ __device__ __forceinline__ uint64_t gate_groups(const GateArgs &a, const F *sk, 
   if (lanes > 16) merge(__shfl_xor(m1, 16, 64), __shfl_xor(m2, 16, 64));
   const bool two = top2 && m2 != (F)-INFINITY;
   const F gs = two ? m1 + m2 : m1;
+  // Groups ahead of this lane's, and the distance of the nearest other group's
+  // score: the lanes of a group share the comparisons (21.5 us for 8192 x 384
+  // where every lane makes all of them, 20.4 so).
   int ahead = 0;
-  float near = INFINITY;                           // distance of the nearest other group's score
-  for (int o = 0; o < G; ++o) {
-    const F v = lane_of(gs, o * lanes);
+  float near = INFINITY;
+  for (int o = lane % lanes; o < G; o += lanes) {
+    const F v = __shfl(gs, o * lanes, 64);         // (a lane that is here while any is)
     ahead += v > gs || (v == gs && o < g);
     if (o != g && (v != (F)-INFINITY || gs != (F)-INFINITY)) near = fminf(near, fabsf((float)(v - gs)));
   }
+  auto join = [&](uint32_t n, float d) { ahead += (int)n, near = fminf(near, d); };
+  if (lanes > 1) join(dpp<0xb1, 0xf>((uint32_t)ahead), dpp<0xb1, 0xf>(near));
+  if (lanes > 2) join(dpp<0x4e, 0xf>((uint32_t)ahead), dpp<0x4e, 0xf>(near));
+  if (lanes > 4) join(dpp<0x141, 0xf>((uint32_t)ahead), dpp<0x141, 0xf>(near));
+  if (lanes > 8) join(dpp<0x140, 0xf>((uint32_t)ahead), dpp<0x140, 0xf>(near));
+  if (lanes > 16) join((uint32_t)__shfl_xor(ahead, 16, 64), __shfl_xor(near, 16, 64));
   if (bounded) {
     // (two finite keys whose sum fp32 does not hold say nothing)
     float bound = g >= G || m1 == (F)-INFINITY ? 0.0f
