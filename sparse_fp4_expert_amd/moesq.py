@@ -12,7 +12,6 @@ importing this module without it raises ImportError.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -344,13 +343,12 @@ def _count(n, name):
         raise ValueError(f"{name} must be below 2^31, got {n}")
 
 
-_as_is = contextlib.nullcontext()
-
-
-def _allocating(stream):
-    """Memory for a call's results comes from the stream that writes them: a
-    block of the current stream may still be in use there."""
-    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else _as_is
+def _current(stream, t):
+    """`stream` as the current one, for a call that allocates its results: a
+    block of another stream's may still be in use there."""
+    if stream.device.index != t.get_device():
+        raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
+    return torch.cuda.stream(stream)
 
 
 def _launch(dev, stream, call, *args):
@@ -765,34 +763,40 @@ def gate_topk(logits, gate: Gate, bias=None, n_rows=None, stream=None):
     topk_weights float32 [T*k]) as moesq_route and moesq_unpermute take them.
     bias: float32 [E], moves the selection but not the weights.  n_rows: a
     1-element int32 device tensor; rows from *n_rows on get ids -1."""
+    if isinstance(stream, torch.cuda.Stream):
+        with _current(stream, logits):
+            return gate_topk(logits, gate, bias, n_rows)
     if logits.dim() != 2:
         raise ValueError(f"logits must be [T, E], got {tuple(logits.shape)}")
     T, E = logits.shape
-    with _allocating(stream):
-        ids = torch.empty(T * gate.k, dtype=torch.int32, device=logits.device)
-        weights = torch.empty(T * gate.k, dtype=torch.float32, device=logits.device)
+    ids = torch.empty(T * gate.k, dtype=torch.int32, device=logits.device)
+    weights = torch.empty(T * gate.k, dtype=torch.float32, device=logits.device)
     moesq_gate_topk(logits, T, E, bias, gate, n_rows, ids, weights, stream)
     return ids, weights
 
 
 def mx_quantize(x, format: int = ROWS_MXFP4, stream=None) -> Mx:
     """float32 or bfloat16 [rows, K] or [E, N, K] -> its MX rows."""
+    if isinstance(stream, torch.cuda.Stream):
+        with _current(stream, x):
+            return mx_quantize(x, format)
     if x.dim() < 2:
         raise ValueError(f"x must be [..., K], got {tuple(x.shape)}")
     K = x.shape[-1]
     _dtype(x, "x")
     if format not in (ROWS_MXFP4, ROWS_MXFP8) or K % 32:
         raise ValueError(f"need an MX format and K % 32 == 0, got format {format}, K = {K}")
-    with _allocating(stream):
-        q = Mx.empty(x.shape[:-1], K, format, device=x.device)
+    q = Mx.empty(x.shape[:-1], K, format, device=x.device)
     moesq_mx_quantize(x, q.rows, K, format, q.codes, q.scales, stream)
     return q
 
 
 def mx_decode(x: Mx, stream=None):
     """The bfloat16 values that MX rows stand for, [..., K]."""
-    with _allocating(stream):
-        out = torch.empty(*x.shape, x.K, dtype=torch.bfloat16, device=x.codes.device)
+    if isinstance(stream, torch.cuda.Stream):
+        with _current(stream, x.codes):
+            return mx_decode(x)
+    out = torch.empty(*x.shape, x.K, dtype=torch.bfloat16, device=x.codes.device)
     moesq_mx_decode(x, out, stream)
     return out
 
@@ -803,19 +807,21 @@ def rmsnorm(x, weight, eps: float = 1e-6, residual=None, y: bool = True, rows: i
     Returns (y, residual_out, quantized rows): y is None with y=False,
     residual_out (x + residual in bfloat16) None without a residual, the rows
     an Mx (rows=ROWS_MXFP4 / ROWS_MXFP8), an Act4 (ROWS_NVFP4) or None."""
+    if isinstance(stream, torch.cuda.Stream):
+        with _current(stream, x):
+            return rmsnorm(x, weight, eps, residual, y, rows)
     if x.dim() != 2:
         raise ValueError(f"x must be [T, K], got {tuple(x.shape)}")
     T, K = x.shape
     rows = rows or ROWS_NONE
     q, codes, scales, row_scale = None, None, None, None
-    with _allocating(stream):
-        out = torch.empty_like(x) if y else None
-        res = torch.empty_like(x) if residual is not None else None
-        if rows in (ROWS_MXFP4, ROWS_MXFP8):
-            q = Mx.empty((T,), K, rows, device=x.device)
-        elif rows == ROWS_NVFP4:
-            q = Act4.empty(T, K, device=x.device)
-            row_scale = q.row_scale
+    out = torch.empty_like(x) if y else None
+    res = torch.empty_like(x) if residual is not None else None
+    if rows in (ROWS_MXFP4, ROWS_MXFP8):
+        q = Mx.empty((T,), K, rows, device=x.device)
+    elif rows == ROWS_NVFP4:
+        q = Act4.empty(T, K, device=x.device)
+        row_scale = q.row_scale
     if q is not None:
         codes, scales = q.codes, q.scales
     moesq_rmsnorm(x, residual, weight, T, K, eps, res, out, rows, codes, scales, row_scale, stream)
@@ -828,13 +834,15 @@ def mx_gemm(x: Mx, w: Mx, expert_offsets=None, perm=None, k: int = 1, epilogue: 
     no expert_offsets), or grouped over the E experts of w [E, N, ...].  With
     `perm`, routed row r reads row perm[r] // k of x; else x's rows are the
     routed rows."""
+    if isinstance(stream, torch.cuda.Stream):
+        with _current(stream, x.codes):
+            return mx_gemm(x, w, expert_offsets, perm, k, epilogue, out)
     E = w.shape[0] if len(w.shape) == 2 else 1
     N = w.shape[-1]
     M = x.rows * k if perm is not None else x.rows
     n_out = N // 2 if (epilogue & ~OUT_FLAT) == EPI_SWIGLU else N
     if out is None:
-        with _allocating(stream):
-            out = torch.empty(M, n_out, dtype=torch.bfloat16, device=x.codes.device)
+        out = torch.empty(M, n_out, dtype=torch.bfloat16, device=x.codes.device)
     elif tuple(out.shape) != (M, n_out):
         raise ValueError(f"out must be [{M}, {n_out}], got {tuple(out.shape)}")
     moesq_mx_gemm(x, perm, x.rows if perm is not None else 0, k, expert_offsets, M, w, E, epilogue, out,
