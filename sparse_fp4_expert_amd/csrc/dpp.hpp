@@ -25,13 +25,6 @@ __device__ __forceinline__ float lane63(float v) { return __uint_as_float(lane63
 __device__ __forceinline__ double lane63(double v) {
   return __hiloint2double((int)lane63((uint32_t)__double2hiint(v)), (int)lane63((uint32_t)__double2loint(v)));
 }
-__device__ __forceinline__ float lane_of(float v, int l) {
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
-}
-__device__ __forceinline__ double lane_of(double v, int l) {
-  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), l),
-                          __builtin_amdgcn_readlane(__double2loint(v), l));
-}
 // op over the 64 lanes, the same value in all of them.  A step's lanes
 // outside its rows see their own value again; lane 63 sees every lane's once
 // in each step, so sums are right there (rows first: rotations by 8, 4, 2

@@ -177,3 +177,38 @@ def test_results_of_a_side_stream_spare_pending_reads(lib):
         torch.cuda.synchronize()
         assert all(bool((c == 7).all()) for c in copies), i
         del kept, copies
+
+
+def test_rows_beyond_4_gib(lib):
+    """The last rows of buffers over 4 GiB are what a call on them alone gives."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    tail = 37
+    T, K = (1 << 20) + tail, 2080
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    x[-tail:] = torch.randn(tail, K, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(K, generator=g, device="cuda").to(torch.bfloat16)
+    end = x[-tail:].clone()
+    for rows in (lib.ROWS_MXFP8, lib.ROWS_NVFP4):
+        y, _, q = lib.rmsnorm(x, w, rows=rows)
+        ye, _, qe = lib.rmsnorm(end, w, rows=rows)
+        assert torch.equal(y[-tail:], ye)
+        assert torch.equal(q.codes[-tail:], qe.codes) and torch.equal(q.scales[-tail:], qe.scales)
+        del y, q
+    q, qe = lib.mx_quantize(x, lib.ROWS_MXFP8), lib.mx_quantize(end, lib.ROWS_MXFP8)
+    assert torch.equal(q.codes[-tail:], qe.codes) and torch.equal(q.scales[-tail:], qe.scales)
+    assert torch.equal(lib.mx_decode(q)[-tail:], lib.mx_decode(qe))
+    del x, q
+    # a product whose sums are exact in fp32 (64 products of E2M1 by two scales each)
+    N, K = 2080, 64
+    x = torch.randn(T, K, generator=g, device="cuda").to(torch.bfloat16)
+    mw = lib.mx_quantize(torch.randn(N, K, generator=g, device="cuda"))
+    y = lib.mx_gemm(lib.mx_quantize(x), mw)
+    assert torch.equal(y[-tail:], lib.mx_gemm(lib.mx_quantize(x[-tail:].clone()), mw))
+    del x, y
+    T, E = (1 << 20) + tail, 1024
+    l = torch.zeros(T, E, device="cuda")
+    l[-tail:] = torch.randn(tail, E, generator=g, device="cuda")
+    gate = lib.Gate(8, score=lib.SCORE_SIGMOID, n_group=8, topk_group=4)
+    bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+    for got, alone in zip(lib.gate_topk(l, gate, bias), lib.gate_topk(l[-tail:].clone(), gate, bias)):
+        assert torch.equal(got.view(T, 8)[-tail:], alone.view(tail, 8))
