@@ -368,7 +368,7 @@ moesq_status_t moesq_grouped_spgemm_act4(const moesq_act4_t *x, const int32_t *p
  *           scores to the lower group; a group whose experts are all masked
  *           is never kept.
  *   ids   = the k largest keys of what stays, in descending order, equal keys
- *           to the lower expert.  When fewer than k experts are left, the
+ *           (-0 and +0 among them) to the lower expert.  When fewer than k are left, the
  *           slots behind them get id -1 and weight 0: moesq_route does not
  *           route those, moesq_unpermute adds nothing for them.
  *   w[j]  = p[ids[j]], divided by the sum of the k selected p with

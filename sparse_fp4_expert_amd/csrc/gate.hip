@@ -42,8 +42,9 @@ struct GateArgs {
 
 constexpr float GATE_BIG = 3.4028234663852886e38f;
 
+// (-0 + 0 is +0: the two zeros are one key, and gate_order tells them apart)
 __device__ __forceinline__ float gate_clean(float l) {
-  return l != l ? -INFINITY : fminf(l, GATE_BIG);
+  return l != l ? -INFINITY : fminf(l, GATE_BIG) + 0.0f;
 }
 
 template <bool BF16>

@@ -153,3 +153,22 @@ def test_no_rows_and_offset_storage(lib):
     ids, _ = lib.gate_topk(l, lib.Gate(3))
     want, _ = oracle.gate_topk(l.float().cpu().numpy(), 3)
     assert np.array_equal(ids.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k", [(12, 4), (96, 9), (384, 8)])
+def test_signed_zeros_are_equal_keys(lib, dtype, E, k):
+    """-0.0 and +0.0 are one value: a tie between them goes to the lower
+    expert, inside the selection and at its border."""
+    rng = np.random.default_rng(7)
+    zeros = np.copysign(np.zeros((5, E)), rng.standard_normal((5, E)))
+    l = np.concatenate([zeros, zeros, zeros])
+    for t in range(5):
+        l[5 + t, rng.permutation(E)[:k // 2]] = 1.0 + rng.random(k // 2)      # the border falls among zeros
+        l[10 + t] = np.where(rng.random(E) < 0.7, rng.standard_normal(E) * 0.0, -1.0 - rng.random(E))
+    l[0, :2] = -0.0, 0.0
+    for score in ("softmax", "sigmoid"):
+        for kw in (dict(), dict(n_group=4, topk_group=2, group_score="max"),
+                   dict(n_group=4, topk_group=3, group_score="top2"), dict(bias=np.zeros(E)),
+                   dict(bias=np.copysign(np.zeros(E), rng.standard_normal(E)))):
+            run(lib, l, k, dtype=dtype, score=score, **kw)
