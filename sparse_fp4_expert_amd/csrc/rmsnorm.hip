@@ -65,10 +65,15 @@ __device__ __forceinline__ uint32_t norm_bf16x2(uint32_t s, uint32_t w, float r)
 }
 
 // The NVFP4 codes and block scale of one lane's unit, the steps of
-// moesq_quantize_activations.
+// moesq_quantize_activations.  Its block maximum passes over NaN, so the one
+// of the MX formats, in which a NaN wins, is not it.
 __device__ __forceinline__ void nvfp4_store_unit(const float (&v)[8], float g, size_t unit,
                                                  uint8_t *codes, uint8_t *scales) {
-  const float bmax = __uint_as_float(mx_block_amax(v));
+  float bmax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bmax = fmaxf(bmax, fabsf(v[i]));
+  bmax = fmaxf(bmax, __shfl_xor(bmax, 1, 64));     // (a block's lanes: see mx_block_amax)
+  bmax = fmaxf(bmax, __shfl_xor(bmax, 2, 64));
   const uint32_t sc = e4m3_encode(__fdiv_rn(bmax, 6.0f * g));
   const float sg = e4m3_to_f32(sc) * g;
   uint32_t c = 0;

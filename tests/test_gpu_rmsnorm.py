@@ -113,3 +113,27 @@ def test_no_rows(lib):
     y, s, q = lib.rmsnorm(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"),
                           torch.ones(64, dtype=torch.bfloat16, device="cuda"), rows=lib.ROWS_MXFP4)
     assert y.shape == (0, 64) and s is None and q.rows == 0
+
+
+@pytest.mark.parametrize("K", [64, 256, 7168, 20480])
+@pytest.mark.parametrize("residual", [False, True])
+def test_nvfp4_rows_with_nan_and_infinity(lib, K, residual):
+    """A NaN or an infinity in a weight, a token or through 0 * inf: the rows
+    are what the quantizer makes of y, block by block."""
+    x, r, w = inputs(9, K, 4)
+    x[1, 3] = float("nan")
+    x[2, 40] = float("inf")
+    x[3] = 0
+    r[3] = 0
+    x[4, 32:64], r[4, 32:64] = 0, 0
+    for name, at, value in (("finite", 0, 1.0), ("nan", 5, float("nan")), ("inf", 37, float("inf")),
+                            ("-inf", 63, -float("inf"))):
+        v = w.clone()
+        v[at] = value
+        for rows in (lib.ROWS_NVFP4, lib.ROWS_MXFP8, lib.ROWS_MXFP4):
+            y, s, q = lib.rmsnorm(x, v, 1e-6, residual=r if residual else None, rows=rows)
+            if name == "nan":
+                assert y[:, 5].isnan().all() and y[0, :5].isfinite().all()
+            check_rows(lib, q, y, rows)
+            _, _, only = lib.rmsnorm(x, v, 1e-6, residual=r if residual else None, y=False, rows=rows)
+            assert torch.equal(only.codes, q.codes) and torch.equal(only.scales, q.scales)
