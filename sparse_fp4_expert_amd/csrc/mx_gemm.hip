@@ -154,15 +154,38 @@ __device__ __forceinline__ uint32_t lds_offset(const void *p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
 }
 
+// The buffer from byte `by` on, or, not `wanted`, one of no bytes (copies from
+// it are zeros).  Where a stage can reach past the buffer (the last row's
+// last one), copies move on by this and not by the load's scalar offset: the
+// compiler's and the hardware's documents differ on whether the check of the
+// range counts that.  (Kernels of whole stages keep the scalar offset: 119, 111
+// and 321 us for the three large cases below, 127, 122 and 356 without it.
+// Added to each lane's offset instead, 128 experts of 2048 x 768 took 119 us
+// for 108.)
+__device__ __forceinline__ i32x4_t buffer_from(i32x4_t b, uint32_t by, bool wanted = true) {
+  const uint64_t u = ((uint64_t)(uint32_t)b[1] << 32 | (uint32_t)b[0]) + by;
+  b[0] = (int)(uint32_t)u;
+  b[1] = (int)(uint32_t)(u >> 32);
+  b[2] = wanted ? b[2] - (int)by : 0;
+  return b;
+}
+
 // 16 (or 4) bytes a lane from a buffer to LDS at lds + 16 (4) * lane.
-__device__ __forceinline__ void copy16_to_lds(uint32_t lds, i32x4_t buf, uint32_t voff, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
-               "s"(buf), "s"(__builtin_amdgcn_readfirstlane((int)soff))
+__device__ __forceinline__ void copy16_to_lds(uint32_t lds, i32x4_t buf, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff),
+               "s"(buf)
                : "memory");
 }
-__device__ __forceinline__ void copy4_to_lds(uint32_t lds, i32x4_t buf, uint32_t voff, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
-               "s"(buf), "s"(__builtin_amdgcn_readfirstlane((int)soff))
+// With all of it inside the buffer, `wanted`; else zeros.
+__device__ __forceinline__ void copy16_to_lds(uint32_t lds, i32x4_t buf, uint32_t voff, uint32_t soff, bool wanted) {
+  buf[2] = wanted ? buf[2] : 0;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
+               "s"(buf), "s"(__builtin_amdgcn_readfirstlane((int)(wanted ? soff : 0u)))
+               : "memory");
+}
+__device__ __forceinline__ void copy4_to_lds(uint32_t lds, i32x4_t buf, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(voff),
+               "s"(buf)
                : "memory");
 }
 
@@ -315,10 +338,11 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGem
   }
   auto fetch_w = [&](int slot, int c) {
     const uint32_t base = lds0 + slot * (uint32_t)sizeof(Ring);
+    const i32x4_t codes = buffer_from(wbuf, (uint32_t)c * 128), scales = buffer_from(wsbuf, (uint32_t)c * 8);
 #pragma unroll
-    for (int i = 0; i < WC; ++i) copy16_to_lds(base + i * 1024, wbuf, wo[i], (uint32_t)c * 128);
+    for (int i = 0; i < WC; ++i) copy16_to_lds(base + i * 1024, codes, wo[i]);
 #pragma unroll
-    for (int i = 0; i < WS; ++i) copy4_to_lds(base + offsetof(Ring, ws) + i * 256, wsbuf, wso[i], (uint32_t)c * 8);
+    for (int i = 0; i < WS; ++i) copy4_to_lds(base + offsetof(Ring, ws) + i * 256, scales, wso[i]);
   };
   // the first weights are under way before the tokens' rows are looked up
   if (n > 0) fetch_w(0, kw);
@@ -346,11 +370,11 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGem
   for (int g = 0; g < FM; ++g) xsub[g] = ALIGNED ? 0 : x_row(16 * g + rl) * (uint32_t)nb + a.xs_off;
   auto fetch_x = [&](int slot, int c) {
     const uint32_t base = lds0 + slot * (uint32_t)sizeof(Ring);
+    const i32x4_t codes = buffer_from(xbuf, (uint32_t)c * XB), scales = buffer_from(xsbuf, (uint32_t)c * 8);
 #pragma unroll
-    for (int i = 0; i < XC; ++i)
-      copy16_to_lds(base + offsetof(Ring, x) + i * 1024, xbuf, xo[i], (uint32_t)c * XB);
+    for (int i = 0; i < XC; ++i) copy16_to_lds(base + offsetof(Ring, x) + i * 1024, codes, xo[i]);
 #pragma unroll
-    for (int i = 0; i < XS; ++i) copy4_to_lds(base + offsetof(Ring, xs) + i * 256, xsbuf, xso[i], (uint32_t)c * 8);
+    for (int i = 0; i < XS; ++i) copy4_to_lds(base + offsetof(Ring, xs) + i * 256, scales, xso[i]);
   };
   if (n > 0) fetch_x(0, kw);
   if (n > 1) fetch_x(1, kw + KSPLIT);
@@ -575,23 +599,25 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled_kernel(MxGemmArgs a)
   Item cur;
   auto copy = [&](int i, int s) {
     const auto &st = lds.stage[s & 1];
-    i32x4_t buf = i < CW ? wbuf : xbuf;
-    buf[2] = s < stages ? buf[2] : 0;
-    if (i < CW)
-      copy16_to_lds(lds_offset(st.w) + (i * WAVES + wave) * 1024, buf, cur.off[i], (uint32_t)s * 128);
+    const uint32_t dst = i < CW ? lds_offset(st.w) + (i * WAVES + wave) * 1024
+                                : lds_offset(st.x) + ((i - CW) * WAVES + wave) * 1024;
+    const i32x4_t buf = i < CW ? wbuf : xbuf;
+    const uint32_t by = (uint32_t)s * (i < CW ? 128 : XB);
+    if constexpr (WIDE)                            // (whole stages)
+      copy16_to_lds(dst, buf, cur.off[i], by, s < stages);
     else
-      copy16_to_lds(lds_offset(st.x) + ((i - CW) * WAVES + wave) * 1024, buf, cur.off[i], (uint32_t)s * XB);
+      copy16_to_lds(dst, buffer_from(buf, by, s < stages), cur.off[i]);
   };
   // Scales of stages 2j and 2j + 1; not wanted: of no bytes, to a place of no use.
   auto copy_scales = [&](int j, bool wanted) {
-    i32x4_t buf = sr0 < BN ? wsbuf : xsbuf;
-    buf[2] = wanted ? buf[2] : 0;
+    const i32x4_t buf = sr0 < BN ? wsbuf : xsbuf;
     const uint32_t dst = (wanted ? lds_offset(lds.scales[j & 1]) : lds_offset(lds.unused)) + sr0 * SB;
     if constexpr (WIDE) {
-      copy16_to_lds(dst, buf, cur.soff[0], (uint32_t)j * 16);
+      copy16_to_lds(dst, buf, cur.soff[0], (uint32_t)j * 16, wanted);
     } else {
+      const i32x4_t from = buffer_from(buf, (uint32_t)j * 16, wanted);
 #pragma unroll
-      for (int i = 0; i < 5; ++i) copy4_to_lds(dst + i * 256, buf, cur.soff[i], (uint32_t)j * 16);
+      for (int i = 0; i < 5; ++i) copy4_to_lds(dst + i * 256, from, cur.soff[i]);
     }
   };
 
