@@ -19,6 +19,9 @@ moesq_status_t fail(moesq_status_t st, const std::string &msg);
 moesq_status_t launch_status(const char *what);
 // Compute units of the current device (cached per device).
 int device_cu_count();
+// Threads that one dimension of a launch may have.  From 2^32 on the count
+// wraps and workgroups are left out without an error.
+constexpr int MAX_LAUNCH_THREADS = 1 << 30;
 // Clears the thread's last-error detail (start of every entry point).
 void clear_error();
 

@@ -174,7 +174,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_kernel(RmsNormArgs a) {
 }
 
 template <int THREADS, int NU>
-static void launch_rows(const RmsNormArgs &a, int T, int rows_format, hipStream_t stream) {
+static void launch_part(const RmsNormArgs &a, int T, int rows_format, hipStream_t stream) {
   const dim3 grid((unsigned)T), block(THREADS);
   switch (rows_format) {
     case MOESQ_ROWS_MXFP4:
@@ -189,6 +189,23 @@ static void launch_rows(const RmsNormArgs &a, int T, int rows_format, hipStream_
     default:
       hipLaunchKernelGGL((rmsnorm_kernel<THREADS, NU, MOESQ_ROWS_NONE>), grid, block, 0, stream, a);
   }
+}
+
+template <int THREADS, int NU>
+static void launch_rows(RmsNormArgs a, int T, int rows_format, hipStream_t stream) {
+  constexpr int PART = MAX_LAUNCH_THREADS / THREADS;
+  for (; T > PART; T -= PART) {
+    launch_part<THREADS, NU>(a, PART, rows_format, stream);
+    const size_t units = (size_t)PART * a.units;
+    a.x += units;
+    if (a.residual) a.residual += units;
+    if (a.residual_out) a.residual_out += units;
+    if (a.y) a.y += units;
+    if (a.codes) a.codes += units * (rows_format == MOESQ_ROWS_MXFP8 ? 8 : 4);
+    if (a.scales) a.scales += units / 4;
+    if (a.row_scale) a.row_scale += PART;
+  }
+  launch_part<THREADS, NU>(a, T, rows_format, stream);
 }
 
 }  // namespace moesq

@@ -137,3 +137,42 @@ def test_nvfp4_rows_with_nan_and_infinity(lib, K, residual):
             check_rows(lib, q, y, rows)
             _, _, only = lib.rmsnorm(x, v, 1e-6, residual=r if residual else None, y=False, rows=rows)
             assert torch.equal(only.codes, q.codes) and torch.equal(only.scales, q.scales)
+
+
+@pytest.mark.parametrize("T,K,rows", [((1 << 26) + 5, 8, 0), ((1 << 26) + 5, 32, 1), ((1 << 25) + 3, 544, 0)])
+def test_more_rows_than_a_launch_has_threads_for(lib, T, K, rows):
+    """2^26 rows of 64 threads, 2^25 of 128: beyond the 2^32 threads of a launch."""
+    tail = 1 << 10
+    some, _, w = inputs(tail, K, 5)
+    y, _, q = lib.rmsnorm(some, w, rows=rows)
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    starts = (0, (1 << 24) - tail // 2, (1 << 25) - tail // 2 if T > 1 << 26 else tail, T - tail)
+    for t in starts:
+        x[t:t + tail] = some
+    yb, _, qb = lib.rmsnorm(x, w, rows=rows)
+    for t in starts:
+        assert torch.equal(yb[t:t + tail], y)
+        if rows:
+            assert torch.equal(qb.codes[t:t + tail], q.codes) and torch.equal(qb.scales[t:t + tail], q.scales)
+
+
+@pytest.mark.parametrize("rows", [2, 3])
+def test_rows_on_both_sides_of_two_launches(lib, rows):
+    """2^24 rows of 64 threads are one launch, what follows another: the
+    residual, its sum and the quantized rows go on there."""
+    T, K, tail = (1 << 24) + 77, 32, 1 << 10
+    some, res, w = inputs(tail, K, 6)
+    want = lib.rmsnorm(some, w, residual=res, rows=rows)
+    x, r = (torch.zeros(T, K, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    starts = (0, T - tail // 2)                      # the second over the border
+    for t in starts:
+        n = min(tail, T - t)
+        x[t:t + n], r[t:t + n] = some[:n], res[:n]
+    y, s, q = lib.rmsnorm(x, w, residual=r, rows=rows)
+    for t in starts:
+        n = min(tail, T - t)
+        parts = [(y, want[0]), (s, want[1]), (q.codes, want[2].codes), (q.scales, want[2].scales)]
+        if rows == lib.ROWS_NVFP4:
+            parts.append((q.row_scale, want[2].row_scale))
+        for u, v in parts:
+            assert torch.equal(u[t:t + n], v[:n])
