@@ -36,6 +36,7 @@ struct GateArgs {
   int32_t *ids;
   float *weights;
   int T, E;
+  int row0;           // of this launch's first row
   uint32_t per_inv;   // e * per_inv >> 20 is e / (experts of a group), for e < 1024
   moesq_gate_t g;
 };
@@ -282,7 +283,7 @@ template <int EPL, bool BF16>
 __global__ __launch_bounds__(GATE_THREADS) void gate_kernel(GateArgs a) {
   extern __shared__ __attribute__((aligned(16))) double s_key[];     // [waves][E] with groups
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row = blockIdx.x * GATE_WAVES + wave;
+  const int row = a.row0 + blockIdx.x * GATE_WAVES + wave;
   if (row >= a.T) return;   // the whole wave leaves together
   const int E = a.E, k = a.g.k;
   const size_t out = (size_t)row * k + lane;
@@ -337,8 +338,8 @@ __global__ __launch_bounds__(GATE_THREADS) void gate_kernel(GateArgs a) {
 }
 
 template <bool BF16>
-static void launch_gate(const GateArgs &a, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.T + GATE_WAVES - 1) / GATE_WAVES)), block(GATE_THREADS);
+static void launch_part(const GateArgs &a, int rows, hipStream_t stream) {
+  const dim3 grid((unsigned)((rows + GATE_WAVES - 1) / GATE_WAVES)), block(GATE_THREADS);
   const size_t lds = a.g.n_group > 1 ? (size_t)GATE_WAVES * a.E * sizeof(double) : 0;
   const int epl = (a.E + 63) / 64;
   if (epl <= 1) hipLaunchKernelGGL((gate_kernel<1, BF16>), grid, block, lds, stream, a);
@@ -347,6 +348,13 @@ static void launch_gate(const GateArgs &a, hipStream_t stream) {
   else if (epl <= 6) hipLaunchKernelGGL((gate_kernel<6, BF16>), grid, block, lds, stream, a);
   else if (epl <= 8) hipLaunchKernelGGL((gate_kernel<8, BF16>), grid, block, lds, stream, a);
   else hipLaunchKernelGGL((gate_kernel<16, BF16>), grid, block, lds, stream, a);
+}
+
+template <bool BF16>
+static void launch_gate(GateArgs a, hipStream_t stream) {
+  constexpr int PART = MAX_LAUNCH_THREADS / 64;
+  for (; a.T - a.row0 > PART; a.row0 += PART) launch_part<BF16>(a, PART, stream);
+  launch_part<BF16>(a, a.T - a.row0, stream);
 }
 
 }  // namespace moesq
@@ -389,7 +397,7 @@ extern "C" moesq_status_t moesq_gate_topk(const void *logits, int32_t dtype, int
   if ((uintptr_t)logits & (dtype == MOESQ_F32 ? 3 : 1))
     return fail(MOESQ_ERR_ARG, who + ": logits not aligned to their type");
   // floor(2^20 / per) + 1 is off by less than per, and e * per < 2^20
-  GateArgs a{logits, bias, n_rows, topk_ids, topk_weights, T, E, (1u << 20) / (uint32_t)(E / gate->n_group) + 1, *gate};
+  GateArgs a{logits, bias, n_rows, topk_ids, topk_weights, T, E, 0, (1u << 20) / (uint32_t)(E / gate->n_group) + 1, *gate};
   if (dtype == MOESQ_F32) launch_gate<false>(a, stream);
   else launch_gate<true>(a, stream);
   return launch_status("moesq_gate_topk");

@@ -172,3 +172,23 @@ def test_signed_zeros_are_equal_keys(lib, dtype, E, k):
                    dict(n_group=4, topk_group=3, group_score="top2"), dict(bias=np.zeros(E)),
                    dict(bias=np.copysign(np.zeros(E), rng.standard_normal(E)))):
             run(lib, l, k, dtype=dtype, score=score, **kw)
+
+
+def test_more_rows_than_a_launch_has_threads_for(lib):
+    """2^26 rows and more, a wave each: beyond the 2^32 threads of a launch."""
+    T, E, tail = (1 << 26) + 7, 4, 1 << 12
+    l = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(8)
+    some = torch.randn(tail, E, generator=g, device="cuda").to(torch.bfloat16)
+    starts = (0, (1 << 25) - tail // 2, T - tail)
+    for t in starts:
+        l[t:t + tail] = some
+    gate = lib.Gate(2)
+    want = [v.view(tail, 2) for v in lib.gate_topk(some, gate)]
+    n = torch.tensor([T - 3], dtype=torch.int32, device="cuda")
+    got = [v.view(T, 2) for v in lib.gate_topk(l, gate, n_rows=n)]
+    for u, v in zip(got, want):
+        for t in starts[:2]:
+            assert torch.equal(u[t:t + tail], v)
+        assert torch.equal(u[T - tail:T - 3], v[:-3])
+    assert (got[0][T - 3:] == -1).all() and (got[1][T - 3:] == 0).all()
