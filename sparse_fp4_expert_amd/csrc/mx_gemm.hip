@@ -36,6 +36,7 @@ struct MxGemmArgs {
   uint16_t *y;
   int k, M, E, N, K;
   int flat;
+  int tile0;                   // first token tile of this launch of the streaming kernel
   bool aligned, wide;          // every row's scales on 4-byte, 16-byte boundaries
   uint32_t xs_off, ws_off;     // of the scales from the 4-byte boundary that xs, ws are
   uint32_t x_bytes, xs_bytes;  // of all activation rows
@@ -299,7 +300,7 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGem
   const int q = lane >> 4, rl = lane & 15;
   const int cols = SWIGLU ? a.N / 2 : a.N;
   const int groups = (cols / FC + RG * FN - 1) / (RG * FN);
-  const MxTile t = mx_find_tile<16 * FM>(a, blockIdx.x / groups, lane);
+  const MxTile t = mx_find_tile<16 * FM>(a, a.tile0 + blockIdx.x / groups, lane);
   if (t.e < 0) return;
   const int kw = wave % KSPLIT;
   const int c0 = ((blockIdx.x % groups) * RG + wave / KSPLIT) * FN * FC;
@@ -843,13 +844,18 @@ static long long mx_tiles(const MxGemmArgs &a, int bm) {
 }
 
 template <bool FP8, bool SWIGLU, int KSPLIT, int FN, int FM>
-static void launch_stream(const MxGemmArgs &a, hipStream_t stream) {
-  const int frags = a.N / 16, rg = mxs_waves(KSPLIT) / KSPLIT * FN;
-  const dim3 grid((unsigned)(mx_tiles(a, 16 * FM) * ((frags + rg - 1) / rg))), block(mxs_waves(KSPLIT) * 64);
-  if (a.aligned)
-    hipLaunchKernelGGL((mx_stream_kernel<FP8, SWIGLU, true, KSPLIT, FN, FM>), grid, block, 0, stream, a);
-  else
-    hipLaunchKernelGGL((mx_stream_kernel<FP8, SWIGLU, false, KSPLIT, FN, FM>), grid, block, 0, stream, a);
+static void launch_stream(MxGemmArgs a, hipStream_t stream) {
+  constexpr int THREADS = mxs_waves(KSPLIT) * 64;
+  const int frags = a.N / 16, rg = mxs_waves(KSPLIT) / KSPLIT * FN, groups = (frags + rg - 1) / rg;
+  const long long tiles = mx_tiles(a, 16 * FM), part = std::max(1, MAX_LAUNCH_THREADS / THREADS / groups);
+  for (long long t = 0; t < tiles; t += part) {
+    a.tile0 = (int)t;
+    const dim3 grid((unsigned)(std::min(part, tiles - t) * groups)), block(THREADS);
+    if (a.aligned)
+      hipLaunchKernelGGL((mx_stream_kernel<FP8, SWIGLU, true, KSPLIT, FN, FM>), grid, block, 0, stream, a);
+    else
+      hipLaunchKernelGGL((mx_stream_kernel<FP8, SWIGLU, false, KSPLIT, FN, FM>), grid, block, 0, stream, a);
+  }
 }
 
 // How the weight rows (`frags` fragments of 16, counting every token tile
@@ -984,7 +990,7 @@ extern "C" moesq_status_t moesq_mx_gemm(const moesq_mx_t *x, const int32_t *perm
     return fail(MOESQ_ERR_ARG, who + ": codes and y must be 16-byte aligned");
   const uint32_t xs_off = (uintptr_t)x->scales & 3, ws_off = (uintptr_t)w->scales & 3;
   MxGemmArgs a{x->codes, x->scales - xs_off, w->codes, w->scales - ws_off, perm, expert_offsets, y,
-               k,        M,                  E,        N,                  w->K, flat};
+               k,        M,                  E,        N,                  w->K, flat, 0};
   a.aligned = w->K % 128 == 0 && !(xs_off | ws_off);
   a.wide = w->K % 512 == 0 && !(((uintptr_t)x->scales | (uintptr_t)w->scales) & 15);
   a.xs_off = xs_off;

@@ -370,3 +370,23 @@ def test_empty(lib):
     off = torch.zeros(3, dtype=torch.int32, device="cuda")
     assert tuple(lib.mx_gemm(q, w, off).shape) == (0, 32)
     assert tuple(lib.mx_decode(q).shape) == (0, 64)
+
+
+@pytest.mark.parametrize("T", [40, 2048])
+def test_more_tiles_than_a_launch_has_threads_for(lib, T):
+    """Few rows an expert and very many weight rows: the token tiles there may
+    be times the weights' workgroups pass the 2^32 threads of a launch (2048
+    rows).  All rows are the last expert's; sums of one block are exact."""
+    E, N, K = 1024, (1 << 21) - 32, 32
+    w = lib.Mx.empty((E, N), K, FMT["mxfp4"])
+    one = lib.mx_quantize(0.02 * torch.randn(N, K, device="cuda"))
+    w.codes[E - 1], w.scales[E - 1] = one.codes, one.scales
+    x = lib.mx_quantize(torch.randn(T, K, device="cuda").to(torch.bfloat16))
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[E] = T
+    y = lib.mx_gemm(x, w, off)
+    alone = lib.mx_gemm(x, one)
+    assert torch.equal(y, alone)
+    off[E - 1] = T // 2                      # the rows before: another expert's
+    w.codes[E - 2], w.scales[E - 2] = one.codes, one.scales
+    assert torch.equal(lib.mx_gemm(x, w, off), alone)
