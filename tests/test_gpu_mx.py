@@ -390,3 +390,26 @@ def test_more_tiles_than_a_launch_has_threads_for(lib, T):
     off[E - 1] = T // 2                      # the rows before: another expert's
     w.codes[E - 2], w.scales[E - 2] = one.codes, one.scales
     assert torch.equal(lib.mx_gemm(x, w, off), alone)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("T", [3000, 13000, 60000])
+def test_far_weights_tiled(lib, fmt, T):
+    """Expert matrices beyond 2^31 bytes of codes in the tiled kernel (more than
+    8 rows an expert on average: tiles of 64, 128 and up to 256 rows): the last
+    expert's result is the one of the same matrix alone."""
+    E, N, K = 300, 2048, 7168
+    w = lib.Mx.empty((E, N), K, FMT["mxfp4"])
+    one = lib.mx_quantize(0.02 * torch.randn(N, K, device="cuda"))
+    w.codes[E - 1], w.scales[E - 1] = one.codes, one.scales
+    x = lib.mx_quantize(torch.randn(T, K, device="cuda").to(torch.bfloat16), FMT[fmt])
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[E] = T
+    y = lib.mx_gemm(x, w, off)
+    a = lib.mx_gemm(x, one, torch.tensor([0, T], dtype=torch.int32, device="cuda")).double()
+    assert (y.double() - a).norm() <= 2.0 ** -8 * a.norm()
+    # against the formula too: the first rows and the last
+    r = torch.cat([torch.arange(5), torch.arange(T - 5, T)]).cuda()
+    xv = oracle.mx_decode(x.codes[r].cpu().numpy(), x.scales[r].cpu().numpy(), fmt)
+    ref, tol = gemm_bound(xv, oracle.mx_decode(one.codes.cpu().numpy(), one.scales.cpu().numpy(), "mxfp4"), fmt, False)
+    assert (np.abs(y[r].double().cpu().numpy() - ref) <= tol).all()
