@@ -16,6 +16,8 @@
 // reloads each 32-position block (the row is still in L2), finds its
 // maximum, its scale and its 32 codes.  The kernel is a stream over the
 // tokens: 2K bytes read and K/2 + K/32 + 4 written per row.
+#include <algorithm>
+
 #include "common.hpp"
 #include "encode.hpp"
 
@@ -100,9 +102,13 @@ extern "C" moesq_status_t moesq_quantize_activations(const uint16_t *x, int32_t 
     return fail(MOESQ_ERR_NULL, std::string(who) + ": NULL buffer");
   if (((uintptr_t)x | (uintptr_t)codes) & 15)
     return fail(MOESQ_ERR_ARG, std::string(who) + ": x and codes must be 16-byte aligned");
-  const unsigned grid = (unsigned)((T + AQ_WAVES - 1) / AQ_WAVES);
-  hipLaunchKernelGGL(act_quant_kernel, dim3(grid), dim3(AQ_THREADS), 0, stream,
-                     reinterpret_cast<const uint4 *>(x), (int)T, (int)K,
-                     reinterpret_cast<uint4 *>(codes), scales, row_scale);
+  constexpr int PART = MAX_LAUNCH_THREADS / 64;   // rows of a launch
+  for (long long row = 0; row < T; row += PART) {
+    const int rows = (int)std::min<long long>(PART, T - row);
+    const size_t block = (size_t)row * (size_t)(K / 32);
+    hipLaunchKernelGGL(act_quant_kernel, dim3((unsigned)((rows + AQ_WAVES - 1) / AQ_WAVES)), dim3(AQ_THREADS), 0,
+                       stream, reinterpret_cast<const uint4 *>(x) + block * 4, rows, (int)K,
+                       reinterpret_cast<uint4 *>(codes) + block, scales + block, row_scale + row);
+  }
   return launch_status(who);
 }

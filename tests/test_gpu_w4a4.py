@@ -259,3 +259,19 @@ def test_w4a4_gather_invalid_perm_entries(lib, paired):
     fkeep[gone] = False
     assert bool((flat[~fkeep] == 7).all())
     assert torch.equal(flat[perm[keep].long()], want[keep])
+
+
+def test_quantizer_rows_beyond_one_launch(lib):
+    """More than 2^26 rows, a wave each: beyond the 2^32 threads of a launch."""
+    T, K, tail = (1 << 26) + 9, 32, 1 << 10
+    g = torch.Generator(device="cuda").manual_seed(9)
+    some = torch.randn(tail, K, generator=g, device="cuda").to(torch.bfloat16)
+    want = lib.quantize_activations(some)
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    starts = (0, (1 << 24) - tail // 2, T - tail)
+    for t in starts:
+        x[t:t + tail] = some
+    q = lib.quantize_activations(x)
+    for t in starts:
+        for u, v in ((q.codes, want.codes), (q.scales, want.scales), (q.row_scale, want.row_scale)):
+            assert torch.equal(u[t:t + tail], v)
