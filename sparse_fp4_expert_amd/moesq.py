@@ -250,6 +250,7 @@ class Gate:
     def __init__(self, k: int, score: int = SCORE_SOFTMAX, n_group: int = 1, topk_group: int = 1,
                  group_score: int = GROUP_TOP2, renormalize: bool = True, scale: float = 1.0):
         self.k = int(k)
+        _count(self.k, "k")
         self.desc = GateDesc(self.k, score, n_group, topk_group, group_score, int(bool(renormalize)),
                              scale)
         self.ref = ctypes.byref(self.desc)
@@ -281,6 +282,7 @@ class Mx:
         """(descriptor, device), checked and made at the first use."""
         if self._desc is None:
             _count(self.rows, "rows")
+            _count(self.K, "K")
             dev, (codes, scales) = _pointers(
                 (self.codes, torch.uint8, self.rows * self.K // (2 if self.format == ROWS_MXFP4 else 1), "codes"),
                 (self.scales, torch.uint8, self.rows * self.K // 32, "scales"))
@@ -338,7 +340,8 @@ def _pointers(*specs):
 
 
 def _count(n, name):
-    """The library counts rows in 32 bits."""
+    """The library counts rows, their elements and experts in 32 bits; ctypes
+    would wrap a larger number."""
     if n >= 1 << 31:
         raise ValueError(f"{name} must be below 2^31, got {n}")
 
@@ -524,6 +527,7 @@ def moesq_gate_topk(logits, T: int, E: int, bias, gate: Gate, n_rows, topk_ids, 
                     stream=None):
     dtype, n = _dtype(logits, "logits"), T * gate.k
     _count(T, "T")
+    _count(E, "E")
     f32, i32 = torch.float32, torch.int32
     dev, (l, b, r, i, w) = _pointers(
         (logits, logits.dtype, T * E, "logits"), (bias, f32, E, "bias"), (n_rows, i32, 1, "n_rows"),
@@ -550,6 +554,7 @@ def _row_elements(format, rows, K):
 def moesq_mx_quantize(x, rows: int, K: int, format: int, codes, scales, stream=None):
     dtype, u8 = _dtype(x, "x"), torch.uint8
     _count(rows, "rows")
+    _count(K, "K")
     dev, (xp, c, s) = _pointers(
         (x, x.dtype, rows * K, "x"), (codes, u8, _row_elements(format, rows, K), "codes"),
         (scales, u8, rows * K // 32, "scales"))
@@ -566,6 +571,7 @@ def moesq_rmsnorm(x, residual, weight, T: int, K: int, eps: float, residual_out,
                   rows_format: int = ROWS_NONE, codes=None, scales=None, row_scale=None, stream=None):
     bf, u8, n = torch.bfloat16, torch.uint8, T * K
     _count(T, "T")
+    _count(K, "K")
     if rows_format == ROWS_NONE:
         codes = scales = row_scale = None
     dev, (xp, rp, wp, ro, yp, c, s, g) = _pointers(

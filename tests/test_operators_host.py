@@ -267,3 +267,18 @@ def test_binding_rejects_counts_beyond_32_bits(m):
                  lambda: many._described()):
         with pytest.raises(ValueError, match="2\\^31"):
             case()
+
+
+def test_binding_rejects_lengths_beyond_32_bits(m):
+    """A wrapped K, E or k would compute a part of every row without an error."""
+    z = lambda *s, dt=torch.uint8: torch.zeros(*s, dtype=dt)        # noqa: E731
+    bf, big = torch.bfloat16, (1 << 32) + 32
+    q = m.Mx.empty((1,), 32, m.ROWS_MXFP4, device="cpu")
+    long = m.Mx.__new__(m.Mx)._set(q.codes, q.scales, m.ROWS_MXFP4, (1,), big)
+    for case in (lambda: m.moesq_gate_topk(z(4, dt=bf), 1, big, None, m.Gate(1), None, None, None),
+                 lambda: m.Gate((1 << 32) + 1),
+                 lambda: m.moesq_mx_quantize(z(32, dt=bf), 1, big, 1, None, None),
+                 lambda: m.moesq_rmsnorm(z(8, dt=bf), None, z(8, dt=bf), 1, big, 1e-6, None, z(8, dt=bf)),
+                 lambda: long._described()):
+        with pytest.raises(ValueError, match="2\\^31"):
+            case()
