@@ -260,7 +260,11 @@ class Mx:
     """Device tensors of microscaled rows: scales uint8 [..., K/32] (E8M0) and
     codes uint8 [..., K/2] (ROWS_MXFP4) or [..., K] (ROWS_MXFP8).  Activations
     are [rows, ...]; MXFP4 weights [E, N, ...], or [N, ...] for one matrix.
-    Their contents may change, the tensors stay the ones it was made with."""
+    Their contents may change, the tensors stay the ones it was made with (the
+    descriptor holds their addresses, so `codes` and `scales` cannot be set)."""
+
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
 
     def __init__(self, codes, scales, format: int):
         if format not in (ROWS_MXFP4, ROWS_MXFP8):
@@ -273,7 +277,7 @@ class Mx:
         self._set(codes, scales, format, shape, K)
 
     def _set(self, codes, scales, format, shape, K):
-        self.codes, self.scales, self.format, self.shape, self.K = codes, scales, format, shape, K
+        self._codes, self._scales, self.format, self.shape, self.K = codes, scales, format, shape, K
         self.rows = math.prod(shape)
         self._desc = None
         return self

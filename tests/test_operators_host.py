@@ -282,3 +282,15 @@ def test_binding_rejects_lengths_beyond_32_bits(m):
                  lambda: long._described()):
         with pytest.raises(ValueError, match="2\\^31"):
             case()
+
+
+def test_rows_keep_their_tensors(m):
+    """Another tensor in the place of one whose address the descriptor may hold
+    would be passed over, and the old one read behind its release."""
+    q = m.Mx.empty((4,), 64, m.ROWS_MXFP4, device="cpu")
+    codes, scales = q.codes, q.scales
+    for name in ("codes", "scales"):
+        with pytest.raises(AttributeError):
+            setattr(q, name, torch.zeros_like(getattr(q, name)))
+    q.codes[1], q.scales[1] = 3, 127                       # their contents may change
+    assert q.codes is codes and q.scales is scales and int(codes[1, 0]) == 3
