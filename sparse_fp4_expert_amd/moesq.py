@@ -351,8 +351,13 @@ def _count(n, name):
 
 
 def _current(stream, t):
-    """`stream` as the current one, for a call that allocates its results: a
-    block of another stream's may still be in use there."""
+    """`stream` (an object, or a raw handle on t's device) as the current one,
+    for a call that allocates its results: a block of another stream's may
+    still be in use there."""
+    if not isinstance(stream, torch.cuda.Stream):
+        if not t.is_cuda:
+            raise ValueError("the tensors must be on the GPU")
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
     if stream.device.index != t.get_device():
         raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
     return torch.cuda.stream(stream)
@@ -773,7 +778,7 @@ def gate_topk(logits, gate: Gate, bias=None, n_rows=None, stream=None):
     topk_weights float32 [T*k]) as moesq_route and moesq_unpermute take them.
     bias: float32 [E], moves the selection but not the weights.  n_rows: a
     1-element int32 device tensor; rows from *n_rows on get ids -1."""
-    if isinstance(stream, torch.cuda.Stream):
+    if stream is not None:
         with _current(stream, logits):
             return gate_topk(logits, gate, bias, n_rows)
     if logits.dim() != 2:
@@ -787,7 +792,7 @@ def gate_topk(logits, gate: Gate, bias=None, n_rows=None, stream=None):
 
 def mx_quantize(x, format: int = ROWS_MXFP4, stream=None) -> Mx:
     """float32 or bfloat16 [rows, K] or [E, N, K] -> its MX rows."""
-    if isinstance(stream, torch.cuda.Stream):
+    if stream is not None:
         with _current(stream, x):
             return mx_quantize(x, format)
     if x.dim() < 2:
@@ -803,7 +808,7 @@ def mx_quantize(x, format: int = ROWS_MXFP4, stream=None) -> Mx:
 
 def mx_decode(x: Mx, stream=None):
     """The bfloat16 values that MX rows stand for, [..., K]."""
-    if isinstance(stream, torch.cuda.Stream):
+    if stream is not None:
         with _current(stream, x.codes):
             return mx_decode(x)
     out = torch.empty(*x.shape, x.K, dtype=torch.bfloat16, device=x.codes.device)
@@ -817,7 +822,7 @@ def rmsnorm(x, weight, eps: float = 1e-6, residual=None, y: bool = True, rows: i
     Returns (y, residual_out, quantized rows): y is None with y=False,
     residual_out (x + residual in bfloat16) None without a residual, the rows
     an Mx (rows=ROWS_MXFP4 / ROWS_MXFP8), an Act4 (ROWS_NVFP4) or None."""
-    if isinstance(stream, torch.cuda.Stream):
+    if stream is not None:
         with _current(stream, x):
             return rmsnorm(x, weight, eps, residual, y, rows)
     if x.dim() != 2:
@@ -844,7 +849,7 @@ def mx_gemm(x: Mx, w: Mx, expert_offsets=None, perm=None, k: int = 1, epilogue: 
     no expert_offsets), or grouped over the E experts of w [E, N, ...].  With
     `perm`, routed row r reads row perm[r] // k of x; else x's rows are the
     routed rows."""
-    if isinstance(stream, torch.cuda.Stream):
+    if stream is not None:
         with _current(stream, x.codes):
             return mx_gemm(x, w, expert_offsets, perm, k, epilogue, out)
     E = w.shape[0] if len(w.shape) == 2 else 1

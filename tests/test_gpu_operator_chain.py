@@ -179,6 +179,37 @@ def test_results_of_a_side_stream_spare_pending_reads(lib):
         del kept, copies
 
 
+def test_results_of_a_raw_stream_handle(lib):
+    """A stream given as its handle: results are allocated there too, and the
+    call is ordered behind that stream's work; 0 is the default stream."""
+    s = torch.cuda.Stream()
+    x = torch.randn(4096, 2048, device="cuda").to(torch.bfloat16)
+    w = torch.ones(2048, device="cuda", dtype=torch.bfloat16)
+    logits = torch.randn(4096, 128, device="cuda")
+    mxw = lib.mx_quantize(torch.randn(2048, 2048, device="cuda"))
+    mxx = lib.mx_quantize(x)
+    gate = lib.Gate(8)
+    calls = (lambda h: [(q := lib.mx_quantize(x, stream=h)).codes, q.scales], lambda h: [lib.mx_decode(mxx, stream=h)],
+             lambda h: [(r := lib.rmsnorm(x, w, rows=lib.ROWS_MXFP8, stream=h))[0], r[2].codes, r[2].scales],
+             lambda h: list(lib.gate_topk(logits, gate, stream=h)), lambda h: [lib.mx_gemm(mxx, mxw, stream=h)])
+    torch.cuda.synchronize()
+    for i, call in enumerate(calls):
+        want = call(None)
+        blocks = [torch.full((n,), 7, dtype=torch.uint8, device="cuda")
+                  for n in (4096 * 4096, 4096 * 2048, 4096 * 1024, 4096 * 64, 4096 * 32) for _ in range(2)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        copies = [b.clone() for b in blocks]
+        del blocks
+        got = call(s.cuda_stream)
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
+        torch.cuda.synchronize()
+        assert all(bool((c == 7).all()) for c in copies), i
+        for u, v, d in zip(got, want, call(0)):
+            assert torch.equal(u, v) and torch.equal(d, v), i
+        del got, copies
+
+
 def test_rows_beyond_4_gib(lib):
     """The last rows of buffers over 4 GiB are what a call on them alone gives."""
     g = torch.Generator(device="cuda").manual_seed(3)
