@@ -16,7 +16,7 @@
 // maximum in a lane, six lane permutations and a ballot.  Bound by these
 // rounds' instructions, not by the scores (13 MB of 8192 x 384, 2.6 us of
 // HBM): about 1000 vector instructions a row, 15 us of them.  Measured, k = 8:
-// 11.0 us for 8192 x 384 by softmax, 15.6 by sigmoid with a bias, 20.4 with 4
+// 11.0 us for 8192 x 384 by softmax, 15.6 by sigmoid with a bias, 21 with 4
 // of 8 groups too (up to 5 of them the one row in 64 bits that ends last; that
 // code as loops over LDS, a third of the instructions to fetch, took as long);
 // 5.4 for 4096 x 128; 4.3 for 16 x 128, of which a launch is 2.5.
@@ -132,7 +132,7 @@ __device__ __forceinline__ uint64_t gate_groups(const GateArgs &a, const F *sk, 
   const F gs = two ? m1 + m2 : m1;
   // Groups ahead of this lane's, and the distance of the nearest other group's
   // score: the lanes of a group share the comparisons (21.5 us for 8192 x 384
-  // where every lane makes all of them, 20.4 so).
+  // where every lane makes all of them, 20.4 so, on the same rows).
   int ahead = 0;
   float near = INFINITY;
   for (int o = lane % lanes; o < G; o += lanes) {

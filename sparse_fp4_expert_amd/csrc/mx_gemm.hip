@@ -261,9 +261,9 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t *p, uint32_t sub, b
 // for the final sum: KSPLIT waves of a workgroup share their rows, each with its
 // own stages, and add their sums in LDS in a fixed order.
 //
-// Measured: 16 rows of FP8 x 4096 x 7168 5.3 us (15.8 MB, 2.5 us of it a
+// Measured: 16 rows of FP8 x 4096 x 7168 5.5 us (15.8 MB, 2.5 us of it a
 // launch); 16 tokens on 8 of 128 experts of 1536 x 2048 FP4, some 70 of them
-// with rows, 15.3 us; 1024 rows on those, all of them with rows, 36 us (214 MB
+// with rows, 17 us; 1024 rows on those, all of them with rows, 36 us (214 MB
 // of weights: 6.0 TB/s, part of it from the last-level cache).
 //
 // SwiGLU: rows 0-7 of a fragment are gate rows, 8-15 the up rows of the same
@@ -455,11 +455,19 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGem
 // Measured: 8192 x 4096 x 7168 FP4 118 us, 4.1 PFLOP/s; its MFMAs alone,
 // without copies and reads of LDS, take 100 us on the same codes: the clock
 // falls to 2.0 GHz, and on codes of zero, with everything in place, the whole
-// kernel takes 96.  FP8 202 us (162 on zeros).  On 48 experts with uneven
+// kernel takes 96.  FP8 196 to 226 us by the clock (162 on zeros).  On 48 experts with uneven
 // loads, 8192 rows of FP8 in all, 320 to 350 us: a quarter more MFMAs than
 // dense for tiles that are partly empty, six rounds of tiles where five would
 // hold them, and 704 MB of weights from HBM.  A prefetch of the weights' lines
 // to the L2 two to six stages ahead made this 6 to 14 % slower.
+//
+// All this is for WIDE rows, K % 512 == 0 with scales on 16-byte boundaries.
+// Others pay for it: five copies of scales instead of one, scales put together
+// from two words, and with 256 x 256 tiles 32 (SwiGLU 65) registers that do not
+// fit.  K of 7136 for 7168, dense: FP4 142 us for 121, FP8 226 for 196; K of 2016
+// for 2048, 128 experts: FP4 165 for 109, FP8 160 for 136.  The down projection
+// of 128 experts, 2048 x 768 on 32768 rows, 127 us FP4 and 133 FP8 (254 and 267
+// MB: 51 and 54 at a copy's rate, most of it results).
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
@@ -920,6 +928,12 @@ static void launch_tiled(const MxGemmArgs &a, hipStream_t stream) {
 //   1024                                  56.2    30.4     29.9     44.9
 //   2048                                  99.7    53.2     40.8     46.6
 //   4096                                          100.5    74.7     61.7
+// (WIDE rows; the rule is the same for others.)  The average says nothing of
+// uneven loads: up to 8 rows an expert, all of them on one, stream that
+// expert's weights once for every 16 of its rows.  Such a call takes, us, and
+// with the one expert alone in it: 1024 rows on 128 experts of 1536 x 2048 FP4 15
+// (8), 384 on 48 of 4096 x 7168 FP8 41 (24), 2048 on 384 of 4096 x 7168 FP4 229
+// (38); with even loads 33, 150 and 1113.
 template <bool FP8, bool SWIGLU>
 static moesq_status_t launch_mx(const MxGemmArgs &a, hipStream_t stream) {
   const int experts = std::min(a.E, a.M), avg = (a.M + experts - 1) / experts;

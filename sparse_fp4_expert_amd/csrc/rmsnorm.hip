@@ -12,10 +12,12 @@
 // (64-bit multiply-adds run at the fp32 rate on this chip.)
 //
 // Bound by HBM: x and residual in, their sum out, and the rows, 6.5 to 9 bytes
-// an element.  Measured: 96 us for 8192 x 7168 with a residual and MXFP8 rows
-// (530 MB: 5.5 TB/s; a large copy reaches 5.0), 5.1 us for 64 x 7168, 2.8 us
-// for one row of 2048 (both the latency of a launch, a load, a reduction and
-// a store).
+// an element.  Measured: 94 us for 8192 x 7168 with a residual and MXFP8 rows
+// (530 MB: 5.6 TB/s; a large copy reaches 5.0), 5.0 us for 64 x 7168, 1.7 us
+// for one row of 2048 (both the latency of a load, a reduction and a store).
+// NVFP4 rows are bound by instructions, two exact divisions and an encoding in
+// fp32 steps for each element: 118 to 130 us for 8192 x 7168 with a residual
+// and no y (383 MB, 77 us at a copy's rate), 7.8 us for 64 x 7168.
 #include "dpp.hpp"
 #include "encode.hpp"
 #include "mx.hpp"
