@@ -507,6 +507,109 @@ moesq_status_t moesq_mx_gemm(const moesq_mx_t *x, const int32_t *perm, int32_t T
                              int32_t E, int32_t epilogue, uint16_t *y, hipStream_t stream);
 
 /*
+ * Product of bf16 rows with bf16 weights, dense or over all experts in one
+ * call: a layer's experts before their compression, or a shared expert or a
+ * dense layer that stays in bf16.
+ *   acc[r][n] = sum_k x[src(r)][k] * w_e[n][k]       (fp32 accumulation)
+ *   epilogue NONE:   y[r][n] = bf16_rne(acc[r][n]),  y is [M][N]
+ *   epilogue SWIGLU: y[r][c] = bf16_rne(silu(acc[r][c]) * acc[r][c+N/2]), y is [M][N/2]:
+ *                    a gated feed-forward block's two projections, activation
+ *                    and product
+ *   x [T][K] (with perm) or [M][K]; w [E][N][K]; expert_offsets, perm, T, k,
+ *   MOESQ_OUT_FLAT, rows outside every expert range: as moesq_mx_gemm.
+ *   z [M][N] bf16 out or NULL: with SWIGLU, bf16_rne(acc) in routed order, what
+ *   moesq_gemm_dx takes in the backward pass (y comes from the unrounded
+ *   sums).  Not with epilogue NONE, not with MOESQ_OUT_FLAT.
+ * All buffers 16-byte aligned; y and z overlap no input and not each other.
+ * Limits: N % 8 == 0, K % 8 == 0 (SWIGLU: N % 16 == 0), N, K <= MOESQ_GEMM_MAX_DIM,
+ *         N*K < 2^31, 1 <= E <= MOESQ_MAX_EXPERTS, 0 <= M <= 2^30; with perm the
+ *         tokens under 4 GiB (T*K <= 2^31 - 8).
+ */
+#define MOESQ_GEMM_MAX_DIM (1 << 20)
+moesq_status_t moesq_gemm(const uint16_t *x, const int32_t *perm, int32_t T, int32_t k,
+                          const int32_t *expert_offsets, int32_t M, const uint16_t *w, int32_t E,
+                          int32_t N, int32_t K, int32_t epilogue, uint16_t *y, uint16_t *z,
+                          hipStream_t stream);
+
+/*
+ * Gradient of the rows of moesq_gemm:
+ *   d[r][c] = sum_n dy[r][n] * w_e[n][c]             (fp32 accumulation), c < K
+ *   z == NULL: dx[r][c] = bf16_rne(d[r][c]), dx is [M][K].  With a gather in
+ *              the forward product these are the gradients of the routed
+ *              rows; moesq_unpermute with weights 1 adds those of a token.
+ *   z != NULL: the rows were the result of a gated block whose projections
+ *              z [M][2K] are: dx is [M][2K], the gradient of those, with
+ *              g = z[r][c], u = z[r][c+K], s = sigmoid(g):
+ *                dx[r][c]   = bf16_rne(d[r][c] * u * s * (1 + g * (1 - s)))
+ *                dx[r][c+K] = bf16_rne(d[r][c] * g * s)
+ *              dx may be z's own buffer.
+ *   dy [M][N] routed rows; w [E][N][K]; expert_offsets as moesq_mx_gemm.
+ * Rows of dx outside every expert range are not written.  All buffers 16-byte
+ * aligned.  Limits: as moesq_gemm without a gather.
+ */
+moesq_status_t moesq_gemm_dx(const uint16_t *dy, const int32_t *expert_offsets, int32_t M,
+                             const uint16_t *w, int32_t E, int32_t N, int32_t K, const uint16_t *z,
+                             uint16_t *dx, hipStream_t stream);
+
+/*
+ * Gradient of the weights of moesq_gemm:
+ *   d_e[n][c] = sum over r in [offsets[e], offsets[e+1]) of dy[r][n] * x[src(r)][c]
+ *                                                    (fp32 accumulation, in row order)
+ *   dw[e][n][c] = d_e[n][c] in `dtype` (MOESQ_BF16 rounded to nearest even, or
+ *   MOESQ_F32); with `accumulate` (MOESQ_F32 only) dw[e][n][c] + d_e[n][c].
+ *   dy [M][N] routed rows; x, perm, T, k, expert_offsets as moesq_gemm: rows with
+ *   perm[r] outside [0, T*k) count as zero.
+ *   dw [E][N][K]: every matrix is written, zeros (with `accumulate`: what was
+ *   there) for experts without rows.
+ * All buffers 16-byte aligned.  Limits: as moesq_gemm.
+ * Results are bit-identical on every run.
+ */
+moesq_status_t moesq_gemm_dw(const uint16_t *dy, const uint16_t *x, const int32_t *perm, int32_t T,
+                             int32_t k, const int32_t *expert_offsets, int32_t M, int32_t E,
+                             int32_t N, int32_t K, int32_t dtype, int32_t accumulate, void *dw,
+                             hipStream_t stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection (whatever
+ * computed it: moesq_mx_gemm, moesq_gemm, or a library):
+ *   v[t][j] = sum_k x[t][k] * a[id][j][k]                      j < slices * rank
+ *   d[t][n] = scale[id] * sum_j v[t][s*rank + j] * b[id][n][j]  s = n / (N / slices)
+ *   epilogue NONE:   y[t][n] = bf16_rne(base[t][n] + d[t][n]), y is [T][N]
+ *   epilogue SWIGLU: with p = base + d: y[t][c] = bf16_rne(silu(p[t][c]) * p[t][c+N/2]),
+ *                    y is [T][N/2]
+ * id = ids[t]; a row with ids[t] outside [0, adapters) has no adapter (d = 0).
+ * Sums are kept in fp32; v enters the second product as two bf16 numbers whose
+ * sum is within 2^-17 of it.
+ *   a [adapters][slices*rank][K], b [adapters][N][rank] bf16, scale [adapters]
+ *   fp32: slices > 1 are projections that share one base, such as gate and up,
+ *   each with adapters of its own.  An adapter of a lower rank has zeros behind it.
+ *   x [T][K] bf16; ids [T] int32; base [T][N] bf16 or NULL (zeros); y may be
+ *   base's own buffer with epilogue NONE.
+ *   ws, ws_bytes: workspace of moesq_lora_workspace_bytes() bytes, 16-byte
+ *   aligned, written and read by this call alone.
+ * The struct is a host object; its pointers are device pointers.  x, a, b, base
+ * and y 16-byte aligned.
+ * Limits: K % 8 == 0, rank % 8 == 0, rank <= MOESQ_LORA_MAX_RANK, 1 <= slices <=
+ *         MOESQ_LORA_MAX_SLICES, N % (8 * slices) == 0 (SWIGLU: N % 16 == 0),
+ *         N, K <= MOESQ_GEMM_MAX_DIM, adapters >= 1, 0 <= T <= 2^26.
+ * Results are bit-identical on every run, and a row's do not depend on the
+ * other rows' adapters.
+ */
+#define MOESQ_LORA_MAX_RANK 256
+#define MOESQ_LORA_MAX_SLICES 4
+typedef struct {
+  const uint16_t *a;
+  const uint16_t *b;
+  const float *scale;
+  int32_t adapters, rank, slices, N, K;
+} moesq_lora_t;
+moesq_status_t moesq_lora(const uint16_t *x, const int32_t *ids, int32_t T, const moesq_lora_t *adapters,
+                          const uint16_t *base, int32_t epilogue, uint16_t *y, void *ws,
+                          size_t ws_bytes, hipStream_t stream);
+/* 0 for sizes that moesq_lora refuses. */
+size_t moesq_lora_workspace_bytes(int32_t T, const moesq_lora_t *adapters);
+
+/*
  * Combine.
  *   topk_weights != NULL: out[t][:] = bf16_rne( sum_{j<k} w[t*k+j] * y[inv_perm[t*k+j]][:] ),
  *                         fp32 accumulation in j order; out is [T][N].
@@ -518,6 +621,24 @@ moesq_status_t moesq_mx_gemm(const moesq_mx_t *x, const int32_t *perm, int32_t T
 moesq_status_t moesq_unpermute(const uint16_t *y, const int32_t *inv_perm,
                                const float *topk_weights, int32_t T, int32_t k, int32_t N,
                                uint16_t *out, hipStream_t stream);
+
+/*
+ * Gradients of the router-weighted combine (moesq_unpermute with weights), of
+ * out[t] = sum_j w[t*k+j] * y[inv_perm[t*k+j]]:
+ *   dy[inv_perm[i]][:] = bf16_rne(w[i] * dout[i/k][:])      (NULL: not wanted)
+ *   dw[i] = sum_n dout[i/k][n] * y[inv_perm[i]][n], fp32     (NULL: not wanted)
+ *   dout [T][N], y [T*k][N] (needed for dw, else may be NULL) bf16, inv_perm
+ *   [T*k] int32, topk_weights [T*k] fp32 (needed for dy, else may be NULL);
+ *   dy [T*k][N] bf16, may be y's own buffer; dw [T*k] fp32.
+ * Entries of inv_perm outside [0, T*k) get dw 0; rows of dy that no entry names
+ * are not written.  inv_perm names a row at most once.  dout, y and dy 16-byte
+ * aligned.  Limits: N % 8 == 0, N > 0, T >= 0, k >= 1, T*k < 2^31.
+ * Results are bit-identical on every run.
+ */
+moesq_status_t moesq_unpermute_backward(const uint16_t *dout, const uint16_t *y,
+                                        const int32_t *inv_perm, const float *topk_weights,
+                                        int32_t T, int32_t k, int32_t N, uint16_t *dy, float *dw,
+                                        hipStream_t stream);
 
 /*
  * Compress dense fp32 experts into the canonical layout above

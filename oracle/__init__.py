@@ -31,6 +31,7 @@ from .pack import PackedExpert, decode, quantize, support
 from .paired import (PAIRS, PackedPairedExpert, decode_paired, paired_pattern,
                      paired_support, pattern_mask, quantize_paired)
 from .route import route
+from .ffn import combine_grad, lora, swiglu_grad
 from .gate import gate_topk
 from .mx import mx_decode, mx_gemm, mx_quantize, rmsnorm
 from .moe import (grouped_gemm, moe_chain, permute, silu, swiglu, unpermute,

@@ -4,7 +4,7 @@
 // "D.3 End-to-end serving benchmark": token combination and output layout
 // stay outside the expert kernel.  All three kernels are HBM copies with
 // 16-byte loads and stores.
-#include "common.hpp"
+#include "dpp.hpp"
 
 namespace moesq {
 
@@ -120,6 +120,53 @@ __global__ __launch_bounds__(DISPATCH_THREADS) void combine_kernel(
   }
 }
 
+// Gradients of the combine: dy[r] = bf16(w[i] dout[t]) and dw[i] = <dout[t],
+// y[r]> of flat entry i = t*k + j with row r = inv_perm[i].  A wave an entry:
+// the k entries of a token read its row of dout from the caches, and the sum
+// over a row's columns stays in one wave, in a fixed order.
+__global__ __launch_bounds__(DISPATCH_THREADS) void combine_grad_kernel(
+    const uint4 *__restrict__ dout, const uint4 *y, const int32_t *__restrict__ inv_perm,
+    const float *__restrict__ w, int k, int M, int N8, uint4 *dy, float *__restrict__ dw) {
+  const int lane = threadIdx.x & 63;
+  const int wave = (blockIdx.x * DISPATCH_THREADS + threadIdx.x) >> 6;
+  const int nwaves = (gridDim.x * DISPATCH_THREADS) >> 6;
+  for (long long i = wave; i < M; i += nwaves) {
+    const int r = inv_perm[i];
+    const bool there = r >= 0 && r < M;
+    float sum = 0.0f;
+    if (there) {
+      const float wi = dy ? w[i] : 0.0f;
+      const uint4 *d = dout + (size_t)(i / k) * N8, *yr = y + (size_t)r * N8;
+      uint4 *o = dy + (size_t)r * N8;
+      for (int c0 = 0; c0 < N8; c0 += 64 * COPY_UNROLL) {
+        uint4 v[COPY_UNROLL], u[COPY_UNROLL];
+#pragma unroll
+        for (int h = 0; h < COPY_UNROLL; ++h) {
+          const int c = c0 + 64 * h + lane;
+          v[h] = c < N8 ? d[c] : make_uint4(0, 0, 0, 0);
+          u[h] = c < N8 && dw ? yr[c] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int h = 0; h < COPY_UNROLL; ++h) {
+          const int c = c0 + 64 * h + lane;
+          const uint32_t p[4] = {v[h].x, v[h].y, v[h].z, v[h].w}, q[4] = {u[h].x, u[h].y, u[h].z, u[h].w};
+          uint32_t b[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sum = fmaf(bf16_lo(p[j]), bf16_lo(q[j]), sum);
+            sum = fmaf(bf16_hi(p[j]), bf16_hi(q[j]), sum);
+            b[j] = pack_bf16x2(wi * bf16_lo(p[j]), wi * bf16_hi(p[j]));
+          }
+          if (dy && c < N8) o[c] = make_uint4(b[0], b[1], b[2], b[3]);
+        }
+      }
+    }
+    if (!dw) continue;
+    sum = wave_reduce(sum, [](float a, float b) { return a + b; });
+    if (lane == 0) dw[i] = there ? sum : 0.0f;
+  }
+}
+
 // Blocks for `units` work units (one wavefront each), capped at 32 blocks
 // per CU.
 static int units_grid(long long units) {
@@ -171,4 +218,29 @@ extern "C" moesq_status_t moesq_unpermute(const uint16_t *y, const int32_t *inv_
                        (const uint4 *)y, inv_perm, (int)M, N / 8, (uint4 *)out);
   }
   return launch_status("moesq_unpermute");
+}
+
+extern "C" moesq_status_t moesq_unpermute_backward(const uint16_t *dout, const uint16_t *y,
+                                                   const int32_t *inv_perm,
+                                                   const float *topk_weights, int32_t T, int32_t k,
+                                                   int32_t N, uint16_t *dy, float *dw,
+                                                   hipStream_t stream) {
+  const std::string who("moesq_unpermute_backward");
+  clear_error();
+  if (T < 0 || k < 1) return fail(MOESQ_ERR_SHAPE, who + ": need T >= 0, k >= 1");
+  if (N <= 0 || N % 8) return fail(MOESQ_ERR_SHAPE, who + ": N must be a positive multiple of 8");
+  const long long M = (long long)T * k;
+  if (M >= (1ll << 31)) return fail(MOESQ_ERR_SHAPE, who + ": T*k must be < 2^31");
+  if (M == 0) return MOESQ_OK;
+  if (!dy && !dw) return fail(MOESQ_ERR_NULL, who + ": neither dy nor dw is wanted");
+  if (!dout || !inv_perm) return fail(MOESQ_ERR_NULL, who + ": NULL dout or inv_perm");
+  if (dy && !topk_weights) return fail(MOESQ_ERR_NULL, who + ": dy needs topk_weights");
+  if (dw && !y) return fail(MOESQ_ERR_NULL, who + ": dw needs y");
+  if (((uintptr_t)dout | (uintptr_t)y | (uintptr_t)dy) & 15)
+    return fail(MOESQ_ERR_ARG, who + ": dout, y and dy must be 16-byte aligned");
+  if (dy == dout) return fail(MOESQ_ERR_ARG, who + ": dy may not be dout's buffer");
+  hipLaunchKernelGGL(combine_grad_kernel, dim3(units_grid(M)), dim3(DISPATCH_THREADS), 0, stream,
+                     (const uint4 *)dout, (const uint4 *)y, inv_perm, topk_weights, k, (int)M, N / 8,
+                     (uint4 *)dy, dw);
+  return launch_status("moesq_unpermute_backward");
 }

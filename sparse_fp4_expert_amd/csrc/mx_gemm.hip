@@ -22,7 +22,7 @@
 #include <type_traits>
 
 #include "mx.hpp"
-#include "route_dev.hpp"
+#include "row_tiles.hpp"
 
 namespace moesq {
 
@@ -52,80 +52,6 @@ __device__ __forceinline__ f32x4_t mfma_mx(i32x8_t w, i32x8_t x, f32x4_t c, uint
                                                           (int)sw, SEL, (int)sx);
 }
 
-// Rows of expert e.
-__device__ __forceinline__ int2 mx_rows_of(const MxGemmArgs &a, int e) {
-  const int lo = min(max(a.offsets[e], 0), a.M), hi = min(max(a.offsets[e + 1], 0), a.M);
-  return make_int2(lo, hi);
-}
-
-struct MxTile {
-  int e, row0, rows;   // e < 0: no such tile
-};
-
-constexpr int FIND_BATCH = 4;
-
-// The t-th token tile of up to BM rows, experts in order; a whole wave calls
-// it and gets the same answer in every lane.
-template <int BM>
-__device__ __forceinline__ MxTile mx_find_tile(const MxGemmArgs &a, int t, int lane) {
-  if (!a.offsets) {
-    const int row0 = t * BM;
-    return row0 < a.M ? MxTile{0, row0, min(BM, a.M - row0)} : MxTile{-1, 0, 0};
-  }
-  int before = 0;
-  for (int b0 = 0; b0 < a.E; b0 += 64 * FIND_BATCH) {
-    int2 r[FIND_BATCH];
-#pragma unroll
-    for (int j = 0; j < FIND_BATCH; ++j) {   // loads of a batch in flight together
-      const int e = b0 + 64 * j + lane;
-      r[j] = e < a.E ? mx_rows_of(a, e) : make_int2(0, 0);
-    }
-#pragma unroll
-    for (int j = 0; j < FIND_BATCH; ++j) {
-      const int e0 = b0 + 64 * j;
-      if (e0 >= a.E) break;
-      const int tiles = r[j].y > r[j].x ? (r[j].y - r[j].x + BM - 1) / BM : 0;
-      const int incl = wave_incl_scan(tiles, lane);
-      const uint64_t hit = __ballot(before + incl > t);
-      if (hit) {
-        const int who = __ffsll((unsigned long long)hit) - 1;
-        const int lo = __shfl(r[j].x, who, 64), hi = __shfl(r[j].y, who, 64);
-        const int row0 = lo + (t - before - __shfl(incl - tiles, who, 64)) * BM;
-        return MxTile{e0 + who, row0, min(BM, hi - row0)};
-      }
-      before += __shfl(incl, 63, 64);
-    }
-  }
-  return MxTile{-1, 0, 0};
-}
-
-// All token tiles of up to BM rows; as mx_find_tile.
-template <int BM>
-__device__ __forceinline__ int mx_count_tiles(const MxGemmArgs &a, int lane) {
-  if (!a.offsets) return (a.M + BM - 1) / BM;
-  int mine = 0;
-#pragma unroll FIND_BATCH
-  for (int e = lane; e < a.E; e += 64) {
-    const int2 r = mx_rows_of(a, e);
-    mine += r.y > r.x ? (r.y - r.x + BM - 1) / BM : 0;
-  }
-  return __shfl(wave_incl_scan(mine, lane), 63, 64);
-}
-
-// Source row of routed row r; -1: a zero row.
-__device__ __forceinline__ int mx_src(const MxGemmArgs &a, int r) {
-  if (!a.perm) return r;
-  const int p = a.perm[r];
-  return p >= 0 && p < a.M ? p / a.k : -1;
-}
-
-// Output row of routed row r; -1: not stored.
-__device__ __forceinline__ int mx_dst(const MxGemmArgs &a, int r) {
-  if (!a.flat) return r;
-  const int p = a.perm[r];
-  return p >= 0 && p < a.M ? p : -1;
-}
-
 __device__ __forceinline__ i32x8_t as_operand(uint4 lo, uint4 hi) {
   i32x8_t v;
   v[0] = (int)lo.x, v[1] = (int)lo.y, v[2] = (int)lo.z, v[3] = (int)lo.w;
@@ -133,73 +59,11 @@ __device__ __forceinline__ i32x8_t as_operand(uint4 lo, uint4 hi) {
   return v;
 }
 
-// ------------------------------------------------------------------ copies to LDS
-//
-// Written as asm without register results, so the compiler's wait counts know
-// nothing of them: a kernel waits for its copies by a count of its own, and
-// its reads of LDS stay ordinary loads that the compiler schedules.
-
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ i32x4_t raw_buffer(const void *p, uint32_t bytes) {
-  const uint64_t u = (uint64_t)(uintptr_t)p;
-  i32x4_t r;
-  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)u);
-  r[1] = __builtin_amdgcn_readfirstlane((int)((uint32_t)(u >> 32) & 0xffffu));
-  r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
-  r[3] = 0x20000;
-  return r;
-}
-
-__device__ __forceinline__ uint32_t lds_offset(const void *p) {
-  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
-}
-
-// The buffer from byte `by` on, or, not `wanted`, one of no bytes (copies from
-// it are zeros).  Where a stage can reach past the buffer (the last row's
-// last one), copies move on by this and not by the load's scalar offset: the
-// compiler's and the hardware's documents differ on whether the check of the
-// range counts that.  (Kernels of whole stages keep the scalar offset: 119, 111
-// and 321 us for the three large cases below, 127, 122 and 356 without it.
-// Added to each lane's offset instead, 128 experts of 2048 x 768 took 119 us
-// for 108.)
-__device__ __forceinline__ i32x4_t buffer_from(i32x4_t b, uint32_t by, bool wanted = true) {
-  const uint64_t u = ((uint64_t)(uint32_t)b[1] << 32 | (uint32_t)b[0]) + by;
-  b[0] = (int)(uint32_t)u;
-  b[1] = (int)(uint32_t)(u >> 32);
-  b[2] = wanted ? b[2] - (int)by : 0;
-  return b;
-}
-
-// 16 (or 4) bytes a lane from a buffer to LDS at lds + 16 (4) * lane.
-__device__ __forceinline__ void copy16_to_lds(uint32_t lds, i32x4_t buf, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff),
-               "s"(buf)
-               : "memory");
-}
-// With all of it inside the buffer, `wanted`; else zeros.
-__device__ __forceinline__ void copy16_to_lds(uint32_t lds, i32x4_t buf, uint32_t voff, uint32_t soff, bool wanted) {
-  buf[2] = wanted ? buf[2] : 0;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
-               "s"(buf), "s"(__builtin_amdgcn_readfirstlane((int)(wanted ? soff : 0u)))
-               : "memory");
-}
-__device__ __forceinline__ void copy4_to_lds(uint32_t lds, i32x4_t buf, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(voff),
-               "s"(buf)
-               : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void wait_copies() {   // all but the last N have landed
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
 // Adds the KSPLIT waves' sums (through `lds`, no longer in use otherwise), and
 // stores the results.  The waves of a row group each finish some of its token
 // fragments.
 template <bool SWIGLU, int KSPLIT, int FM>
-__device__ __forceinline__ void mx_stream_finish(const MxGemmArgs &a, const MxTile &t, f32x4_t (&acc)[FM], void *lds,
+__device__ __forceinline__ void mx_stream_finish(const MxGemmArgs &a, const RowTile &t, f32x4_t (&acc)[FM], void *lds,
                                                  int c0, int cols, int wave, int lane) {
   const int q = lane >> 4, rl = lane & 15, kw = wave % KSPLIT;
   f32x4_t *part = static_cast<f32x4_t *>(lds);     // [waves][FM][64]
@@ -227,20 +91,13 @@ __device__ __forceinline__ void mx_stream_finish(const MxGemmArgs &a, const MxTi
     }
     const int r = 16 * g + rl;
     if (c0 >= cols || r >= t.rows || (SWIGLU && q >= 2)) continue;
-    const int dst = mx_dst(a, t.row0 + r);
+    const int dst = dst_row(a, t.row0 + r);
     if (dst < 0) continue;
-    const bool ok = mx_src(a, t.row0 + r) >= 0;
+    const bool ok = src_row(a, t.row0 + r) >= 0;
     *reinterpret_cast<uint2 *>(a.y + (size_t)dst * cols + c0 + 4 * q) =
         ok ? make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])) : make_uint2(0, 0);
   }
 }
-
-// Chunk positions in LDS: rows are as in memory, their 16-byte pieces permuted
-// by the row number so that the 16 rows that read one piece together touch
-// all 64 banks once.  Piece c of row r of 128-byte rows (256 positions of
-// E2M1) and of 256-byte rows (E4M3).
-__device__ __forceinline__ int piece4(int r, int c) { return c ^ ((r >> 1) & 7); }
-__device__ __forceinline__ int piece8(int r, int c) { return c ^ (r & 15); }
 
 // Scales in LDS.  A row's scale bytes may start anywhere; copies take 4-byte
 // words from the boundary at or before a stage's first byte, and `sub`, the
@@ -300,7 +157,7 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGem
   const int q = lane >> 4, rl = lane & 15;
   const int cols = SWIGLU ? a.N / 2 : a.N;
   const int groups = (cols / FC + RG * FN - 1) / (RG * FN);
-  const MxTile t = mx_find_tile<16 * FM>(a, a.tile0 + blockIdx.x / groups, lane);
+  const RowTile t = find_tile<16 * FM>(a, a.tile0 + blockIdx.x / groups, lane);
   if (t.e < 0) return;
   const int kw = wave % KSPLIT;
   const int c0 = ((blockIdx.x % groups) * RG + wave / KSPLIT) * FN * FC;
@@ -350,7 +207,7 @@ __global__ __launch_bounds__(mxs_waves(KSPLIT) * 64) void mx_stream_kernel(MxGem
   if (n > 1) fetch_w(1, kw + KSPLIT);
 
   const i32x4_t xbuf = raw_buffer(a.xc, a.x_bytes), xsbuf = raw_buffer(a.xs, (a.xs_off + a.xs_bytes + 3) & ~3u);
-  auto x_row = [&](int r) { return (uint32_t)(r < t.rows ? max(mx_src(a, t.row0 + r), 0) : 0); };
+  auto x_row = [&](int r) { return (uint32_t)(r < t.rows ? max(src_row(a, t.row0 + r), 0) : 0); };
   uint32_t xo[XC], xso[XS];
 #pragma unroll
   for (int i = 0; i < XC; ++i) {
@@ -536,11 +393,11 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled_kernel(MxGemmArgs a)
   // share panels of both operands in its L2; each walks the run by the number
   // of them.  (Full tiles first and partial ones last balances better, and was
   // 3 to 9 % slower with uneven loads: weights are read twice.)
-  const int mt = __builtin_amdgcn_readfirstlane(mx_count_tiles<BM>(a, lane)), items = mt * nt, run = (items + 7) >> 3;
+  const int mt = __builtin_amdgcn_readfirstlane(count_tiles<BM>(a, lane)), items = mt * nt, run = (items + 7) >> 3;
   const int last = min(items, ((blockIdx.x & 7) + 1) * run);
   auto set_up = [&](Item &it, int item) {
     const int first = item / (4 * nt) * 4, in = item - first * nt, four = min(4, mt - first);
-    const MxTile t = mx_find_tile<BM>(a, first + in % four, lane);
+    const RowTile t = find_tile<BM>(a, first + in % four, lane);
     it.e = __builtin_amdgcn_readfirstlane(t.e);
     it.c0 = in / four * BC;
     const int rows = __builtin_amdgcn_readfirstlane(t.e < 0 ? 0 : t.rows);
@@ -560,7 +417,7 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled_kernel(MxGemmArgs a)
       return (uint32_t)n;
     };
     // (rows that are not there read row 0, and their results are not used)
-    auto x_row = [&](int r) { return (uint32_t)(r < rows ? max(mx_src(a, t.row0 + r), 0) : 0); };
+    auto x_row = [&](int r) { return (uint32_t)(r < rows ? max(src_row(a, t.row0 + r), 0) : 0); };
 #pragma unroll
     for (int i = 0; i < CW; ++i) {
       const int r = (i * WAVES + wave) * 8 + (lane >> 3);
@@ -590,8 +447,8 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled_kernel(MxGemmArgs a)
 #pragma unroll
     for (int g = 0; g < FM; ++g) {
       const int r = (wave / WN) * FM * 32 + 32 * g + rl;
-      it.dst[g] = r < rows ? mx_dst(a, t.row0 + r) : -1;
-      it.zero[g] = r < rows && mx_src(a, t.row0 + r) < 0;
+      it.dst[g] = r < rows ? dst_row(a, t.row0 + r) : -1;
+      it.zero[g] = r < rows && src_row(a, t.row0 + r) < 0;
     }
   };
   const i32x4_t xbuf = raw_buffer(a.xc, a.x_bytes);
@@ -845,17 +702,11 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled_kernel(MxGemmArgs a)
 // Rows of tiles, the last one partial, are counted in 32 bits.
 constexpr int32_t MX_MAX_ROWS = 1 << 30;
 
-// Upper bound of the token tiles of BM rows: an expert with rows has at most
-// one partial tile.
-static long long mx_tiles(const MxGemmArgs &a, int bm) {
-  return ((long long)a.M + (long long)std::min(a.E, a.M) * (bm - 1)) / bm;
-}
-
 template <bool FP8, bool SWIGLU, int KSPLIT, int FN, int FM>
 static void launch_stream(MxGemmArgs a, hipStream_t stream) {
   constexpr int THREADS = mxs_waves(KSPLIT) * 64;
   const int frags = a.N / 16, rg = mxs_waves(KSPLIT) / KSPLIT * FN, groups = (frags + rg - 1) / rg;
-  const long long tiles = mx_tiles(a, 16 * FM), part = std::max(1, MAX_LAUNCH_THREADS / THREADS / groups);
+  const long long tiles = most_tiles(a, 16 * FM), part = std::max(1, MAX_LAUNCH_THREADS / THREADS / groups);
   for (long long t = 0; t < tiles; t += part) {
     a.tile0 = (int)t;
     const dim3 grid((unsigned)(std::min(part, tiles - t) * groups)), block(THREADS);
@@ -878,7 +729,7 @@ static void launch_stream(MxGemmArgs a, hipStream_t stream) {
 //   4064 of up to 12288 (384 experts, K 7168 FP4)    4/2 57.4 2/2 47.0  1/2 59.3
 template <bool FP8, bool SWIGLU, int FM>
 static void launch_stream_split(const MxGemmArgs &a, hipStream_t stream) {
-  const long long frags = mx_tiles(a, 16 * FM) * (a.N / 16);
+  const long long frags = most_tiles(a, 16 * FM) * (a.N / 16);
   const int cus = device_cu_count();
   if (frags <= cus && a.K >= 2048) {
     if constexpr (FM == 1) return launch_stream<FP8, SWIGLU, 8, 1, FM>(a, stream);
@@ -892,7 +743,7 @@ static void launch_stream_split(const MxGemmArgs &a, hipStream_t stream) {
 template <bool FP8, bool SWIGLU, int WN, int WM, int FN, int FM>
 static void launch_tiled(const MxGemmArgs &a, hipStream_t stream) {
   constexpr int BM = WM * FM * 32, BC = WN * FN * 32 / (SWIGLU ? 2 : 1);
-  const long long items = mx_tiles(a, BM) * (((SWIGLU ? a.N / 2 : a.N) + BC - 1) / BC);
+  const long long items = most_tiles(a, BM) * (((SWIGLU ? a.N / 2 : a.N) + BC - 1) / BC);
   // as many workgroups as run at a time, each walking over its tiles
   constexpr int PER_CU = sizeof(MxTileLds<FP8, false, WN * FN * 32, BM>) > 80 * 1024 ? 1 : 2;
   const long long slots = (long long)device_cu_count() * PER_CU;

@@ -63,6 +63,12 @@ class MxDesc(ctypes.Structure):
     _fields_ = [("codes", _vp), ("scales", _vp), ("rows", _i32), ("K", _i32), ("format", _i32)]
 
 
+class LoraDesc(ctypes.Structure):
+    """moesq_lora_t."""
+    _fields_ = [("a", _vp), ("b", _vp), ("scale", _vp), ("adapters", _i32), ("rank", _i32),
+                ("slices", _i32), ("N", _i32), ("K", _i32)]
+
+
 def _sig(name, restype, *argtypes):
     f = getattr(_lib, name)
     f.restype = restype
@@ -101,6 +107,13 @@ _rmsnorm = _sig("moesq_rmsnorm", _i32, _vp, _vp, _vp, _i32, _i32, ctypes.c_doubl
                 _vp, _vp, _vp)
 _mx_gemm = _sig("moesq_mx_gemm", _i32, ctypes.POINTER(MxDesc), _vp, _i32, _i32, _vp, _i32,
                 ctypes.POINTER(MxDesc), _i32, _i32, _vp, _vp)
+_gemm = _sig("moesq_gemm", _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp)
+_gemm_dx = _sig("moesq_gemm_dx", _i32, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _vp, _vp)
+_gemm_dw = _sig("moesq_gemm_dw", _i32, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp,
+                _vp)
+_unpermute_bw = _sig("moesq_unpermute_backward", _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp)
+_lora = _sig("moesq_lora", _i32, _vp, _vp, _i32, ctypes.POINTER(LoraDesc), _vp, _i32, _vp, _vp, _sz, _vp)
+_lora_ws = _sig("moesq_lora_workspace_bytes", _sz, _i32, ctypes.POINTER(LoraDesc))
 _status_string = _sig("moesq_status_string", ctypes.c_char_p, _i32)
 _last_error = _sig("moesq_last_error", ctypes.c_char_p)
 _version = _sig("moesq_version", _i32)
@@ -113,7 +126,8 @@ EXPORTED = ["moesq_route", "moesq_route_workspace_bytes", "moesq_route_noalloc",
             "moesq_pack_weights", "moesq_pack_weights_paired", "moesq_tile_weights",
             "moesq_decode_weights",
             "moesq_gate_topk", "moesq_mx_quantize", "moesq_mx_decode", "moesq_rmsnorm",
-            "moesq_mx_gemm",
+            "moesq_mx_gemm", "moesq_gemm", "moesq_gemm_dx", "moesq_gemm_dw", "moesq_unpermute_backward",
+            "moesq_lora", "moesq_lora_workspace_bytes",
             "moesq_validate", "moesq_stream_read", "moesq_status_string",
             "moesq_last_error", "moesq_version"]
 
@@ -304,6 +318,41 @@ class Mx:
         codes = torch.empty(shape + (K // 2 if format == ROWS_MXFP4 else K,), dtype=torch.uint8, device=device)
         scales = torch.empty(shape + (K // 32,), dtype=torch.uint8, device=device)
         return Mx.__new__(Mx)._set(codes, scales, format, shape, K)
+
+
+class Lora:
+    """Low-rank adapters of one projection: a bfloat16 [adapters, slices*rank, K],
+    b bfloat16 [adapters, N, rank], scale float32 [adapters].  Their contents may
+    change (an adapter is loaded into its place), the tensors stay the ones it
+    was made with."""
+
+    a = property(lambda self: self._a)
+    b = property(lambda self: self._b)
+    scale = property(lambda self: self._scale)
+
+    def __init__(self, a, b, scale, slices: int = 1):
+        if a.dim() != 3 or b.dim() != 3 or slices < 1 or a.shape[1] != slices * b.shape[2]:
+            raise ValueError(f"need a [adapters, slices * rank, K] and b [adapters, N, rank], got "
+                             f"{tuple(a.shape)} and {tuple(b.shape)} with slices = {slices}")
+        self.adapters, self.N, self.rank = (int(n) for n in b.shape)
+        self.K, self.slices = int(a.shape[2]), int(slices)
+        if a.shape[0] != self.adapters or tuple(scale.shape) != (self.adapters,):
+            raise ValueError(f"a has {a.shape[0]} adapters, scale {tuple(scale.shape)}, b {self.adapters}")
+        self._a, self._b, self._scale = a, b, scale
+        self._desc = None
+
+    def _described(self):
+        """(descriptor, device), checked and made at the first use."""
+        if self._desc is None:
+            for n, name in ((self.adapters, "adapters"), (self.N, "N"), (self.K, "K")):
+                _count(n, name)
+            n = self.adapters * self.rank
+            dev, (a, b, scale) = _pointers(
+                (self.a, torch.bfloat16, n * self.slices * self.K, "a"), (self.b, torch.bfloat16, n * self.N, "b"),
+                (self.scale, torch.float32, self.adapters, "scale"))
+            self._desc = ctypes.byref(LoraDesc(a, b, scale, self.adapters, self.rank, self.slices, self.N,
+                                               self.K)), dev
+        return self._desc
 
 
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
@@ -545,12 +594,12 @@ def moesq_gate_topk(logits, T: int, E: int, bias, gate: Gate, n_rows, topk_ids, 
 
 
 def _one_device(dev, *rows):
-    """The descriptors of Mx rows, which have to be on the call's device."""
+    """The descriptors of Mx rows or adapters, which have to be on the call's device."""
     found = []
     for q in rows:
         desc, d = q._described()
         if d is not None and dev is not None and d != dev:
-            raise ValueError("the rows are on another device than the other tensors")
+            raise ValueError(f"{type(q).__name__} is on another device than the other tensors")
         found.append(desc)
     return found
 
@@ -607,6 +656,72 @@ def moesq_mx_gemm(x: Mx, perm, T: int, k: int, expert_offsets, M: int, w: Mx, E:
         (y, torch.bfloat16, M * (N // 2 if (epilogue & ~OUT_FLAT) == EPI_SWIGLU else N), "y"))
     xd, wd = _one_device(dev, x, w)
     _launch(dev, stream, _mx_gemm, xd, p, T, k, off, M, wd, E, epilogue, yp)
+
+
+def _swiglu(epilogue):
+    return (epilogue & ~OUT_FLAT) == EPI_SWIGLU
+
+
+def _counts(*named):
+    for n, name in named:
+        _count(n, name)
+
+
+def moesq_gemm(x, perm, T: int, k: int, expert_offsets, M: int, w, E: int, N: int, K: int, epilogue: int, y,
+               z=None, stream=None):
+    _counts((T, "T"), (k, "k"), (M, "M"), (E, "E"), (N, "N"), (K, "K"))
+    bf, i32 = torch.bfloat16, torch.int32
+    dev, (xp, p, off, wp, yp, zp) = _pointers(
+        (x, bf, (T if perm is not None else M) * K, "x"), (perm, i32, M, "perm"),
+        (expert_offsets, i32, E + 1, "expert_offsets"), (w, bf, E * N * K, "w"),
+        (y, bf, M * (N // 2 if _swiglu(epilogue) else N), "y"), (z, bf, M * N, "z"))
+    _launch(dev, stream, _gemm, xp, p, T, k, off, M, wp, E, N, K, epilogue, yp, zp)
+
+
+def moesq_gemm_dx(dy, expert_offsets, M: int, w, E: int, N: int, K: int, z, dx, stream=None):
+    _counts((M, "M"), (E, "E"), (N, "N"), (K, "K"))
+    bf = torch.bfloat16
+    dev, (d, off, wp, zp, o) = _pointers(
+        (dy, bf, M * N, "dy"), (expert_offsets, torch.int32, E + 1, "expert_offsets"), (w, bf, E * N * K, "w"),
+        (z, bf, 2 * M * K, "z"), (dx, bf, (1 if z is None else 2) * M * K, "dx"))
+    _launch(dev, stream, _gemm_dx, d, off, M, wp, E, N, K, zp, o)
+
+
+def moesq_gemm_dw(dy, x, perm, T: int, k: int, expert_offsets, M: int, E: int, N: int, K: int, dw,
+                  accumulate: bool = False, stream=None):
+    """The type of dw (float32 or bfloat16) is the call's dtype."""
+    dtype = _dtype(dw, "dw")
+    _counts((T, "T"), (k, "k"), (M, "M"), (E, "E"), (N, "N"), (K, "K"))
+    bf, i32 = torch.bfloat16, torch.int32
+    dev, (d, xp, p, off, o) = _pointers(
+        (dy, bf, M * N, "dy"), (x, bf, (T if perm is not None else M) * K, "x"), (perm, i32, M, "perm"),
+        (expert_offsets, i32, E + 1, "expert_offsets"), (dw, dw.dtype, E * N * K, "dw"))
+    _launch(dev, stream, _gemm_dw, d, xp, p, T, k, off, M, E, N, K, dtype, int(bool(accumulate)), o)
+
+
+def moesq_unpermute_backward(dout, y, inv_perm, topk_weights, T: int, k: int, N: int, dy, dw, stream=None):
+    _counts((T, "T"), (k, "k"), (N, "N"))
+    bf, f32, M = torch.bfloat16, torch.float32, T * k
+    dev, (d, yp, inv, w, o, ow) = _pointers(
+        (dout, bf, T * N, "dout"), (y, bf, M * N, "y"), (inv_perm, torch.int32, M, "inv_perm"),
+        (topk_weights, f32, M, "topk_weights"), (dy, bf, M * N, "dy"), (dw, f32, M, "dw"))
+    _launch(dev, stream, _unpermute_bw, d, yp, inv, w, T, k, N, o, ow)
+
+
+def moesq_lora_workspace_bytes(T: int, adapters: Lora) -> int:
+    _count(T, "T")
+    return int(_lora_ws(T, adapters._described()[0]))
+
+
+def moesq_lora(x, ids, T: int, adapters: Lora, base, epilogue: int, y, ws, stream=None):
+    _count(T, "T")
+    bf, N = torch.bfloat16, adapters.N
+    dev, (xp, i, b, o, w) = _pointers(
+        (x, bf, T * adapters.K, "x"), (ids, torch.int32, T, "ids"), (base, bf, T * N, "base"),
+        (y, bf, T * (N // 2 if epilogue == EPI_SWIGLU else N), "y"),
+        (ws, torch.uint8, 0 if ws is None else ws.numel(), "ws"))
+    desc = _one_device(dev, adapters)
+    _launch(dev, stream, _lora, xp, i, T, desc[0], b, epilogue, o, w, 0 if ws is None else ws.numel())
 
 
 VALIDATE_CHECKS = ("ids", "offsets", "masks", "scales", "global_scales")
@@ -863,3 +978,109 @@ def mx_gemm(x: Mx, w: Mx, expert_offsets=None, perm=None, k: int = 1, epilogue: 
     moesq_mx_gemm(x, perm, x.rows if perm is not None else 0, k, expert_offsets, M, w, E, epilogue, out,
                   stream)
     return out
+
+
+def _out(out, shape, like):
+    if out is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"out must be {list(shape)}, got {tuple(out.shape)}")
+    return out
+
+
+def _experts(w):
+    """(E, N, K) of weights [E, N, K], or of one matrix [N, K]."""
+    if w.dim() not in (2, 3):
+        raise ValueError(f"w must be [E, N, K] or [N, K], got {tuple(w.shape)}")
+    return (1, *w.shape) if w.dim() == 2 else tuple(w.shape)
+
+
+def _rows(x, K, name):
+    if x.dim() != 2 or (K is not None and x.shape[1] != K):
+        raise ValueError(f"{name} must be [rows, {'columns' if K is None else K}], got {tuple(x.shape)}")
+    return x.shape[0]
+
+
+def gemm(x, w, expert_offsets=None, perm=None, k: int = 1, epilogue: int = EPI_NONE, save: bool = False,
+         out=None, stream=None):
+    """Product of bfloat16 rows with bfloat16 weights: dense (w [N, K] or
+    [1, N, K], no expert_offsets), or grouped over the E experts of w [E, N, K].
+    With `perm`, routed row r reads row perm[r] // k of x; else x's rows are the
+    routed rows.  With EPI_SWIGLU and `save`, returns (y, z): z [rows, N] are the
+    projections before the activation, for gemm_dx."""
+    if stream is not None:
+        with _current(stream, x):
+            return gemm(x, w, expert_offsets, perm, k, epilogue, save, out)
+    E, N, K = _experts(w)
+    T = _rows(x, K, "x")
+    M = T * k if perm is not None else T
+    y = _out(out, (M, N // 2 if _swiglu(epilogue) else N), x)
+    z = torch.empty(M, N, dtype=torch.bfloat16, device=x.device) if save else None
+    moesq_gemm(x, perm, T if perm is not None else 0, k, expert_offsets, M, w, E, N, K, epilogue, y, z)
+    return (y, z) if save else y
+
+
+def gemm_dx(dy, w, expert_offsets=None, z=None, out=None, stream=None):
+    """Gradient of the (routed) rows of gemm from that of its result dy [rows, N]:
+    [rows, K].  With z [rows, 2K], the projections that a gated block made these
+    rows from, the gradient of z instead (`out` may be z)."""
+    if stream is not None:
+        with _current(stream, dy):
+            return gemm_dx(dy, w, expert_offsets, z, out)
+    E, N, K = _experts(w)
+    M = _rows(dy, N, "dy")
+    dx = _out(out, (M, K if z is None else 2 * K), dy)
+    moesq_gemm_dx(dy, expert_offsets, M, w, E, N, K, z, dx)
+    return dx
+
+
+def gemm_dw(dy, x, expert_offsets=None, E: int = 1, perm=None, k: int = 1, out=None, accumulate: bool = False,
+            dtype=torch.bfloat16, stream=None):
+    """Gradient of the weights of gemm, [E, N, K], from that of its result
+    dy [rows, N] (routed rows) and its rows x (with `perm`, the tokens).  `out`,
+    if given, sets the type; with `accumulate` (float32) the gradient is added to it."""
+    if stream is not None:
+        with _current(stream, dy):
+            return gemm_dw(dy, x, expert_offsets, E, perm, k, out, accumulate, dtype)
+    M, T = _rows(dy, None, "dy"), _rows(x, None, "x")
+    N, K = dy.shape[1], x.shape[1]
+    if M != (T * k if perm is not None else T):
+        raise ValueError(f"dy has {M} rows, x {T} with k = {k}")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty(E, N, K, dtype=dtype, device=dy.device)
+    elif tuple(out.shape) != (E, N, K) and (E > 1 or tuple(out.shape) != (N, K)):
+        raise ValueError(f"out must be {[E, N, K]}, got {tuple(out.shape)}")
+    moesq_gemm_dw(dy, x, perm, T if perm is not None else 0, k, expert_offsets, M, E, N, K, out, accumulate)
+    return out
+
+
+def unpermute_backward(dout, y, inv_perm, topk_weights, T: int, k: int, dy: bool = True, dw: bool = True,
+                       stream=None):
+    """Gradients of unpermute with weights from that of its result dout [T, N]:
+    (dy [T*k, N] in routed order, dw float32 [T*k]); None for one not wanted."""
+    if stream is not None:
+        with _current(stream, dout):
+            return unpermute_backward(dout, y, inv_perm, topk_weights, T, k, dy, dw)
+    if _rows(dout, None, "dout") != T:
+        raise ValueError(f"dout must be [T = {T}, N], got {tuple(dout.shape)}")
+    N = dout.shape[1]
+    gy = torch.empty(T * k, N, dtype=torch.bfloat16, device=dout.device) if dy else None
+    gw = torch.empty(T * k, dtype=torch.float32, device=dout.device) if dw else None
+    moesq_unpermute_backward(dout, y, inv_perm, topk_weights, T, k, N, gy, gw)
+    return gy, gw
+
+
+def lora(x, adapters: Lora, ids, base=None, epilogue: int = EPI_NONE, out=None, stream=None):
+    """base + scale * (x a') b' with row t's adapter ids[t] (int32; a row with an
+    id outside [0, adapters) has none), [T, N], or its SwiGLU, [T, N/2].  `base`
+    [T, N]: the shared projection's result, zeros if None; `out` may be base."""
+    if stream is not None:
+        with _current(stream, x):
+            return lora(x, adapters, ids, base, epilogue, out)
+    T = _rows(x, adapters.K, "x")
+    y = _out(out, (T, adapters.N // 2 if epilogue == EPI_SWIGLU else adapters.N), x)
+    ws = torch.empty(moesq_lora_workspace_bytes(T, adapters), dtype=torch.uint8, device=x.device)
+    moesq_lora(x, ids, T, adapters, base, epilogue, y, ws)
+    return y
