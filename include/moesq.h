@@ -522,8 +522,8 @@ moesq_status_t moesq_mx_gemm(const moesq_mx_t *x, const int32_t *perm, int32_t T
  *   sums).  Not with epilogue NONE, not with MOESQ_OUT_FLAT.
  * All buffers 16-byte aligned; y and z overlap no input and not each other.
  * Limits: N % 8 == 0, K % 8 == 0 (SWIGLU: N % 16 == 0), N, K <= MOESQ_GEMM_MAX_DIM,
- *         N*K < 2^31, 1 <= E <= MOESQ_MAX_EXPERTS, 0 <= M <= 2^30; with perm the
- *         tokens under 4 GiB (T*K <= 2^31 - 8).
+ *         1 <= E <= MOESQ_MAX_EXPERTS, 0 <= M <= 2^30; an expert's weights and, with
+ *         perm, the tokens under 4 GiB (N*K and T*K at most 2^31 - 2^16).
  */
 #define MOESQ_GEMM_MAX_DIM (1 << 20)
 moesq_status_t moesq_gemm(const uint16_t *x, const int32_t *perm, int32_t T, int32_t k,

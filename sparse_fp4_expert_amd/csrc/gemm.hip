@@ -10,6 +10,7 @@
 // P is the first operand of the MFMA, Q the second: a lane's results are
 // neighbouring columns of one row.
 #include <type_traits>
+#include <utility>
 
 #include "row_tiles.hpp"
 
@@ -23,6 +24,7 @@ struct GemmArgs {
   int k, M, E, N, K;
   int flat;
   bool out32, accumulate;
+  uint32_t k_mul, k_shift;     // n / k = (n * k_mul) >> (32 + k_shift) for k > 1 and n < 2^31
 };
 
 enum { GEMM_FWD = 0, GEMM_DX = 1, GEMM_DW = 2 };
@@ -34,136 +36,520 @@ __device__ __forceinline__ void swiglu_grad(float d, float g, float u, float &dg
   du = d * (g * s);
 }
 
-constexpr int ST = 64, SC = 32, SPITCH = SC + 8;   // tile, positions a step, row of LDS
+// ------------------------------------------------------------------ tiled kernel
+//
+// A workgroup computes BP columns x BQ rows.  Stages of 64 positions of both
+// operands are copied to LDS, two in turn, and contracted in two steps of 32 on
+// the 16 x 16 x 32 MFMA.  (On that of 32 x 32 x 16 two waves of a SIMD lose a third of the
+// rate: 147 us for 99 in a loop of MFMAs alone, and on random values 165 for 120, where
+// power sets the clock.)  The one barrier of a stage is early in its second step, behind the
+// stage's reads: it hands the stage's buffer to the copies of the stage after the next and
+// says that the next has landed.  An operand of the next step is read into the
+// registers of this step's as soon as its MFMAs are issued (P), or into a
+// second set (Q).
+//
+// Every vector instruction beside the MFMAs takes time from them, so the loop has
+// none but what a gather needs: it is unrolled over the two buffers, so that reads
+// have constant offsets; copies go by the load's own offset, which counts in
+// memory and in LDS, and the offsets of positions that are not there are changed
+// once, before the last stages.
+//
+// An operand whose positions are contiguous lies in LDS as rows of 128 bytes
+// (piece4).  Of one whose other index is contiguous, position by position,
+// BP (BQ) elements each; the transposing read of LDS gives a lane four
+// positions of its column, in groups of 16 lanes that read 4 positions x 32
+// bytes.  The 16-byte chunks of a position are permuted so that the positions that
+// are read together touch all 64 banks.
+//
+// Nothing is read behind a row or a buffer: copies whose position, row or column
+// is not there are sent out of the buffer's range, which makes them zeros in LDS.
 
-// A simple kernel: 64 x 64 results a workgroup, operands through LDS element
-// by element.
-template <int WHAT, bool SWIGLU>
-__global__ __launch_bounds__(256) void gemm_simple_kernel(GemmArgs a) {
-  __shared__ __attribute__((aligned(16))) uint16_t P[ST * SPITCH], Q[ST * SPITCH];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  constexpr bool GATE = WHAT == GEMM_FWD && SWIGLU;
-  const int cols = WHAT == GEMM_FWD ? (SWIGLU ? a.N / 2 : a.N) : a.K;
-  constexpr int BC = GATE ? ST / 2 : ST;
-  const int nt = (cols + BC - 1) / BC;
-  int e, row0, rows, c0 = (blockIdx.x % nt) * BC, C;
-  long long lo = 0;
-  if constexpr (WHAT == GEMM_DW) {
-    const int qt = (a.N + ST - 1) / ST, rest = blockIdx.x / nt;
-    e = rest / qt;
-    row0 = rest % qt * ST;
-    rows = min(ST, a.N - row0);
-    const int2 r = a.offsets ? rows_of(a, e) : make_int2(0, a.M);
-    lo = r.x;
-    C = max(r.y - r.x, 0);
-  } else {
-    const RowTile t = find_tile<ST>(a, blockIdx.x / nt, lane);
-    if (t.e < 0) return;
-    e = t.e, row0 = t.row0, rows = t.rows;
-    C = WHAT == GEMM_FWD ? a.K : a.N;
-  }
-  const uint16_t *w = WHAT == GEMM_DW ? nullptr : a.w + (size_t)e * a.N * a.K;
-  auto column = [&](int p) {   // column of the result (GATE: row of w) of row p of the tile, or -1
-    if constexpr (GATE) {
-      const int c = c0 + (p >> 5) * 16 + (p & 15);
-      return c < cols ? c + ((p >> 4) & 1) * cols : -1;
-    }
-    return c0 + p < cols ? c0 + p : -1;
-  };
-  f32x4_t acc[2][2] = {};
-  for (int k0 = 0; k0 < C; k0 += SC) {
-    for (int i = threadIdx.x; i < ST * SC; i += 256) {
-      // the index that is contiguous in memory runs over the threads
-      const int p = WHAT == GEMM_FWD ? i / SC : i % ST, pc = WHAT == GEMM_FWD ? i % SC : i / ST;
-      const int q = WHAT == GEMM_DW ? i % ST : i / SC, qc = WHAT == GEMM_DW ? i / ST : i % SC;
-      uint16_t vp = 0, vq = 0;
-      if (const int n = column(p); n >= 0 && k0 + pc < C) {
-        if constexpr (WHAT == GEMM_FWD) vp = w[(size_t)n * a.K + k0 + pc];
-        if constexpr (WHAT == GEMM_DX) vp = w[(size_t)(k0 + pc) * a.K + n];
-        if constexpr (WHAT == GEMM_DW) {
-          const int s = src_row(a, (int)lo + k0 + pc);
-          if (s >= 0) vp = a.x[(size_t)s * a.K + n];
-        }
-      }
-      if (q < rows && k0 + qc < C) {
-        if constexpr (WHAT == GEMM_FWD) {
-          const int s = src_row(a, row0 + q);
-          if (s >= 0) vq = a.x[(size_t)s * a.K + k0 + qc];
-        }
-        if constexpr (WHAT == GEMM_DX) vq = a.dy[(size_t)(row0 + q) * a.N + k0 + qc];
-        if constexpr (WHAT == GEMM_DW) vq = a.dy[(size_t)(lo + k0 + qc) * a.N + row0 + q];
-      }
-      P[p * SPITCH + pc] = vp;
-      Q[q * SPITCH + qc] = vq;
-    }
-    __syncthreads();
-    bf16x8_t op[2], oq[2];
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const int at = (16 * f + (lane & 15)) * SPITCH + 8 * (lane >> 4);
-      op[f] = as_bf16x8(*reinterpret_cast<const uint4 *>(P + (wave & 1) * 32 * SPITCH + at));
-      oq[f] = as_bf16x8(*reinterpret_cast<const uint4 *>(Q + (wave >> 1) * 32 * SPITCH + at));
-    }
-#pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int g = 0; g < 2; ++g) acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(op[f], oq[g], acc[f][g], 0, 0, 0);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const int q = (wave >> 1) * 32 + 16 * g + (lane & 15);
-    if (q >= rows) continue;
-    const int r = row0 + q;
-#pragma unroll
-    for (int f = 0; f < (GATE ? 1 : 2); ++f) {
-      const int c = GATE ? c0 + (wave & 1) * 16 + 4 * (lane >> 4) : c0 + (wave & 1) * 32 + 16 * f + 4 * (lane >> 4);
-      if (c >= cols) continue;
-      const f32x4_t v = acc[f][g], u = acc[1][g];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (WHAT == GEMM_FWD) {
-          const int dst = dst_row(a, r);
-          if (dst >= 0) a.y[(size_t)dst * cols + c + i] = (uint16_t)bf16_bits_rne(GATE ? silu_f32(v[i]) * u[i] : v[i]);
-          if (GATE && a.z) {
-            a.z[(size_t)r * a.N + c + i] = (uint16_t)bf16_bits_rne(v[i]);
-            a.z[(size_t)r * a.N + cols + c + i] = (uint16_t)bf16_bits_rne(u[i]);
-          }
-        }
-        if constexpr (WHAT == GEMM_DX) {
-          if constexpr (SWIGLU) {
-            uint16_t *o = a.y + (size_t)r * 2 * cols + c + i;
-            const uint16_t *z = a.zin + (size_t)r * 2 * cols + c + i;
-            float dg, du;
-            swiglu_grad(v[i], bf16_lo(z[0]), bf16_lo(z[cols]), dg, du);
-            o[0] = (uint16_t)bf16_bits_rne(dg);
-            o[cols] = (uint16_t)bf16_bits_rne(du);
-          } else {
-            a.y[(size_t)r * cols + c + i] = (uint16_t)bf16_bits_rne(v[i]);
-          }
-        }
-        if constexpr (WHAT == GEMM_DW) {
-          const size_t at = ((size_t)e * a.N + r) * cols + c + i;
-          float *o = reinterpret_cast<float *>(a.y) + at;
-          if (!a.out32) a.y[at] = (uint16_t)bf16_bits_rne(v[i]);
-          else *o = a.accumulate ? *o + v[i] : v[i];
-        }
-      }
-    }
-  }
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+// Buffers cover all that an offset of 32 bits reaches up to here, and a copy
+// from this offset is behind them (whether or not the check of the range counts the load's own).
+constexpr uint32_t NOWHERE = 0xffff0000u;
+
+// 16 bytes a lane to LDS, at lds + OFF + 16 * lane; the load's own offset counts
+// in memory too.
+template <int OFF>
+__device__ __forceinline__ void copy16_to_lds_at(uint32_t lds, i32x4_t buf, uint32_t voff) {
+  static_assert(OFF >= 0 && OFF < 4096, "twelve bits (the assembler drops others without an error)");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen offset:%3 lds" ::"s"(lds),
+               "v"(voff), "s"(buf), "n"(OFF)
+               : "memory");
 }
 
+template <typename F, int... I>
+__device__ __forceinline__ void for_each_in(std::integer_sequence<int, I...>, F &&f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+// f(0), ..., f(N - 1), with constants.
+template <int N, typename F>
+__device__ __forceinline__ void for_each(F &&f) {
+  for_each_in(std::make_integer_sequence<int, N>{}, f);
+}
+
+// The buffer, moved on by `by` bytes.
+__device__ __forceinline__ i32x4_t moved(i32x4_t b, uint64_t by) {
+  const uint64_t u = ((uint64_t)(uint32_t)b[1] << 32 | (uint32_t)b[0]) + by;
+  b[0] = (int)(uint32_t)u;
+  b[1] = (int)(uint32_t)(u >> 32);
+  return b;
+}
+
+// Chunk of position r at which chunk 0 of a row of B elements lies (the
+// others likewise, by exclusive or).
+template <int B>
+__device__ __forceinline__ int chunk_turn(int r) {
+  return (B >= 128 ? (r & 3) << 2 : (r & 2) << 1) | ((r >> 3) & 1) << 1;
+}
+
+// WP waves over the columns (FP fragments of 16 each), WQ over the rows (FQ).
+template <int WHAT, bool SWIGLU, bool GATHER, int WP, int WQ, int FP, int FQ>
+__global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2) void gemm_tiled_kernel(GemmArgs a) {
+  constexpr bool GATE = WHAT == GEMM_FWD && SWIGLU;
+  constexpr bool PT = WHAT != GEMM_FWD, QT = WHAT == GEMM_DW;    // position by position
+  constexpr int WAVES = WP * WQ, BP = WP * FP * 16, BQ = WQ * FQ * 16;
+  constexpr int PB = BP * 128, QB = BQ * 128;                    // bytes of a stage
+  constexpr int CP = PB / 1024 / WAVES, CQ = QB / 1024 / WAVES;
+  static_assert(CP >= 1 && CQ >= 1 && WAVES % 2 == 0 && BP % 64 == 0 && BQ % 64 == 0, "whole copies");
+  // Results leave 16 rows x W columns at a time, in fp32, through a wave's own part of LDS.
+  constexpr int OF = GATE ? FP / 2 : FP, PF = OF < 4 ? OF : 4, W = PF * 16;
+  struct Lds {
+    uint8_t p[2][PB], q[2][QB];
+    float out[WAVES][16 * W];
+  };
+  __shared__ __attribute__((aligned(1024))) Lds lds;
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = lane >> 4, rl = lane & 15;         // eight positions, row or column of a fragment
+  const int wp = wave % WP, wq = wave / WP;
+  const int cols = WHAT == GEMM_FWD ? (SWIGLU ? a.N / 2 : a.N) : a.K;
+  constexpr int BC = GATE ? BP / 2 : BP;           // output columns of a tile
+  const int nt = (cols + BC - 1) / BC;
+
+  // The tiles.  The workgroups of one XCD (every eighth) take a run of them, row
+  // tiles in fours and those before column tiles, so that those running at a time
+  // share panels of both operands in its L2; each walks the run by the number of
+  // them.  (Gradients of many experts' weights have nothing to share.)
+  struct Tile {
+    int e, row0, rows, c0, lo, C;                  // rows [row0, row0 + rows) of expert e, columns from c0; C positions, from lo on (dw)
+  };
+  const int qt = WHAT == GEMM_DW ? (a.N + BQ - 1) / BQ : __builtin_amdgcn_readfirstlane(count_tiles<BQ>(a, lane));
+  const int each = qt * nt, items = WHAT == GEMM_DW ? each * a.E : each;
+  const bool runs = WHAT != GEMM_DW || a.E == 1;
+  const int run = (items + 7) >> 3, stride = runs ? (int)gridDim.x >> 3 : (int)gridDim.x;
+  int item = runs ? (int)(blockIdx.x & 7) * run + (int)(blockIdx.x >> 3) : (int)blockIdx.x;
+  const int last = runs ? min(items, ((int)(blockIdx.x & 7) + 1) * run) : items;
+  if (item >= last) return;
+  auto look_up = [&](int n) {
+    Tile t;
+    t.e = WHAT == GEMM_DW ? n / each : 0;
+    const int in_e = n - t.e * each;
+    const int first = in_e / (4 * nt) * 4, in = in_e - first * nt, four = min(4, qt - first);
+    const int r = first + in % four;
+    t.c0 = in / four * BC;
+    if constexpr (WHAT == GEMM_DW) {
+      t.row0 = r * BQ;
+      t.rows = min(BQ, a.N - t.row0);
+      const int2 of = a.offsets ? rows_of(a, t.e) : make_int2(0, a.M);
+      t.lo = __builtin_amdgcn_readfirstlane(of.x);
+      t.C = __builtin_amdgcn_readfirstlane(max(of.y - of.x, 0));
+    } else {
+      const RowTile rt = find_tile<BQ>(a, r, lane);
+      t.e = max(__builtin_amdgcn_readfirstlane(rt.e), 0);   // (offsets that changed meanwhile: no rows)
+      t.row0 = __builtin_amdgcn_readfirstlane(rt.row0);
+      t.rows = __builtin_amdgcn_readfirstlane(rt.rows);
+      t.lo = 0;
+      t.C = WHAT == GEMM_FWD ? a.K : a.N;
+    }
+    return t;
+  };
+
+  // Sources of this lane's copies: offsets from a buffer that moves on by a
+  // stage.  Copies 4i to 4i + 3 of a wave go to neighbouring kilobytes of LDS by the
+  // load's own offset, so their sources are that much less (and all of them, and the
+  // buffer's start, BIAS apart).
+  const int K = a.K, N = a.N;
+  constexpr uint32_t BIAS = 3 * 1024;
+  constexpr int LP = BP / 8, LQ = BQ / 8;          // lanes a position
+  i32x4_t pbuf, qbuf;
+  uint64_t pstep = 128, qstep = 128;
+  uint32_t poff[CP], qoff[CQ];
+  // First position that copy i of this lane takes.
+  auto ppos = [&](int i) { return PT ? (wave * CP + i) * (64 / LP) + lane / LP : 8 * piece4((wave * CP + i) * 8 + (lane >> 3), lane & 7); };
+  auto qpos = [&](int i) { return QT ? (wave * CQ + i) * (64 / LQ) + lane / LQ : 8 * piece4((wave * CQ + i) * 8 + (lane >> 3), lane & 7); };
+  Tile t = look_up(item);
+  auto from = [](const void *p, uint32_t bias) { return raw_buffer(static_cast<const uint8_t *>(p) - bias, NOWHERE); };
+  uint32_t pcol[GATHER ? CP : 1];
+  // Copies' sources of tile t.
+  auto set_up = [&] {
+    if constexpr (PT) {
+      pbuf = from(WHAT == GEMM_DX ? a.w + (size_t)t.e * N * K : a.x + (GATHER ? (size_t)0 : (size_t)t.lo * K), BIAS);
+      pstep = GATHER ? 0 : (uint64_t)K * 128;
+#pragma unroll
+      for (int i = 0; i < CP; ++i) {
+        const int r = ppos(i), c = t.c0 + 8 * (lane % LP ^ chunk_turn<BP>(r));
+        poff[i] = c < cols ? (GATHER ? (uint32_t)c * 2 : ((uint32_t)r * K + c) * 2) + BIAS - i % 4 * 1024 : NOWHERE;
+      }
+    } else {
+      pbuf = from(a.w + (size_t)t.e * N * K, BIAS);
+#pragma unroll
+      for (int i = 0; i < CP; ++i) {
+        // GATE: the first half of a wave's t.rows are gate t.rows, the second half the
+        // up t.rows of the same columns.  (Columns that are not there read another
+        // row, and their results are not used.)
+        constexpr int H = FP * 8;
+        const int r = (wave * CP + i) * 8 + (lane >> 3);
+        const int in = r % (2 * H), c = GATE ? t.c0 + r / (2 * H) * H + in % H : t.c0 + r;
+        const uint32_t n = (uint32_t)min(c, cols - 1) + (GATE && in >= H ? cols : 0);
+        poff[i] = (n * (uint32_t)K + ppos(i)) * 2 + BIAS - i % 4 * 1024;
+      }
+    }
+    if constexpr (QT) {
+      qbuf = from(a.dy + (size_t)t.lo * N, BIAS);
+      qstep = (uint64_t)N * 128;
+#pragma unroll
+      for (int i = 0; i < CQ; ++i) {
+        const int r = qpos(i), c = t.row0 + 8 * (lane % LQ ^ chunk_turn<BQ>(r));
+        qoff[i] = c < N ? ((uint32_t)r * N + c) * 2 + BIAS - i % 4 * 1024 : NOWHERE;
+      }
+    } else {
+      const bool direct = WHAT == GEMM_DX || !a.perm;
+      qbuf = from(WHAT == GEMM_DX ? a.dy + (size_t)t.row0 * N : direct ? a.x + (size_t)t.row0 * K : a.x, BIAS);
+#pragma unroll
+      for (int i = 0; i < CQ; ++i) {
+        const int r = (wave * CQ + i) * 8 + (lane >> 3);
+        const int src = r >= t.rows ? -1 : direct ? r : src_row(a, t.row0 + r);
+        qoff[i] = src < 0 ? NOWHERE : ((uint32_t)src * (uint32_t)t.C + qpos(i)) * 2 + BIAS - i % 4 * 1024;
+      }
+    }
+    if constexpr (GATHER)
+#pragma unroll
+      for (int i = 0; i < CP; ++i) pcol[i] = poff[i];
+  };
+  // Gathered positions: the rows of the copies of a stage.
+  int psrc[GATHER ? CP : 1];
+  auto load_src = [&](int s) {
+    if constexpr (GATHER)
+#pragma unroll
+      for (int i = 0; i < CP; ++i) {
+        const int r = 64 * s + ppos(i);
+        psrc[i] = r < t.C ? a.perm[t.lo + r] : -1;
+      }
+  };
+  auto use_src = [&] {
+    if constexpr (GATHER)
+#pragma unroll
+      for (int i = 0; i < CP; ++i) {
+        const uint32_t q = a.k == 1 ? psrc[i] : __umulhi((uint32_t)psrc[i], a.k_mul) >> a.k_shift;
+        poff[i] = psrc[i] >= 0 && psrc[i] < a.M && pcol[i] != NOWHERE ? q * (uint32_t)K * 2 + pcol[i] : NOWHERE;
+      }
+  };
+
+  // Copy i of a stage (P and Q in turn) into buffer `slot`, and the step to the
+  // next stage, of which `left` positions are there.
+  const uint32_t plds = lds_offset(lds.p[0]) + wave * CP * 1024, qlds = lds_offset(lds.q[0]) + wave * CQ * 1024;
+  auto copy = [&](auto i, int slot) {
+    constexpr int I = decltype(i)::value, B = 2 * (CP < CQ ? CP : CQ);
+    constexpr bool OF_P = I < B ? I % 2 == 0 : CP > CQ;
+    constexpr int J = I < B ? I / 2 : I - B / 2;
+    if constexpr (OF_P)
+      copy16_to_lds_at<J % 4 * 1024>(plds + slot * PB + J / 4 * 4096, pbuf, poff[J]);
+    else
+      copy16_to_lds_at<J % 4 * 1024>(qlds + slot * QB + J / 4 * 4096, qbuf, qoff[J]);
+  };
+  auto next_p = [&](int left) {
+    pbuf = moved(pbuf, pstep);
+    if (!GATHER && left < 64)
+#pragma unroll
+      for (int i = 0; i < CP; ++i) poff[i] = ppos(i) < left ? poff[i] : NOWHERE;
+  };
+  auto next_q = [&](int left) {
+    qbuf = moved(qbuf, qstep);
+    if (left < 64)
+#pragma unroll
+      for (int i = 0; i < CQ; ++i) qoff[i] = qpos(i) < left ? qoff[i] : NOWHERE;
+  };
+
+  // Operand of fragment f (of 16 columns or rows), positions [32k, 32k + 32) of a stage.
+  auto operand = [&](const uint8_t *base, auto trans, auto width, int f, int k) -> bf16x8_t {
+    constexpr int B = decltype(width)::value;
+    if constexpr (decltype(trans)::value) {
+      const int r = 8 * h + (rl >> 2), ch = 2 * f + ((rl & 3) >> 1);
+      const uint8_t *at = base + (32 * k + r) * B * 2 + ((ch ^ chunk_turn<B>(r)) << 4) + 8 * (rl & 1);
+      typedef __attribute__((address_space(3))) s16x4_t *lds_ptr;
+      const s16x4_t u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)at);
+      const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + 4 * B * 2));
+      return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      const int r = 16 * f + rl;
+      return as_bf16x8(*reinterpret_cast<const uint4 *>(base + r * 128 + 16 * piece4(r, 4 * k + h)));
+    }
+  };
+  bf16x8_t P[FP], Q[2][FQ];
+  auto read_p = [&](int f, int slot, int k) {
+    P[f] = operand(lds.p[slot], std::bool_constant<PT>{}, std::integral_constant<int, BP>{}, wp * FP + f, k);
+  };
+  auto read_q = [&](int g, int slot, int k) {
+    Q[k][g] = operand(lds.q[slot], std::bool_constant<QT>{}, std::integral_constant<int, BQ>{}, wq * FQ + g, k);
+  };
+  f32x4_t acc[FP][FQ];
+  bool busy;                                       // this wave has results in the tile
+  // MFMAs [M0, M1) of step k, with work(j) behind each.
+  auto mfmas = [&](auto m0, auto m1, int k, auto &&work) {
+    for_each<decltype(m1)::value - decltype(m0)::value>([&](auto n) {
+      constexpr int j = decltype(m0)::value + decltype(n)::value, f = j / FQ, g = j % FQ;
+      acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(P[f], Q[k][g], acc[f][g], 0, 0, 0);
+      work(std::integral_constant<int, j>{});
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  // this wave's copies have landed and its reads are done; then every wave's
+  auto arrive = [&] {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  // Of the second step's MFMAS, those of AF fragments of P (ARRIVE) are before the barrier;
+  // behind it a copy follows every EVERY.  (Copies one behind the other keep the wave from its
+  // MFMAS until the address unit has taken them: on zeros, 4096 x 4096 x 7168, 153 us with all of
+  // them at once, 150 every third in pairs, 146 every fifth in pairs, 139 so.)
+  constexpr int MFMAS = FP * FQ, AF = 1, ARRIVE = AF * FQ, COPIES = CP + CQ, EVERY = (MFMAS - ARRIVE) / COPIES;
+  static_assert(EVERY >= 1, "a copy behind an MFMA at most");
+  constexpr std::integral_constant<int, 0> i0{};
+  constexpr std::integral_constant<int, ARRIVE> mid{};
+  constexpr std::integral_constant<int, MFMAS> end{};
+  // Reads of the next step's operands (in buffer `slot`, step k) behind MFMA j:
+  // Q and the AF fragments of P that are done by then in turn, every second
+  // one, and each other fragment of P behind its own MFMAs.
+  auto reads = [&](auto jc, auto af, int slot, int k) {
+    constexpr int j = decltype(jc)::value, A = decltype(af)::value, n = j - A * FQ, f = j / FQ;
+    if constexpr (n % 2 == 0 && n / 2 < FQ + A) {
+      constexpr int i = n / 2;
+      if constexpr (i >= 2 * A) read_q(i - A, slot, k);
+      else if constexpr (i & 1) read_p(i / 2, slot, k);
+      else read_q(i / 2, slot, k);
+    }
+    if constexpr (f > A && j % FQ == 1) read_p(f - 1, slot, k);
+    if constexpr (j == MFMAS - 1) read_p(f, slot, k);
+  };
+  // Stage s, in buffer `slot`.
+  auto stage = [&](int s, auto slot) {
+    constexpr int S = decltype(slot)::value;
+    load_src(s + 2);
+    if (busy) {
+      mfmas(i0, end, 0, [&](auto j) { reads(j, i0, S, 1); });
+      mfmas(i0, mid, 1, [&](auto) {});
+    }
+    arrive();
+    use_src();
+    if (busy) {
+      // (behind the last stage, operands are read for nothing)
+      mfmas(mid, end, 1, [&](auto j) {
+        constexpr int n = decltype(j)::value - ARRIVE;
+        reads(j, std::integral_constant<int, AF>{}, S ^ 1, 0);
+        if constexpr (n % EVERY == EVERY / 2 && n / EVERY < COPIES) copy(std::integral_constant<int, n / EVERY>{}, S);
+      });
+    } else {
+      for_each<COPIES>([&](auto i) { copy(i, S); });
+    }
+    next_p(t.C - 64 * (s + 3));
+    next_q(t.C - 64 * (s + 3));
+  };
+
+  // The first copies of tile t: stages 0 and 1.
+  auto start = [&] {
+    set_up();
+    load_src(0);
+    use_src();
+    // (the first stage may be a partial one)
+    pbuf = moved(pbuf, 0 - pstep), next_p(t.C);
+    qbuf = moved(qbuf, 0 - qstep), next_q(t.C);
+    for_each<COPIES>([&](auto i) { copy(i, 0); });
+    next_p(t.C - 64), next_q(t.C - 64);
+    load_src(1);
+    use_src();
+    for_each<COPIES>([&](auto i) { copy(i, 1); });
+    next_p(t.C - 128), next_q(t.C - 128);
+  };
+  start();
+  while (true) {
+    // the next tile is looked up while the first copies are in flight, and its own
+    // first copies while this one's results are stored
+    const int next = item + stride;
+    Tile nxt = t;
+    if (next < last) nxt = look_up(next);
+    busy = wq * FQ * 16 < t.rows && t.c0 + wp * (BC / WP) < cols;
+#pragma unroll
+    for (int f = 0; f < FP; ++f)
+#pragma unroll
+      for (int g = 0; g < FQ; ++g) acc[f][g] = f32x4_t{0, 0, 0, 0};
+    arrive();
+    if (busy) {
+#pragma unroll
+      for (int g = 0; g < FQ; ++g) read_q(g, 0, 0);
+#pragma unroll
+      for (int f = 0; f < FP; ++f) read_p(f, 0, 0);
+    }
+    const int stages = (t.C + 63) / 64;
+    for (int s = 0; s < stages; s += 2) {
+      stage(s, i0);
+      if (s + 1 < stages) stage(s + 1, std::integral_constant<int, 1>{});
+    }
+    const Tile done = t;
+    const bool results = busy;
+    if (next < last) {
+      // every wave is done with the buffers: its last reads were before the last barrier (without
+      // stages, the first), and its copies behind the end, zeros, have landed
+      wait_copies<0>();
+      if (stages == 0) arrive();
+      t = nxt;
+      start();
+    }
+    // Results.  A lane stores eight neighbouring columns of a row, a wave whole lines.
+    constexpr int L = W / 8, STORES = 16 * L / 64;   // lanes a row, rows 64 / L apart
+    static_assert(64 % L == 0 && STORES >= 1 && OF % PF == 0, "whole rows");
+    float *mine = lds.out[wave];
+    auto turn = [](int row, int four) { return four ^ (row & (W < 64 ? W / 8 - 1 : 7)) << 1; };   // 16-byte chunks of a row
+    // (a wave's accesses to LDS happen in order; the compiler, which sees one
+    // lane's addresses, has to keep that order)
+    auto put = [&](auto &&value) {
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int f = 0; f < PF; ++f)
+        *reinterpret_cast<f32x4_t *>(mine + rl * W + 4 * turn(rl, 4 * f + h)) = value(f);
+      asm volatile("" ::: "memory");
+    };
+    auto pack = [](f32x4_t u, f32x4_t v) {
+      return make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    };
+    for_each<FQ * OF / PF>([&](auto nc) {
+      constexpr int g = decltype(nc)::value / (OF / PF), f0 = decltype(nc)::value % (OF / PF) * PF;
+      if (!results) return;
+      __builtin_amdgcn_sched_barrier(0);
+      auto each = [&](auto &&store) {              // store(row of the tile, column, eight values)
+#pragma unroll
+        for (int i = 0; i < STORES; ++i) {
+          const int row = i * (64 / L) + lane / L, ch = lane % L * 2;
+          const f32x4_t u = *reinterpret_cast<const f32x4_t *>(mine + row * W + 4 * turn(row, ch));
+          const f32x4_t v = *reinterpret_cast<const f32x4_t *>(mine + row * W + 4 * turn(row, ch + 1));
+          const int q = (wq * FQ + g) * 16 + row, c = done.c0 + (wp * OF + f0) * 16 + 4 * ch;
+          if (q < done.rows && c < cols) store(done.row0 + q, c, u, v);
+        }
+      };
+      if constexpr (GATE)
+        put([&](int f) {
+          f32x4_t v;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = silu_f32(acc[f0 + f][g][j]) * acc[f0 + f + OF][g][j];
+          return v;
+        });
+      else
+        put([&](int f) { return acc[f0 + f][g]; });
+      each([&](int r, int c, f32x4_t u, f32x4_t v) {   // r: routed row (dw: row of the matrix)
+        if constexpr (WHAT == GEMM_FWD) {
+          const int dst = a.perm ? dst_row(a, r) : r;
+          const bool zero = a.perm && src_row(a, r) < 0;
+          if (dst >= 0)
+            *reinterpret_cast<uint4 *>(a.y + (size_t)dst * cols + c) = zero ? make_uint4(0, 0, 0, 0) : pack(u, v);
+        } else if constexpr (WHAT == GEMM_DW) {
+          const size_t at = ((size_t)done.e * N + r) * cols + c;
+          if (a.out32) {
+            f32x4_t *o = reinterpret_cast<f32x4_t *>(reinterpret_cast<float *>(a.y) + at);
+            o[0] = a.accumulate ? o[0] + u : u;
+            o[1] = a.accumulate ? o[1] + v : v;
+          } else {
+            *reinterpret_cast<uint4 *>(a.y + at) = pack(u, v);
+          }
+        } else if constexpr (SWIGLU) {
+          const size_t at = (size_t)r * 2 * cols + c;
+          const uint4 zg = *reinterpret_cast<const uint4 *>(a.zin + at);
+          const uint4 zu = *reinterpret_cast<const uint4 *>(a.zin + at + cols);
+          const uint32_t gw[4] = {zg.x, zg.y, zg.z, zg.w}, uw[4] = {zu.x, zu.y, zu.z, zu.w};
+          f32x4_t og[2], ou[2];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float gj = j & 1 ? bf16_hi(gw[j / 2]) : bf16_lo(gw[j / 2]), uj = j & 1 ? bf16_hi(uw[j / 2]) : bf16_lo(uw[j / 2]);
+            float dg, du;
+            swiglu_grad(j < 4 ? u[j & 3] : v[j & 3], gj, uj, dg, du);
+            og[j / 4][j & 3] = dg, ou[j / 4][j & 3] = du;
+          }
+          *reinterpret_cast<uint4 *>(a.y + at) = pack(og[0], og[1]);
+          *reinterpret_cast<uint4 *>(a.y + at + cols) = pack(ou[0], ou[1]);
+        } else {
+          *reinterpret_cast<uint4 *>(a.y + (size_t)r * cols + c) = pack(u, v);
+        }
+      });
+      if constexpr (GATE) {
+        if (a.z) {
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            put([&](int f) { return acc[f0 + f + part * OF][g]; });
+            each([&](int r, int c, f32x4_t u, f32x4_t v) {
+              *reinterpret_cast<uint4 *>(a.z + (size_t)r * N + part * cols + c) = pack(u, v);
+            });
+          }
+        }
+      }
+    });
+    if (next >= last) break;
+    item = next;
+  }
+  wait_copies<0>();
+}
+
+template <int WHAT, bool SWIGLU, int WP, int WQ, int FP, int FQ>
+static void launch_tiled(const GemmArgs &a, hipStream_t stream) {
+  constexpr int BQ = WQ * FQ * 16, BC = WP * FP * 16 / (WHAT == GEMM_FWD && SWIGLU ? 2 : 1);
+  const int cols = WHAT == GEMM_FWD ? (SWIGLU ? a.N / 2 : a.N) : a.K;
+  const long long tiles = WHAT == GEMM_DW ? (long long)a.E * ((a.N + BQ - 1) / BQ) : most_tiles(a, BQ);
+  // As many workgroups as run at a time, each walking over its tiles.  Gradients of
+  // many experts' weights, tiles of unequal length, get a workgroup each (E = 128, 1536 x 2048:
+  // 480 us for 655).
+  constexpr int THREADS = WP * WQ * 64, PER_CU = THREADS == 512 ? 1 : 2;
+  const long long items = tiles * ((cols + BC - 1) / BC);
+  const long long slots = WHAT == GEMM_DW && a.E > 1 ? MAX_LAUNCH_THREADS / THREADS : (long long)device_cu_count() * PER_CU;
+  const dim3 grid((unsigned)((std::min(items, slots) + 7) & ~7ll)), block(THREADS);
+  if (WHAT == GEMM_DW && a.perm)
+    hipLaunchKernelGGL((gemm_tiled_kernel<WHAT, SWIGLU, WHAT == GEMM_DW, WP, WQ, FP, FQ>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((gemm_tiled_kernel<WHAT, SWIGLU, false, WP, WQ, FP, FQ>), grid, block, 0, stream, a);
+}
+
+// The tile, from the time that the workgroups' rounds take by it (us a stage; the host knows the
+// experts' average rows only).  Measured per stage of 64 positions, one and two workgroups on a CU:
+// 256 x 256 1.5; 128 x 128 0.5 and 0.9; 128 x 64 0.4 and 0.65.  Measured, us:
+//                                                     256 x 256  128 x 128  128 x 64
+//   8192 x 4096 x 7168                                      339        418       564
+//   its rows' gradient, 4096 rows (448 tiles in two rounds) 185        212       294
+//   4096 rows' through a block of 2048 (128 tiles)          144        110       152
+//   128 experts of 1536 x 2048, 256 uneven rows each        359        354       429
+//   the same, 128 rows each                                 266        244       275
+//   777 x 1536 x 2048                                        41         23        20
 template <int WHAT, bool SWIGLU>
 static moesq_status_t launch_gemm(const GemmArgs &a, hipStream_t stream, const char *who) {
-  const int cols = WHAT == GEMM_FWD ? (SWIGLU ? a.N / 2 : a.N) : a.K, bc = WHAT == GEMM_FWD && SWIGLU ? ST / 2 : ST;
-  const long long tiles = WHAT == GEMM_DW ? (long long)a.E * ((a.N + ST - 1) / ST) : most_tiles(a, ST);
-  hipLaunchKernelGGL((gemm_simple_kernel<WHAT, SWIGLU>), dim3((unsigned)(tiles * ((cols + bc - 1) / bc))), dim3(256), 0, stream, a);
+  const int n = WHAT == GEMM_FWD ? a.N : a.K, cus = device_cu_count();
+  const int experts = WHAT == GEMM_DW ? a.E : std::min(a.E, a.M), rows = WHAT == GEMM_DW ? a.N : (a.M + experts - 1) / experts;
+  // `first`: of one round that leaves every workgroup a CU of its own
+  auto time = [&](int bp, int bq, int per_cu, float first, float round) {
+    const long long tiles = (long long)experts * ((rows + bq - 1) / bq) * ((n + bp - 1) / bp), slots = (long long)cus * per_cu;
+    return tiles <= cus ? first : (float)((tiles + slots - 1) / slots) * round;
+  };
+  const float large = time(256, 256, 1, 1.5f, 1.5f), mid = time(128, 128, 2, 0.5f, 0.9f), small = time(128, 64, 2, 0.4f, 0.65f);
+  if (large <= mid && large <= small) launch_tiled<WHAT, SWIGLU, 2, 4, 8, 4>(a, stream);
+  else if (mid <= small) launch_tiled<WHAT, SWIGLU, 2, 2, 4, 4>(a, stream);
+  else launch_tiled<WHAT, SWIGLU, 2, 2, 4, 2>(a, stream);
   return launch_status(who);
 }
 
 // ------------------------------------------------------------------ checks
 
 constexpr int32_t GEMM_MAX_ROWS = 1 << 30;   // rows of tiles, the last one partial, are counted in 32 bits
+
+constexpr long long GEMM_MAX_ELEMENTS = (1ll << 31) - (1 << 16);   // of an expert or of gathered tokens: below NOWHERE
 
 static moesq_status_t check_sizes(const std::string &who, const int32_t *offsets, int32_t M, int32_t E, int32_t N,
                                   int32_t K) {
@@ -172,7 +558,8 @@ static moesq_status_t check_sizes(const std::string &who, const int32_t *offsets
   if (N < 8 || N % 8 || N > MOESQ_GEMM_MAX_DIM || K < 8 || K % 8 || K > MOESQ_GEMM_MAX_DIM)
     return fail(MOESQ_ERR_SHAPE, who + ": N and K must be positive multiples of 8, at most " +
                                      std::to_string(MOESQ_GEMM_MAX_DIM));
-  if ((long long)N * K >= (1ll << 31)) return fail(MOESQ_ERR_SHAPE, who + ": an expert's weights must stay under 4 GiB");
+  if ((long long)N * K > GEMM_MAX_ELEMENTS)
+    return fail(MOESQ_ERR_SHAPE, who + ": an expert's weights must stay under 4 GiB");
   if (M < 0 || M > GEMM_MAX_ROWS)
     return fail(MOESQ_ERR_SHAPE, who + ": M must be in [0, " + std::to_string(GEMM_MAX_ROWS) + "]");
   if (!offsets && E != 1) return fail(MOESQ_ERR_NULL, who + ": expert_offsets may be NULL only with E == 1");
@@ -184,10 +571,20 @@ static moesq_status_t check_gather(const std::string &who, const int32_t *perm, 
   if (!perm) return MOESQ_OK;
   if (T < 0 || k < 1 || (long long)T * k != M)
     return fail(MOESQ_ERR_SHAPE, who + ": a gather needs T >= 0, k >= 1 and M == T*k");
-  if ((long long)T * K > (1ll << 31) - 8)
+  if ((long long)T * K > GEMM_MAX_ELEMENTS)
     return fail(MOESQ_ERR_SHAPE, who + ": tokens that are gathered must stay under 4 GiB");
   if (!offsets) return fail(MOESQ_ERR_NULL, who + ": a gather needs expert_offsets");
   return MOESQ_OK;
+}
+
+// n / k by a multiplication: with s = ceil(log2 k) and m = floor(2^(31+s) / k) + 1, n m / 2^(31+s)
+// exceeds n / k by less than 1 / k for n < 2^31.
+static void set_division(GemmArgs &a, int k) {
+  a.k = k;
+  if (k < 2) return;
+  const int s = 32 - __builtin_clz((unsigned)(k - 1));
+  a.k_mul = (uint32_t)((1ull << (31 + s)) / (unsigned)k + 1);
+  a.k_shift = s - 1;
 }
 
 template <typename... Ps>
@@ -256,7 +653,8 @@ extern "C" moesq_status_t moesq_gemm_dw(const uint16_t *dy, const uint16_t *x, c
   if (misaligned(dy, x, dw)) return fail(MOESQ_ERR_ARG, who + ": dy, x and dw must be 16-byte aligned");
   GemmArgs a{};
   a.dy = dy, a.x = x, a.perm = perm, a.offsets = expert_offsets, a.y = static_cast<uint16_t *>(dw);
-  a.k = k, a.M = M, a.E = E, a.N = N, a.K = K;
+  a.M = M, a.E = E, a.N = N, a.K = K;
+  set_division(a, k);
   a.out32 = dtype == MOESQ_F32, a.accumulate = accumulate != 0;
   return launch_gemm<GEMM_DW, false>(a, stream, "moesq_gemm_dw");
 }
