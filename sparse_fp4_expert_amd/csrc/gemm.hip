@@ -24,6 +24,7 @@ struct GemmArgs {
   int k, M, E, N, K;
   int flat;
   bool out32, accumulate;
+  int item0;                   // first item of this launch: row tile (streaming kernel) or tile (dw)
   uint32_t k_mul, k_shift;     // n / k = (n * k_mul) >> (32 + k_shift) for k > 1 and n < 2^31
 };
 
@@ -34,6 +35,178 @@ __device__ __forceinline__ void swiglu_grad(float d, float g, float u, float &dg
   const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
   dg = d * u * (s * (1.0f + g * (1.0f - s)));
   du = d * (g * s);
+}
+
+// Buffers cover all that an offset of 32 bits reaches up to here, and a copy
+// from this offset is behind them (whether or not the check of the range counts the load's own).
+constexpr uint32_t NOWHERE = 0xffff0000u;
+
+template <typename F, int... I>
+__device__ __forceinline__ void for_each_in(std::integer_sequence<int, I...>, F &&f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+// f(0), ..., f(N - 1), with constants.
+template <int N, typename F>
+__device__ __forceinline__ void for_each(F &&f) {
+  for_each_in(std::make_integer_sequence<int, N>{}, f);
+}
+
+// ------------------------------------------------------------------ streaming kernel
+//
+// The product of few rows: bound by the stream of weights.  A wave contracts FN
+// fragments of 16 weight rows with FM of 16 rows of x in stages of 64 positions,
+// copied to a ring of its own in LDS, DEPTH stages deep: whole lines, and all of
+// them under way at once.  No wave waits for another but for the final sum: KSPLIT
+// waves of a workgroup share their rows, each with its own stages, and add their
+// sums in LDS in a fixed order.  Stages that are not there are copied as zeros, so that
+// the counts of copies in flight are constants.
+//
+// SwiGLU: rows 0-7 of a fragment are gate rows, 8-15 the up rows of the same
+// eight columns.
+constexpr int stream_waves(int ksplit) { return ksplit < 4 ? 4 : ksplit; }
+
+template <bool SWIGLU, int KSPLIT, int FN, int FM, int DEPTH>
+__global__ __launch_bounds__(stream_waves(KSPLIT) * 64) void gemm_stream_kernel(GemmArgs a) {
+  constexpr int WAVES = stream_waves(KSPLIT), RG = WAVES / KSPLIT;   // row groups of FN fragments a workgroup
+  constexpr int FC = SWIGLU ? 8 : 16;              // output columns a fragment
+  constexpr int WC = FN * 2, XC = FM * 2;          // copies of a stage
+  struct Ring {
+    uint8_t w[FN * 16 * 128], x[FM * 16 * 128];
+  };
+  __shared__ __attribute__((aligned(1024))) Ring ring[WAVES][DEPTH];
+  static_assert(sizeof(ring) >= WAVES * FM * 64 * sizeof(f32x4_t), "sums fit into the rings");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, rl = lane & 15;
+  const int cols = SWIGLU ? a.N / 2 : a.N, K = a.K;
+  const int groups = ((cols + FC - 1) / FC + RG * FN - 1) / (RG * FN);
+  const RowTile t = find_tile<16 * FM>(a, a.item0 + blockIdx.x / groups, lane);
+  if (t.e < 0) return;
+  const int kw = wave % KSPLIT;
+  const int c0 = ((blockIdx.x % groups) * RG + wave / KSPLIT) * FN * FC;
+  const int n = ((K + 63) / 64 - kw + KSPLIT - 1) / KSPLIT;   // this wave's stages: kw, kw + KSPLIT, ...
+  const uint32_t lds0 = lds_offset(&ring[wave][0]);
+  // copy i of a stage takes piece `pos` / 8 of rows 8i to 8i + 7
+  auto pos = [&](int i) { return 8 * piece4(8 * i + (lane >> 3), lane & 7); };
+  const i32x4_t wbuf = raw_buffer(a.w + (size_t)t.e * a.N * K, NOWHERE);
+  uint32_t wo[WC], xo[XC];
+#pragma unroll
+  for (int i = 0; i < WC; ++i) {
+    // (columns that are not there read another row, and their results are not used)
+    const int r = 8 * i + (lane >> 3), c = min(c0 + (r >> 4) * FC + (SWIGLU ? r & 7 : r & 15), cols - 1);
+    wo[i] = ((uint32_t)(c + (SWIGLU && (r & 8) ? cols : 0)) * (uint32_t)K + pos(i)) * 2;
+  }
+  auto fetch_w = [&](int slot, int c) {
+#pragma unroll
+    for (int i = 0; i < WC; ++i)
+      copy16_to_lds(lds0 + slot * (uint32_t)sizeof(Ring) + i * 1024, wbuf, 64 * c + pos(i) < K ? wo[i] + 128 * c : NOWHERE);
+  };
+  // the first weights are under way before the rows are looked up
+#pragma unroll
+  for (int i = 0; i < DEPTH; ++i) fetch_w(i, kw + i * KSPLIT);
+  const bool direct = !a.perm;
+  const i32x4_t xbuf = raw_buffer(direct ? a.x + (size_t)t.row0 * K : a.x, NOWHERE);
+#pragma unroll
+  for (int i = 0; i < XC; ++i) {
+    const int r = 8 * i + (lane >> 3), from = r >= t.rows ? -1 : direct ? r : src_row(a, t.row0 + r);
+    xo[i] = from < 0 ? NOWHERE : ((uint32_t)from * (uint32_t)K + pos(i)) * 2;
+  }
+  auto fetch_x = [&](int slot, int c) {
+#pragma unroll
+    for (int i = 0; i < XC; ++i)
+      copy16_to_lds(lds0 + slot * (uint32_t)sizeof(Ring) + (WC + i) * 1024, xbuf,
+                    64 * c + pos(i) < K && xo[i] != NOWHERE ? xo[i] + 128 * c : NOWHERE);
+  };
+#pragma unroll
+  for (int i = 0; i < DEPTH; ++i) fetch_x(i, kw + i * KSPLIT);
+
+  f32x4_t acc[FN][FM];
+#pragma unroll
+  for (int f = 0; f < FN; ++f)
+#pragma unroll
+    for (int g = 0; g < FM; ++g) acc[f][g] = f32x4_t{0, 0, 0, 0};
+  // contracts this wave's stage i, in its slot, and refills that
+  auto contract = [&](int i, int slot) {
+    const Ring &k = ring[wave][slot];
+    auto operand = [&](const uint8_t *p, int f, int s) {
+      const int r = 16 * f + rl;
+      return as_bf16x8(*reinterpret_cast<const uint4 *>(p + r * 128 + 16 * piece4(r, 4 * s + q)));
+    };
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      bf16x8_t X[FM];
+#pragma unroll
+      for (int g = 0; g < FM; ++g) X[g] = operand(k.x, g, s);
+#pragma unroll
+      for (int f = 0; f < FN; ++f) {
+        const bf16x8_t W = operand(k.w, f, s);
+#pragma unroll
+        for (int g = 0; g < FM; ++g) acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(W, X[g], acc[f][g], 0, 0, 0);
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot's reads are done before it is written again
+    fetch_w(slot, kw + (i + DEPTH) * KSPLIT);
+    fetch_x(slot, kw + (i + DEPTH) * KSPLIT);
+  };
+  // of the first stages, the weights of all were copied before the rows of any
+  for_each<DEPTH>([&](auto ic) {
+    constexpr int i = decltype(ic)::value;
+    if (i >= n) return;
+    wait_copies<XC * (DEPTH - 1 - i) + (WC + XC) * i>();
+    contract(i, i);
+  });
+  for (int i = DEPTH; i < n; ++i) {
+    wait_copies<(WC + XC) * (DEPTH - 1)>();
+    contract(i, i % DEPTH);
+  }
+
+  // The KSPLIT waves' sums; the waves of a row group each finish some of its row fragments.
+  f32x4_t *part = reinterpret_cast<f32x4_t *>(&ring[0][0]);     // [waves][FM][64]
+  wait_copies<0>();
+#pragma unroll
+  for (int f = 0; f < FN; ++f) {
+    if constexpr (KSPLIT > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int g = 0; g < FM; ++g) part[(wave * FM + g) * 64 + lane] = acc[f][g];
+      __syncthreads();
+    }
+#pragma unroll
+    for (int g = 0; g < FM; ++g) {
+      if (KSPLIT > 1 && g % KSPLIT != kw) continue;
+      f32x4_t v = acc[f][g];
+      if constexpr (KSPLIT > 1) {
+        v = part[((wave - kw) * FM + g) * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < KSPLIT; ++w) v += part[((wave - kw + w) * FM + g) * 64 + lane];
+      }
+      f32x4_t h = v;
+      if constexpr (SWIGLU) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = silu_f32(v[i]) * __shfl_down(v[i], 32, 64);
+      }
+      const int r = 16 * g + rl, c = c0 + f * FC + 4 * (SWIGLU ? q & 1 : q);
+      if (r >= t.rows || c >= cols) continue;
+      const int dst = dst_row(a, t.row0 + r);
+      if (dst >= 0 && (!SWIGLU || q < 2))
+        *reinterpret_cast<uint2 *>(a.y + (size_t)dst * cols + c) = make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+      if (SWIGLU && a.z)
+        *reinterpret_cast<uint2 *>(a.z + (size_t)(t.row0 + r) * a.N + (q < 2 ? 0 : cols) + c) =
+            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    }
+  }
+}
+
+template <bool SWIGLU, int KSPLIT, int FN, int FM, int DEPTH>
+static void launch_stream(GemmArgs a, hipStream_t stream) {
+  constexpr int THREADS = stream_waves(KSPLIT) * 64;
+  const int cols = SWIGLU ? a.N / 2 : a.N, frags = (cols + (SWIGLU ? 7 : 15)) / (SWIGLU ? 8 : 16);
+  const int rg = stream_waves(KSPLIT) / KSPLIT * FN, groups = (frags + rg - 1) / rg;
+  const long long tiles = most_tiles(a, 16 * FM), part = std::max(1, MAX_LAUNCH_THREADS / THREADS / groups);
+  for (long long first = 0; first < tiles; first += part) {
+    a.item0 = (int)first;
+    hipLaunchKernelGGL((gemm_stream_kernel<SWIGLU, KSPLIT, FN, FM, DEPTH>), dim3((unsigned)(std::min(part, tiles - first) * groups)),
+                       dim3(THREADS), 0, stream, a);
+  }
 }
 
 // ------------------------------------------------------------------ tiled kernel
@@ -66,10 +239,6 @@ __device__ __forceinline__ void swiglu_grad(float d, float g, float u, float &dg
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
-// Buffers cover all that an offset of 32 bits reaches up to here, and a copy
-// from this offset is behind them (whether or not the check of the range counts the load's own).
-constexpr uint32_t NOWHERE = 0xffff0000u;
-
 // 16 bytes a lane to LDS, at lds + OFF + 16 * lane; the load's own offset counts
 // in memory too.
 template <int OFF>
@@ -80,14 +249,11 @@ __device__ __forceinline__ void copy16_to_lds_at(uint32_t lds, i32x4_t buf, uint
                : "memory");
 }
 
-template <typename F, int... I>
-__device__ __forceinline__ void for_each_in(std::integer_sequence<int, I...>, F &&f) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-// f(0), ..., f(N - 1), with constants.
-template <int N, typename F>
-__device__ __forceinline__ void for_each(F &&f) {
-  for_each_in(std::make_integer_sequence<int, N>{}, f);
+// The lane number as the compiler cannot know it, so that what follows from it is
+// computed where it is used and holds no registers through a kernel's main loop.
+__device__ __forceinline__ int fresh(int lane) {
+  asm volatile("" : "+v"(lane));
+  return lane;
 }
 
 // The buffer, moved on by `by` bytes.
@@ -106,7 +272,7 @@ __device__ __forceinline__ int chunk_turn(int r) {
 }
 
 // WP waves over the columns (FP fragments of 16 each), WQ over the rows (FQ).
-template <int WHAT, bool SWIGLU, bool GATHER, int WP, int WQ, int FP, int FQ>
+template <int WHAT, bool SWIGLU, bool GATHER, bool WALK, int WP, int WQ, int FP, int FQ>
 __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2) void gemm_tiled_kernel(GemmArgs a) {
   constexpr bool GATE = WHAT == GEMM_FWD && SWIGLU;
   constexpr bool PT = WHAT != GEMM_FWD, QT = WHAT == GEMM_DW;    // position by position
@@ -114,11 +280,12 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
   constexpr int PB = BP * 128, QB = BQ * 128;                    // bytes of a stage
   constexpr int CP = PB / 1024 / WAVES, CQ = QB / 1024 / WAVES;
   static_assert(CP >= 1 && CQ >= 1 && WAVES % 2 == 0 && BP % 64 == 0 && BQ % 64 == 0, "whole copies");
-  // Results leave 16 rows x W columns at a time, in fp32, through a wave's own part of LDS.
-  constexpr int OF = GATE ? FP / 2 : FP, PF = OF < 4 ? OF : 4, W = PF * 16;
+  // Results leave 16 rows at a time through a wave's own part of LDS: W columns in
+  // fp32 where they are not yet the output's bf16, else all WB columns of the wave.
+  constexpr int OF = GATE ? FP / 2 : FP, PF = OF < 4 ? OF : 4, W = PF * 16, WB = OF * 16;
   struct Lds {
     uint8_t p[2][PB], q[2][QB];
-    float out[WAVES][16 * W];
+    float out[WAVES][16 * W];                      // (or 16 * WB of bf16)
   };
   __shared__ __attribute__((aligned(1024))) Lds lds;
 
@@ -132,7 +299,7 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
 
   // The tiles.  The workgroups of one XCD (every eighth) take a run of them, row
   // tiles in fours and those before column tiles, so that those running at a time
-  // share panels of both operands in its L2; each walks the run by the number of
+  // share panels of both operands in its L2; with WALK, each walks the run by the number of
   // them.  (Gradients of many experts' weights have nothing to share.)
   struct Tile {
     int e, row0, rows, c0, lo, C;                  // rows [row0, row0 + rows) of expert e, columns from c0; C positions, from lo on (dw)
@@ -141,7 +308,7 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
   const int each = qt * nt, items = WHAT == GEMM_DW ? each * a.E : each;
   const bool runs = WHAT != GEMM_DW || a.E == 1;
   const int run = (items + 7) >> 3, stride = runs ? (int)gridDim.x >> 3 : (int)gridDim.x;
-  int item = runs ? (int)(blockIdx.x & 7) * run + (int)(blockIdx.x >> 3) : (int)blockIdx.x;
+  int item = runs ? (int)(blockIdx.x & 7) * run + (int)(blockIdx.x >> 3) : a.item0 + (int)blockIdx.x;
   const int last = runs ? min(items, ((int)(blockIdx.x & 7) + 1) * run) : items;
   if (item >= last) return;
   auto look_up = [&](int n) {
@@ -179,19 +346,20 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
   uint64_t pstep = 128, qstep = 128;
   uint32_t poff[CP], qoff[CQ];
   // First position that copy i of this lane takes.
-  auto ppos = [&](int i) { return PT ? (wave * CP + i) * (64 / LP) + lane / LP : 8 * piece4((wave * CP + i) * 8 + (lane >> 3), lane & 7); };
-  auto qpos = [&](int i) { return QT ? (wave * CQ + i) * (64 / LQ) + lane / LQ : 8 * piece4((wave * CQ + i) * 8 + (lane >> 3), lane & 7); };
+  auto ppos = [&](int i, int lane) { return PT ? (wave * CP + i) * (64 / LP) + lane / LP : 8 * piece4((wave * CP + i) * 8 + (lane >> 3), lane & 7); };
+  auto qpos = [&](int i, int lane) { return QT ? (wave * CQ + i) * (64 / LQ) + lane / LQ : 8 * piece4((wave * CQ + i) * 8 + (lane >> 3), lane & 7); };
   Tile t = look_up(item);
   auto from = [](const void *p, uint32_t bias) { return raw_buffer(static_cast<const uint8_t *>(p) - bias, NOWHERE); };
   uint32_t pcol[GATHER ? CP : 1];
   // Copies' sources of tile t.
   auto set_up = [&] {
+    const int ln = fresh(lane);
     if constexpr (PT) {
       pbuf = from(WHAT == GEMM_DX ? a.w + (size_t)t.e * N * K : a.x + (GATHER ? (size_t)0 : (size_t)t.lo * K), BIAS);
       pstep = GATHER ? 0 : (uint64_t)K * 128;
 #pragma unroll
       for (int i = 0; i < CP; ++i) {
-        const int r = ppos(i), c = t.c0 + 8 * (lane % LP ^ chunk_turn<BP>(r));
+        const int r = ppos(i, ln), c = t.c0 + 8 * (ln % LP ^ chunk_turn<BP>(r));
         poff[i] = c < cols ? (GATHER ? (uint32_t)c * 2 : ((uint32_t)r * K + c) * 2) + BIAS - i % 4 * 1024 : NOWHERE;
       }
     } else {
@@ -202,10 +370,10 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
         // up t.rows of the same columns.  (Columns that are not there read another
         // row, and their results are not used.)
         constexpr int H = FP * 8;
-        const int r = (wave * CP + i) * 8 + (lane >> 3);
+        const int r = (wave * CP + i) * 8 + (ln >> 3);
         const int in = r % (2 * H), c = GATE ? t.c0 + r / (2 * H) * H + in % H : t.c0 + r;
         const uint32_t n = (uint32_t)min(c, cols - 1) + (GATE && in >= H ? cols : 0);
-        poff[i] = (n * (uint32_t)K + ppos(i)) * 2 + BIAS - i % 4 * 1024;
+        poff[i] = (n * (uint32_t)K + ppos(i, ln)) * 2 + BIAS - i % 4 * 1024;
       }
     }
     if constexpr (QT) {
@@ -213,7 +381,7 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
       qstep = (uint64_t)N * 128;
 #pragma unroll
       for (int i = 0; i < CQ; ++i) {
-        const int r = qpos(i), c = t.row0 + 8 * (lane % LQ ^ chunk_turn<BQ>(r));
+        const int r = qpos(i, ln), c = t.row0 + 8 * (ln % LQ ^ chunk_turn<BQ>(r));
         qoff[i] = c < N ? ((uint32_t)r * N + c) * 2 + BIAS - i % 4 * 1024 : NOWHERE;
       }
     } else {
@@ -221,9 +389,9 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
       qbuf = from(WHAT == GEMM_DX ? a.dy + (size_t)t.row0 * N : direct ? a.x + (size_t)t.row0 * K : a.x, BIAS);
 #pragma unroll
       for (int i = 0; i < CQ; ++i) {
-        const int r = (wave * CQ + i) * 8 + (lane >> 3);
+        const int r = (wave * CQ + i) * 8 + (ln >> 3);
         const int src = r >= t.rows ? -1 : direct ? r : src_row(a, t.row0 + r);
-        qoff[i] = src < 0 ? NOWHERE : ((uint32_t)src * (uint32_t)t.C + qpos(i)) * 2 + BIAS - i % 4 * 1024;
+        qoff[i] = src < 0 ? NOWHERE : ((uint32_t)src * (uint32_t)t.C + qpos(i, ln)) * 2 + BIAS - i % 4 * 1024;
       }
     }
     if constexpr (GATHER)
@@ -236,7 +404,7 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
     if constexpr (GATHER)
 #pragma unroll
       for (int i = 0; i < CP; ++i) {
-        const int r = 64 * s + ppos(i);
+        const int r = 64 * s + ppos(i, lane);
         psrc[i] = r < t.C ? a.perm[t.lo + r] : -1;
       }
   };
@@ -263,15 +431,17 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
   };
   auto next_p = [&](int left) {
     pbuf = moved(pbuf, pstep);
-    if (!GATHER && left < 64)
+    if (GATHER || left >= 64) return;
+    const int ln = fresh(lane);
 #pragma unroll
-      for (int i = 0; i < CP; ++i) poff[i] = ppos(i) < left ? poff[i] : NOWHERE;
+    for (int i = 0; i < CP; ++i) poff[i] = ppos(i, ln) < left ? poff[i] : NOWHERE;
   };
   auto next_q = [&](int left) {
     qbuf = moved(qbuf, qstep);
-    if (left < 64)
+    if (left >= 64) return;
+    const int ln = fresh(lane);
 #pragma unroll
-      for (int i = 0; i < CQ; ++i) qoff[i] = qpos(i) < left ? qoff[i] : NOWHERE;
+    for (int i = 0; i < CQ; ++i) qoff[i] = qpos(i, ln) < left ? qoff[i] : NOWHERE;
   };
 
   // Operand of fragment f (of 16 columns or rows), positions [32k, 32k + 32) of a stage.
@@ -381,7 +551,7 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
     // first copies while this one's results are stored
     const int next = item + stride;
     Tile nxt = t;
-    if (next < last) nxt = look_up(next);
+    if (WALK && next < last) nxt = look_up(next);
     busy = wq * FQ * 16 < t.rows && t.c0 + wp * (BC / WP) < cols;
 #pragma unroll
     for (int f = 0; f < FP; ++f)
@@ -401,7 +571,7 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
     }
     const Tile done = t;
     const bool results = busy;
-    if (next < last) {
+    if (WALK && next < last) {
       // every wave is done with the buffers: its last reads were before the last barrier (without
       // stages, the first), and its copies behind the end, zeros, have landed
       wait_copies<0>();
@@ -411,7 +581,9 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
     }
     // Results.  A lane stores eight neighbouring columns of a row, a wave whole lines.
     constexpr int L = W / 8, STORES = 16 * L / 64;   // lanes a row, rows 64 / L apart
-    static_assert(64 % L == 0 && STORES >= 1 && OF % PF == 0, "whole rows");
+    constexpr int LB = WB / 8, STORESB = 16 * LB / 64;
+    static_assert(64 % L == 0 && 64 % LB == 0 && STORES >= 1 && OF % PF == 0 && WB <= 2 * W, "whole rows");
+    const int ln = fresh(lane);
     float *mine = lds.out[wave];
     auto turn = [](int row, int four) { return four ^ (row & (W < 64 ? W / 8 - 1 : 7)) << 1; };   // 16-byte chunks of a row
     // (a wave's accesses to LDS happen in order; the compiler, which sees one
@@ -420,125 +592,194 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
       asm volatile("" ::: "memory");
 #pragma unroll
       for (int f = 0; f < PF; ++f)
-        *reinterpret_cast<f32x4_t *>(mine + rl * W + 4 * turn(rl, 4 * f + h)) = value(f);
+        *reinterpret_cast<f32x4_t *>(mine + (ln & 15) * W + 4 * turn((ln & 15), 4 * f + (ln >> 4))) = value(f);
       asm volatile("" ::: "memory");
     };
     auto pack = [](f32x4_t u, f32x4_t v) {
       return make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     };
-    for_each<FQ * OF / PF>([&](auto nc) {
-      constexpr int g = decltype(nc)::value / (OF / PF), f0 = decltype(nc)::value % (OF / PF) * PF;
-      if (!results) return;
-      __builtin_amdgcn_sched_barrier(0);
-      auto each = [&](auto &&store) {              // store(row of the tile, column, eight values)
+    // 16 rows x WB columns of bf16, and store(row, column, eight of them).
+    uint16_t *mineb = reinterpret_cast<uint16_t *>(mine);
+    auto turnb = [](int row, int chunk) { return chunk ^ (row & (LB - 1)); };
+    auto whole = [&](int g, auto &&value, auto &&store) {
+      asm volatile("" ::: "memory");
 #pragma unroll
-        for (int i = 0; i < STORES; ++i) {
-          const int row = i * (64 / L) + lane / L, ch = lane % L * 2;
-          const f32x4_t u = *reinterpret_cast<const f32x4_t *>(mine + row * W + 4 * turn(row, ch));
-          const f32x4_t v = *reinterpret_cast<const f32x4_t *>(mine + row * W + 4 * turn(row, ch + 1));
-          const int q = (wq * FQ + g) * 16 + row, c = done.c0 + (wp * OF + f0) * 16 + 4 * ch;
-          if (q < done.rows && c < cols) store(done.row0 + q, c, u, v);
-        }
-      };
-      if constexpr (GATE)
-        put([&](int f) {
-          f32x4_t v;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = silu_f32(acc[f0 + f][g][j]) * acc[f0 + f + OF][g][j];
-          return v;
-        });
-      else
-        put([&](int f) { return acc[f0 + f][g]; });
-      each([&](int r, int c, f32x4_t u, f32x4_t v) {   // r: routed row (dw: row of the matrix)
-        if constexpr (WHAT == GEMM_FWD) {
-          const int dst = a.perm ? dst_row(a, r) : r;
-          const bool zero = a.perm && src_row(a, r) < 0;
-          if (dst >= 0)
-            *reinterpret_cast<uint4 *>(a.y + (size_t)dst * cols + c) = zero ? make_uint4(0, 0, 0, 0) : pack(u, v);
-        } else if constexpr (WHAT == GEMM_DW) {
-          const size_t at = ((size_t)done.e * N + r) * cols + c;
-          if (a.out32) {
-            f32x4_t *o = reinterpret_cast<f32x4_t *>(reinterpret_cast<float *>(a.y) + at);
-            o[0] = a.accumulate ? o[0] + u : u;
-            o[1] = a.accumulate ? o[1] + v : v;
-          } else {
-            *reinterpret_cast<uint4 *>(a.y + at) = pack(u, v);
-          }
-        } else if constexpr (SWIGLU) {
-          const size_t at = (size_t)r * 2 * cols + c;
-          const uint4 zg = *reinterpret_cast<const uint4 *>(a.zin + at);
-          const uint4 zu = *reinterpret_cast<const uint4 *>(a.zin + at + cols);
-          const uint32_t gw[4] = {zg.x, zg.y, zg.z, zg.w}, uw[4] = {zu.x, zu.y, zu.z, zu.w};
-          f32x4_t og[2], ou[2];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float gj = j & 1 ? bf16_hi(gw[j / 2]) : bf16_lo(gw[j / 2]), uj = j & 1 ? bf16_hi(uw[j / 2]) : bf16_lo(uw[j / 2]);
-            float dg, du;
-            swiglu_grad(j < 4 ? u[j & 3] : v[j & 3], gj, uj, dg, du);
-            og[j / 4][j & 3] = dg, ou[j / 4][j & 3] = du;
-          }
-          *reinterpret_cast<uint4 *>(a.y + at) = pack(og[0], og[1]);
-          *reinterpret_cast<uint4 *>(a.y + at + cols) = pack(ou[0], ou[1]);
-        } else {
-          *reinterpret_cast<uint4 *>(a.y + (size_t)r * cols + c) = pack(u, v);
-        }
-      });
-      if constexpr (GATE) {
-        if (a.z) {
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            put([&](int f) { return acc[f0 + f + part * OF][g]; });
-            each([&](int r, int c, f32x4_t u, f32x4_t v) {
-              *reinterpret_cast<uint4 *>(a.z + (size_t)r * N + part * cols + c) = pack(u, v);
-            });
-          }
-        }
+      for (int f = 0; f < OF; ++f) {
+        const f32x4_t v = value(f);
+        *reinterpret_cast<uint2 *>(mineb + (ln & 15) * WB + 8 * turnb((ln & 15), 2 * f + ((ln >> 4) >> 1)) + 4 * ((ln >> 4) & 1)) =
+            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
       }
-    });
-    if (next >= last) break;
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < STORESB; ++i) {
+        const int row = i * (64 / LB) + ln / LB, ch = ln % LB;
+        const uint4 v = *reinterpret_cast<const uint4 *>(mineb + row * WB + 8 * turnb(row, ch));
+        const int q = (wq * FQ + g) * 16 + row, c = done.c0 + wp * WB + 8 * ch;
+        if (q < done.rows && c < cols) store(done.row0 + q, c, v);
+      }
+    };
+    if (results && !(WHAT == GEMM_DX && SWIGLU) && !(WHAT == GEMM_DW && a.out32))
+      for_each<FQ>([&](auto gc) {
+        constexpr int g = decltype(gc)::value;
+        __builtin_amdgcn_sched_barrier(0);
+        whole(
+            g,
+            [&](int f) {
+              if constexpr (!GATE) return acc[f][g];
+              f32x4_t v;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[j] = silu_f32(acc[f][g][j]) * acc[GATE ? f + OF : f][g][j];
+              return v;
+            },
+            [&](int r, int c, uint4 v) {           // r: routed row (dw: row of the matrix)
+              const int dst = WHAT == GEMM_FWD ? dst_row(a, r) : r;
+              const size_t at = WHAT == GEMM_DW ? (size_t)done.e * N + r : (size_t)dst;
+              if (dst >= 0) *reinterpret_cast<uint4 *>(a.y + at * cols + c) = v;
+            });
+        if constexpr (GATE)
+          if (a.z)
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+              whole(g, [&](int f) { return acc[f + part * OF][g]; },
+                    [&](int r, int c, uint4 v) { *reinterpret_cast<uint4 *>(a.z + (size_t)r * N + part * cols + c) = v; });
+      });
+    if constexpr ((WHAT == GEMM_DX && SWIGLU) || WHAT == GEMM_DW) {
+      if (results && (WHAT == GEMM_DX || a.out32))
+        for_each<FQ * OF / PF>([&](auto nc) {
+          constexpr int g = decltype(nc)::value / (OF / PF), f0 = decltype(nc)::value % (OF / PF) * PF;
+          __builtin_amdgcn_sched_barrier(0);
+          put([&](int f) { return acc[f0 + f][g]; });
+#pragma unroll
+          for (int i = 0; i < STORES; ++i) {
+            const int row = i * (64 / L) + ln / L, ch = ln % L * 2;
+            const f32x4_t u = *reinterpret_cast<const f32x4_t *>(mine + row * W + 4 * turn(row, ch));
+            const f32x4_t v = *reinterpret_cast<const f32x4_t *>(mine + row * W + 4 * turn(row, ch + 1));
+            const int q = (wq * FQ + g) * 16 + row, c = done.c0 + (wp * OF + f0) * 16 + 4 * ch, r = done.row0 + q;
+            if (q >= done.rows || c >= cols) continue;
+            if constexpr (WHAT == GEMM_DW) {
+              f32x4_t *o = reinterpret_cast<f32x4_t *>(reinterpret_cast<float *>(a.y) + ((size_t)done.e * N + r) * cols + c);
+              o[0] = a.accumulate ? o[0] + u : u;
+              o[1] = a.accumulate ? o[1] + v : v;
+            } else {
+              const size_t at = (size_t)r * 2 * cols + c;
+              const uint4 zg = *reinterpret_cast<const uint4 *>(a.zin + at);
+              const uint4 zu = *reinterpret_cast<const uint4 *>(a.zin + at + cols);
+              const uint32_t gw[4] = {zg.x, zg.y, zg.z, zg.w}, uw[4] = {zu.x, zu.y, zu.z, zu.w};
+              f32x4_t og[2], ou[2];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float gj = j & 1 ? bf16_hi(gw[j / 2]) : bf16_lo(gw[j / 2]), uj = j & 1 ? bf16_hi(uw[j / 2]) : bf16_lo(uw[j / 2]);
+                float dg, du;
+                swiglu_grad(j < 4 ? u[j & 3] : v[j & 3], gj, uj, dg, du);
+                og[j / 4][j & 3] = dg, ou[j / 4][j & 3] = du;
+              }
+              *reinterpret_cast<uint4 *>(a.y + at) = pack(og[0], og[1]);
+              *reinterpret_cast<uint4 *>(a.y + at + cols) = pack(ou[0], ou[1]);
+            }
+          }
+        });
+    }
+    if (!WALK || next >= last) break;
     item = next;
   }
   wait_copies<0>();
 }
 
 template <int WHAT, bool SWIGLU, int WP, int WQ, int FP, int FQ>
-static void launch_tiled(const GemmArgs &a, hipStream_t stream) {
+static void launch_tiled(GemmArgs a, hipStream_t stream) {
   constexpr int BQ = WQ * FQ * 16, BC = WP * FP * 16 / (WHAT == GEMM_FWD && SWIGLU ? 2 : 1);
   const int cols = WHAT == GEMM_FWD ? (SWIGLU ? a.N / 2 : a.N) : a.K;
   const long long tiles = WHAT == GEMM_DW ? (long long)a.E * ((a.N + BQ - 1) / BQ) : most_tiles(a, BQ);
-  // As many workgroups as run at a time, each walking over its tiles.  Gradients of
-  // many experts' weights, tiles of unequal length, get a workgroup each (E = 128, 1536 x 2048:
-  // 480 us for 655).
+  // As many workgroups as run at a time, each walking over its tiles; gradients of
+  // weights, tiles of unequal length, get a workgroup each.
+  constexpr bool WALK = WHAT != GEMM_DW;
   constexpr int THREADS = WP * WQ * 64, PER_CU = THREADS == 512 ? 1 : 2;
   const long long items = tiles * ((cols + BC - 1) / BC);
-  const long long slots = WHAT == GEMM_DW && a.E > 1 ? MAX_LAUNCH_THREADS / THREADS : (long long)device_cu_count() * PER_CU;
-  const dim3 grid((unsigned)((std::min(items, slots) + 7) & ~7ll)), block(THREADS);
-  if (WHAT == GEMM_DW && a.perm)
-    hipLaunchKernelGGL((gemm_tiled_kernel<WHAT, SWIGLU, WHAT == GEMM_DW, WP, WQ, FP, FQ>), grid, block, 0, stream, a);
-  else
-    hipLaunchKernelGGL((gemm_tiled_kernel<WHAT, SWIGLU, false, WP, WQ, FP, FQ>), grid, block, 0, stream, a);
+  const long long slots = WALK ? (long long)device_cu_count() * PER_CU : MAX_LAUNCH_THREADS / THREADS;
+  for (long long first = 0; first < items; first += slots) {
+    a.item0 = (int)first;
+    const dim3 grid((unsigned)((std::min(items - first, slots) + 7) & ~7ll)), block(THREADS);
+    if (WHAT == GEMM_DW && a.perm)
+      hipLaunchKernelGGL((gemm_tiled_kernel<WHAT, SWIGLU, WHAT == GEMM_DW, WALK, WP, WQ, FP, FQ>), grid, block, 0, stream, a);
+    else
+      hipLaunchKernelGGL((gemm_tiled_kernel<WHAT, SWIGLU, false, WALK, WP, WQ, FP, FQ>), grid, block, 0, stream, a);
+    if (WALK) break;
+  }
 }
 
-// The tile, from the time that the workgroups' rounds take by it (us a stage; the host knows the
-// experts' average rows only).  Measured per stage of 64 positions, one and two workgroups on a CU:
-// 256 x 256 1.5; 128 x 128 0.5 and 0.9; 128 x 64 0.4 and 0.65.  Measured, us:
-//                                                     256 x 256  128 x 128  128 x 64
-//   8192 x 4096 x 7168                                      339        418       564
-//   its rows' gradient, 4096 rows (448 tiles in two rounds) 185        212       294
-//   4096 rows' through a block of 2048 (128 tiles)          144        110       152
-//   128 experts of 1536 x 2048, 256 uneven rows each        359        354       429
-//   the same, 128 rows each                                 266        244       275
-//   777 x 1536 x 2048                                        41         23        20
+// Times by which the kernel and its tile are chosen (us; the host knows the experts'
+// average rows only).  `stages` of 64 positions; `rows` rows of each of `experts` results, of n columns.
+struct GemmShape {
+  int experts, rows, n, stages, cus;
+  long long tiles(int bp, int bq) const { return (long long)experts * ((rows + bq - 1) / bq) * ((n + bp - 1) / bp); }
+};
+
+// Tiles: per stage, a round that leaves every workgroup a CU of its own (`first`) or
+// not.  Measured, us:                                256 x 256  128 x 128  128 x 64
+//   8192 x 4096 x 7168                                      334        418       564
+//   its rows' gradient, 4096 rows (448 tiles in two rounds) 180        212       294
+//   4096 rows' through a block of 2048 (128 tiles)          144        107       152
+//   128 experts of 1536 x 2048, 256 uneven rows each        348        359       429
+//   the same, 128 rows each                                 252        238       275
+static float tile_time(const GemmShape &g, int bp, int bq, int per_cu, float first, float round) {
+  const long long tiles = g.tiles(bp, bq), slots = (long long)g.cus * per_cu;
+  return g.stages * (tiles <= g.cus ? first : (float)((tiles + slots - 1) / slots) * round);
+}
+
+// Streaming: a CU copies 100 KB/us to LDS, and a wave's ring takes 0.9 us from its
+// copies to their use.  Measured, us (in brackets the tiled kernel's best):
+//   KSPLIT/FN/FM/DEPTH  4/1/1/4 4/2/1/2 2/2/1/2 4/1/2/4 4/2/2/2 2/2/2/2 4/2/4/2 4/4/4/2 2/4/4/2
+//     16 x 4096 x 7168     13.7    15.6    25.0    14.4    18.3    29.2    20.8              (89)
+//     64 x 4096 x 7168     32.0    18.9    18.6    22.7    14.2    21.6    18.6    24.1  41.8 (61)
+//    200 x 4096 x 7168    101.9    60.7    57.5    72.0    42.9    36.8    34.4    22.9  37.5 (59)
+//    400 x 4096 x 7168     195     112      99.7   132      73.6    72.3    63.6    44.9  39.0 (62)
+//    777 x 1536 x 2048     35.9    24.6    21.7    36.2    18.7    18.0    19.2    18.4  15.7 (20)
+//   128 experts of 1536 x 2048, 8 choices of 16 tokens (52 of them used, 327 MB)
+//                          89.4    59.2    53.1   149      69.4    57.7   108      79.6  72.0 (75)
+//   the same, 512 tokens  362     220     194     440     205     171     262     191   175   (160)
+template <bool SWIGLU, int KSPLIT, int FN, int FM, int DEPTH>
+struct Stream {
+  static float time(const GemmShape &g) {
+    constexpr int RG = stream_waves(KSPLIT) / KSPLIT;
+    const long long groups = g.tiles(RG * FN * 16, FM * 16);
+    const float copies = (float)((groups + g.cus - 1) / g.cus) * g.stages * RG * (FN + FM) * 2 / 100;
+    return std::max(copies, (float)((g.stages + KSPLIT - 1) / KSPLIT) * 0.9f / DEPTH);
+  }
+  static void launch(const GemmArgs &a, hipStream_t stream) { launch_stream<SWIGLU, KSPLIT, FN, FM, DEPTH>(a, stream); }
+};
+
+template <typename... S>
+struct Streams {
+  // Launches the one that is fastest, if that takes less than `limit`.
+  static bool launch(const GemmShape &g, const GemmArgs &a, hipStream_t stream, float limit) {
+    const float times[] = {S::time(g)...};
+    int best = 0, i = 0;
+    for (int n = 1; n < (int)sizeof...(S); ++n)
+      if (times[n] < times[best]) best = n;
+    if (times[best] >= limit) return false;
+    ((i++ == best ? S::launch(a, stream) : void()), ...);
+    return true;
+  }
+};
+
 template <int WHAT, bool SWIGLU>
 static moesq_status_t launch_gemm(const GemmArgs &a, hipStream_t stream, const char *who) {
-  const int n = WHAT == GEMM_FWD ? a.N : a.K, cus = device_cu_count();
-  const int experts = WHAT == GEMM_DW ? a.E : std::min(a.E, a.M), rows = WHAT == GEMM_DW ? a.N : (a.M + experts - 1) / experts;
-  // `first`: of one round that leaves every workgroup a CU of its own
-  auto time = [&](int bp, int bq, int per_cu, float first, float round) {
-    const long long tiles = (long long)experts * ((rows + bq - 1) / bq) * ((n + bp - 1) / bp), slots = (long long)cus * per_cu;
-    return tiles <= cus ? first : (float)((tiles + slots - 1) / slots) * round;
-  };
-  const float large = time(256, 256, 1, 1.5f, 1.5f), mid = time(128, 128, 2, 0.5f, 0.9f), small = time(128, 64, 2, 0.4f, 0.65f);
+  GemmShape g;
+  g.cus = device_cu_count();
+  g.n = WHAT == GEMM_FWD ? a.N : a.K;
+  g.experts = WHAT == GEMM_DW ? a.E : std::min(a.E, a.M);
+  const int mean = (a.M + std::max(g.experts, 1) - 1) / std::max(g.experts, 1);
+  g.rows = WHAT == GEMM_DW ? a.N : mean;
+  g.stages = ((WHAT == GEMM_FWD ? a.K : WHAT == GEMM_DX ? a.N : mean) + 63) / 64;
+  const float large = tile_time(g, 256, 256, 1, 1.5f, 1.5f), mid = tile_time(g, 128, 128, 2, 0.5f, 0.9f),
+              small = tile_time(g, 128, 64, 2, 0.4f, 0.65f);
+  if constexpr (WHAT == GEMM_FWD) {
+    // (of equals the first)
+    using Choice = Streams<Stream<SWIGLU, 2, 2, 1, 2>, Stream<SWIGLU, 4, 2, 1, 2>, Stream<SWIGLU, 4, 1, 1, 4>, Stream<SWIGLU, 2, 2, 2, 2>,
+                           Stream<SWIGLU, 4, 2, 2, 2>, Stream<SWIGLU, 4, 1, 2, 4>, Stream<SWIGLU, 2, 4, 4, 2>,
+                           Stream<SWIGLU, 4, 2, 4, 2>, Stream<SWIGLU, 4, 4, 4, 2>>;
+    if (Choice::launch(g, a, stream, 0.9f * std::min(large, std::min(mid, small)))) return launch_status(who);
+  }
   if (large <= mid && large <= small) launch_tiled<WHAT, SWIGLU, 2, 4, 8, 4>(a, stream);
   else if (mid <= small) launch_tiled<WHAT, SWIGLU, 2, 2, 4, 4>(a, stream);
   else launch_tiled<WHAT, SWIGLU, 2, 2, 4, 2>(a, stream);

@@ -488,7 +488,12 @@ def test_far_weights_and_results(lib):
     x = torch.randn(24, K, generator=g, device="cuda").to(BF)
     off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
     off[-1] = 24
-    assert torch.equal(lib.gemm(x, w, off), lib.gemm(x, w[-1]))
-    assert torch.equal(lib.gemm_dx(x, w, off), lib.gemm_dx(x, w[-1]))
+    # (one expert and forty take kernels that add in another order: both are held to
+    # the products' own bound)
+    xe, we = f64(x), f64(w[-1])
+    ref = xe @ we.T
+    within(lib.gemm(x, w, off), ref, bf16_tol(ref, acc(xe, we.T)), "y")
+    ref = xe @ we
+    within(lib.gemm_dx(x, w, off), ref, bf16_tol(ref, acc(xe, we)), "dx")
     dw = lib.gemm_dw(x, x, off, E=E, out=w)
     assert torch.equal(dw[-1], lib.gemm_dw(x, x)[0]) and not dw[:-1].any()
