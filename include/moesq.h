@@ -590,8 +590,9 @@ moesq_status_t moesq_gemm_dw(const uint16_t *dy, const uint16_t *x, const int32_
  * The struct is a host object; its pointers are device pointers.  x, a, b, base
  * and y 16-byte aligned.
  * Limits: K % 8 == 0, rank % 8 == 0, rank <= MOESQ_LORA_MAX_RANK, 1 <= slices <=
- *         MOESQ_LORA_MAX_SLICES, N % (8 * slices) == 0 (SWIGLU: N % 16 == 0),
- *         N, K <= MOESQ_GEMM_MAX_DIM, adapters >= 1, 0 <= T <= 2^26.
+ *         MOESQ_LORA_MAX_SLICES, N % (8 * slices) == 0 (SWIGLU: N % 16 == 0, slices
+ *         not 3), N, K <= MOESQ_GEMM_MAX_DIM, adapters >= 1, 0 <= T <= 2^26,
+ *         T * slices * rank <= 2^33.
  * Results are bit-identical on every run, and a row's do not depend on the
  * other rows' adapters.
  */

@@ -1,7 +1,14 @@
 // Low-rank adapters of many requests beside a shared projection: every row's
-// own adapter, in two products of rank `rank` with the sums between them in
-// the workspace.
-#include "common.hpp"
+// own adapter, in two kernels of rank `rank` with fp32 sums between them in the
+// workspace.
+//
+// Both take tiles of rows in order and go over the tile's adapters one by one: found
+// with ballots over the ids, each computes for the whole tile on the matrix units
+// and keeps the rows that are its own.  A request's rows are neighbours in a prefill (an
+// adapter or two a tile); in a decode batch every row may have its own, and its
+// adapter has to be read for it anyway.  No sorting, nothing that the host would
+// have to know.  Bound by memory: x in, base in, y out, and the adapters.
+#include "row_tiles.hpp"
 
 namespace moesq {
 
@@ -10,44 +17,308 @@ struct LoraArgs {
   const float *scale;
   const int32_t *ids;
   uint16_t *y;
-  float *v;                    // [T][slices * rank]
+  float *v;                    // [splits][T][slices * rank]
   int T, adapters, rank, slices, N, K;
+  int splits, lanes;           // of K; workgroups that share a tile's adapters
+  int chunk;                   // columns of a wave of the second product
 };
 
-// A simple kernel: a wave a sum.
-__global__ __launch_bounds__(256) void lora_down_simple_kernel(LoraArgs l) {
-  const int R = l.slices * l.rank, lane = threadIdx.x & 63;
-  const long long n = (long long)l.T * R, waves = (long long)gridDim.x * 4;
-  for (long long i = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); i < n; i += waves) {
-    const int t = (int)(i / R), j = (int)(i % R), id = l.ids[t];
-    if (id < 0 || id >= l.adapters) continue;
-    const uint16_t *x = l.x + (size_t)t * l.K, *a = l.a + ((size_t)id * R + j) * l.K;
-    float s = 0.0f;
-    for (int k = lane; k < l.K; k += 64) s = fmaf(bf16_lo(x[k]), bf16_lo(a[k]), s);
-    for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d, 64);
-    if (lane == 0) l.v[i] = s;
+constexpr uint32_t LORA_NOWHERE = 0xffff0000u;   // an offset behind every buffer: copies from it are zeros
+
+// The tile's adapters in order of their first rows: f(number, id, rows that have it).
+// Lane l holds the id of row l of the tile, -1 for none; all lanes take part.
+template <typename F>
+__device__ __forceinline__ void each_adapter(int id, F &&f) {
+  uint64_t left = __ballot(id >= 0);
+  for (int n = 0; left; ++n) {
+    const int cur = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
+    const uint64_t rows = __ballot(id == cur);
+    f(n, cur, rows);
+    left &= ~rows;
   }
 }
 
-// One thread a result.
-template <bool SWIGLU>
-__global__ __launch_bounds__(256) void lora_up_simple_kernel(LoraArgs l) {
-  const int cols = SWIGLU ? l.N / 2 : l.N, R = l.slices * l.rank, per = l.N / l.slices;
-  const long long n = (long long)l.T * cols, threads = (long long)gridDim.x * 256;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += threads) {
-    const int t = (int)(i / cols), c = (int)(i % cols), id = l.ids[t];
-    auto at = [&](int col) {
-      float p = l.base ? bf16_lo(l.base[(size_t)t * l.N + col]) : 0.0f;
-      if (id < 0 || id >= l.adapters) return p;
-      const uint16_t *b = l.b + ((size_t)id * l.N + col) * l.rank;
-      const float *v = l.v + (size_t)t * R + col / per * l.rank;
-      float s = 0.0f;
-      for (int j = 0; j < l.rank; ++j) s = fmaf(v[j], bf16_lo(b[j]), s);
-      return fmaf(l.scale[id], s, p);
+__device__ __forceinline__ int lora_id(const LoraArgs &l, int row, bool there) {
+  const int id = there && row < l.T ? l.ids[row] : -1;
+  return id >= 0 && id < l.adapters ? id : -1;
+}
+
+// ------------------------------------------------------------------ x a'
+//
+// 16 FM rows and 16 FN ranks a workgroup, K over `splits` workgroups and the four
+// waves of each: a wave copies stages of 64 positions of its own to a ring in LDS,
+// DEPTH deep, contracts them on the 16 x 16 x 32 MFMA, and the waves add their sums in
+// LDS in order.  Rows of other adapters are not copied (zeros).
+template <int FN, int FM, int DEPTH>
+__global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
+  constexpr int AC = FN * 2, XC = FM * 2;          // copies of a stage
+  struct Ring {
+    uint8_t a[FN * 16 * 128], x[FM * 16 * 128];
+  };
+  __shared__ __attribute__((aligned(1024))) Ring ring[4][DEPTH];
+  static_assert(sizeof(ring) >= 4 * FM * 64 * sizeof(f32x4_t), "sums fit into the rings");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, rl = lane & 15;
+  const int R = l.slices * l.rank, K = l.K, groups = (R + FN * 16 - 1) / (FN * 16);
+  int b = blockIdx.x;
+  const int r0 = b % groups * FN * 16;
+  b /= groups;
+  const int split = b % l.splits;
+  b /= l.splits;
+  const int mine = b % l.lanes, row0 = b / l.lanes * (16 * FM);
+  const int first = split * 4 + wave, step = l.splits * 4;
+  const int n = ((K + 63) / 64 - first + step - 1) / step;   // this wave's stages: first, first + step, ...
+  const uint32_t lds0 = lds_offset(&ring[wave][0]);
+  auto pos = [&](int i) { return 8 * piece4(8 * i + (lane >> 3), lane & 7); };
+  const i32x4_t xbuf = raw_buffer(l.x + (size_t)row0 * K, LORA_NOWHERE);
+
+  each_adapter(lora_id(l, row0 + lane, lane < 16 * FM), [&](int number, int cur, uint64_t rows) {
+    if (number % l.lanes != mine) return;
+    const i32x4_t abuf = raw_buffer(l.a + (size_t)cur * R * K, LORA_NOWHERE);
+    uint32_t ao[AC], xo[XC];
+#pragma unroll
+    for (int i = 0; i < AC; ++i) {
+      const int r = r0 + 8 * i + (lane >> 3);
+      ao[i] = r < R ? ((uint32_t)r * (uint32_t)K + pos(i)) * 2 : LORA_NOWHERE;
+    }
+#pragma unroll
+    for (int i = 0; i < XC; ++i) {
+      const int r = 8 * i + (lane >> 3);
+      xo[i] = (rows >> r) & 1 ? ((uint32_t)r * (uint32_t)K + pos(i)) * 2 : LORA_NOWHERE;
+    }
+    auto fetch = [&](int slot, int c) {            // (stages that are not there are copied as zeros)
+      const uint32_t to = lds0 + slot * (uint32_t)sizeof(Ring);
+#pragma unroll
+      for (int i = 0; i < AC; ++i)
+        copy16_to_lds(to + i * 1024, abuf, ao[i] != LORA_NOWHERE && 64 * c + pos(i) < K ? ao[i] + 128 * c : LORA_NOWHERE);
+#pragma unroll
+      for (int i = 0; i < XC; ++i)
+        copy16_to_lds(to + (AC + i) * 1024, xbuf, xo[i] != LORA_NOWHERE && 64 * c + pos(i) < K ? xo[i] + 128 * c : LORA_NOWHERE);
     };
-    const float p = at(c);
-    l.y[i] = (uint16_t)bf16_bits_rne(SWIGLU ? silu_f32(p) * at(c + cols) : p);
-  }
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) fetch(i, first + i * step);
+    f32x4_t acc[FN][FM];
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+#pragma unroll
+      for (int g = 0; g < FM; ++g) acc[f][g] = f32x4_t{0, 0, 0, 0};
+    for (int i = 0; i < n; ++i) {
+      wait_copies<(AC + XC) * (DEPTH - 1)>();
+      const Ring &k = ring[wave][i % DEPTH];
+      auto operand = [&](const uint8_t *p, int f, int s) {
+        const int r = 16 * f + rl;
+        return as_bf16x8(*reinterpret_cast<const uint4 *>(p + r * 128 + 16 * piece4(r, 4 * s + q)));
+      };
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        bf16x8_t X[FM];
+#pragma unroll
+        for (int g = 0; g < FM; ++g) X[g] = operand(k.x, g, s);
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+          const bf16x8_t A = operand(k.a, f, s);
+#pragma unroll
+          for (int g = 0; g < FM; ++g) acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, X[g], acc[f][g], 0, 0, 0);
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot's reads are done before it is written again
+      fetch(i % DEPTH, first + (i + DEPTH) * step);
+    }
+    wait_copies<0>();
+    f32x4_t *part = reinterpret_cast<f32x4_t *>(&ring[0][0]);     // [waves][FM][64]
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+      __syncthreads();
+#pragma unroll
+      for (int g = 0; g < FM; ++g) part[(wave * FM + g) * 64 + lane] = acc[f][g];
+      __syncthreads();
+#pragma unroll
+      for (int g = 0; g < FM; ++g) {
+        if ((f * FM + g) % 4 != wave) continue;
+        f32x4_t v = part[g * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) v += part[(w * FM + g) * 64 + lane];
+        const int r = 16 * g + rl, j = r0 + 16 * f + 4 * q;
+        if (((rows >> r) & 1) && j < R)
+          *reinterpret_cast<f32x4_t *>(l.v + ((size_t)split * l.T + row0 + r) * R + j) = v;
+      }
+    }
+    __syncthreads();                               // the sums are read before the next adapter's copies
+  });
+}
+
+// ------------------------------------------------------------------ base + scale v b'
+//
+// A wave takes 16 FM rows and `chunk` columns of one slice (with SwiGLU, of one slice
+// of each half).  v is the second operand of the MFMA, as two bf16 numbers whose
+// sum is within 2^-17 of the fp32 sum.  Two fragments of 16 columns are
+// interleaved by fours, so that a lane's results are eight neighbouring columns.
+template <bool SWIGLU, int NS, int FM>             // NS: steps of 32 ranks
+__global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs l) {
+  constexpr int H = SWIGLU ? 2 : 1;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, rl = lane & 15;
+  const int rank = l.rank, R = l.slices * rank, N = l.N, cols = N / H;
+  const int seg = N / max(l.slices, H), per = (seg + l.chunk - 1) / l.chunk;   // columns of a slice, its chunks
+  const int all = cols / seg * per, groups = (all + 3) / 4;
+  const int row0 = blockIdx.x / groups * (16 * FM), c = blockIdx.x % groups * 4 + wave;
+  if (c >= all) return;
+  const int s = c / per, col0 = s * seg + c % per * l.chunk, end = min(col0 + l.chunk, (s + 1) * seg);
+  const int id = lora_id(l, row0 + lane, lane < 16 * FM);
+
+  // v of this lane's rows
+  bf16x8_t hi[H][FM][NS], lo[H][FM][NS];
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int g = 0; g < FM; ++g) {
+      const int row = row0 + 16 * g + rl;
+      const bool own = __shfl(id, 16 * g + rl, 64) >= 0;
+      const float *v = l.v + (size_t)row * R + (l.slices == 1 ? 0 : s + h * (l.slices / 2)) * rank;
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        const int p = 32 * j + 8 * q;
+        f32x4_t sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        if (own && p < rank)
+          for (int i = 0; i < l.splits; ++i) {
+            const f32x4_t *from = reinterpret_cast<const f32x4_t *>(v + (size_t)i * l.T * R + p);
+            sum[0] += from[0];
+            sum[1] += from[1];
+          }
+        uint32_t u[4], w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x0 = sum[i / 2][2 * (i & 1)], x1 = sum[i / 2][2 * (i & 1) + 1];
+          u[i] = pack_bf16x2(x0, x1);
+          const float y0 = x0 - bf16_lo(u[i]), y1 = x1 - bf16_hi(u[i]);
+          // (an infinite sum has no rest)
+          w[i] = pack_bf16x2(fabsf(x0) < INFINITY ? y0 : 0.0f, fabsf(x1) < INFINITY ? y1 : 0.0f);
+        }
+        hi[h][g][j] = as_bf16x8(make_uint4(u[0], u[1], u[2], u[3]));
+        lo[h][g][j] = as_bf16x8(make_uint4(w[0], w[1], w[2], w[3]));
+      }
+    }
+
+  // The rows of one adapter (b: its matrix), or, b NULL, those without one.
+  auto rows_of_adapter = [&](const uint16_t *b, float scale, uint64_t rows) {
+    for (int col = col0; col < end; col += 32) {
+      f32x4_t d[H][FM][2];
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int g = 0; g < FM; ++g) d[h][g][0] = d[h][g][1] = f32x4_t{0, 0, 0, 0};
+      if (b) {
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const int n = min(col + 8 * (rl >> 2) + 4 * f + (rl & 3), end - 1) + h * cols;
+            bf16x8_t B[NS];
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+              const int p = 32 * j + 8 * q;
+              B[j] = as_bf16x8(p < rank ? *reinterpret_cast<const uint4 *>(b + (uint32_t)n * (uint32_t)rank + p)
+                                        : make_uint4(0, 0, 0, 0));
+            }
+#pragma unroll
+            for (int g = 0; g < FM; ++g)
+#pragma unroll
+              for (int j = 0; j < NS; ++j) {
+                d[h][g][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(B[j], lo[h][g][j], d[h][g][f], 0, 0, 0);
+                d[h][g][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(B[j], hi[h][g][j], d[h][g][f], 0, 0, 0);
+              }
+          }
+      }
+      const int at = col + 8 * q;
+#pragma unroll
+      for (int g = 0; g < FM; ++g) {
+        const int r = 16 * g + rl;
+        if (!((rows >> r) & 1) || at >= end) continue;
+        float p[H][8];
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (l.base) w = *reinterpret_cast<const uint4 *>(l.base + (size_t)(row0 + r) * N + at + h * cols);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float in = i & 1 ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]);
+            p[h][i] = b ? fmaf(scale, d[h][g][i / 4][i & 3], in) : in;
+          }
+        }
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = SWIGLU ? silu_f32(p[0][i]) * p[H - 1][i] : p[0][i];
+        *reinterpret_cast<uint4 *>(l.y + (size_t)(row0 + r) * cols + at) =
+            make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+      }
+    }
+  };
+  each_adapter(id, [&](int, int cur, uint64_t rows) {
+    rows_of_adapter(l.b + (size_t)cur * N * rank, l.scale[cur], rows);
+  });
+  const int there = min(l.T - row0, 16 * FM);
+  const uint64_t none = ~__ballot(id >= 0) & (there >= 64 ? ~0ull : (1ull << there) - 1);
+  if (none && (l.base != l.y || SWIGLU)) rows_of_adapter(nullptr, 0.0f, none);
+}
+
+// ------------------------------------------------------------------ launches
+
+struct LoraPlan {
+  int fn, fm, splits, lanes;
+};
+
+// Workgroups of a launch that fill the chip.
+constexpr int LORA_WORKGROUPS = 256;
+
+// How the first product is spread.  (By sizes alone: the workspace's size follows
+// from it.)  Large calls take 64 rows at a time, which reads an adapter once for them
+// where a request's rows are neighbours; small ones 16, with the tile's adapters and K
+// over workgroups until there are enough of them.
+static LoraPlan lora_plan(const moesq_lora_t &l, int T) {
+  LoraPlan p;
+  const int R = l.slices * l.rank, stages = (l.K + 63) / 64;
+  p.fn = R > 32 ? 4 : R > 16 ? 2 : 1;
+  p.fm = T > 1024 ? 4 : 1;
+  const long long base = (long long)((T + 16 * p.fm - 1) / (16 * p.fm)) * ((R + 16 * p.fn - 1) / (16 * p.fn));
+  p.lanes = p.fm == 4 ? 1 : std::min(std::min(16, T), l.adapters);
+  const long long want = (2 * LORA_WORKGROUPS + base * p.lanes - 1) / std::max(base * p.lanes, 1ll);
+  p.splits = (int)std::max(1ll, std::min(std::min(8ll, (long long)(stages + 3) / 4), want));
+  return p;
+}
+
+template <bool SWIGLU, int NS, int FM>
+static void launch_up(LoraArgs l, hipStream_t stream) {
+  const int seg = l.N / std::max(l.slices, SWIGLU ? 2 : 1), cols = l.N / (SWIGLU ? 2 : 1);
+  const long long tiles = (l.T + 16 * FM - 1) / (16 * FM);
+  // 32 columns a wave until there are four waves for every SIMD, then up to 512
+  l.chunk = 32;
+  while (l.chunk < 512 && tiles * (cols / l.chunk) > 16 * 4 * LORA_WORKGROUPS) l.chunk *= 2;
+  const int all = cols / seg * ((seg + l.chunk - 1) / l.chunk);
+  const long long grid = tiles * ((all + 3) / 4);
+  hipLaunchKernelGGL((lora_up_kernel<SWIGLU, NS, FM>), dim3((unsigned)grid), dim3(256), 0, stream, l);
+}
+
+template <bool SWIGLU>
+static void launch_lora(const LoraArgs &l, const LoraPlan &p, hipStream_t stream) {
+  const int R = l.slices * l.rank;
+  const long long grid = (long long)((l.T + 16 * p.fm - 1) / (16 * p.fm)) * ((R + 16 * p.fn - 1) / (16 * p.fn)) * p.splits * p.lanes;
+  const dim3 blocks((unsigned)grid), threads(256);
+#define DOWN(FN, FM, DEPTH) \
+  if (p.fn == FN && p.fm == FM) hipLaunchKernelGGL((lora_down_kernel<FN, FM, DEPTH>), blocks, threads, 0, stream, l)
+  DOWN(1, 1, 4);
+  DOWN(2, 1, 4);
+  DOWN(4, 1, 4);
+  DOWN(1, 4, 2);
+  DOWN(2, 4, 2);
+  DOWN(4, 4, 2);
+#undef DOWN
+  // few rows: one fragment of them a wave; ranks that leave registers for it, four or two
+  const bool few = l.T <= 1024;
+  if (l.rank <= 32) few ? launch_up<SWIGLU, 1, 1>(l, stream) : launch_up<SWIGLU, 1, SWIGLU ? 2 : 4>(l, stream);
+  else if (l.rank <= 64) few ? launch_up<SWIGLU, 2, 1>(l, stream) : launch_up<SWIGLU, 2, SWIGLU ? 2 : 4>(l, stream);
+  else if (l.rank <= 128) launch_up<SWIGLU, 4, 1>(l, stream);
+  else launch_up<SWIGLU, 8, 1>(l, stream);
 }
 
 constexpr int32_t LORA_MAX_ROWS = 1 << 26;
@@ -66,6 +337,8 @@ static moesq_status_t check_adapters(const std::string &who, const moesq_lora_t 
                                      std::to_string(MOESQ_GEMM_MAX_DIM));
   if (T < 0 || T > LORA_MAX_ROWS)
     return fail(MOESQ_ERR_SHAPE, who + ": T must be in [0, " + std::to_string(LORA_MAX_ROWS) + "]");
+  if ((long long)T * l->slices * l->rank > 1ll << 33)
+    return fail(MOESQ_ERR_SHAPE, who + ": T * slices * rank must be at most 2^33");
   return MOESQ_OK;
 }
 
@@ -75,7 +348,7 @@ using namespace moesq;
 
 extern "C" size_t moesq_lora_workspace_bytes(int32_t T, const moesq_lora_t *adapters) {
   if (check_adapters("moesq_lora_workspace_bytes", adapters, T)) return 0;
-  return (size_t)T * adapters->slices * adapters->rank * 4;
+  return (size_t)lora_plan(*adapters, T).splits * T * adapters->slices * adapters->rank * 4;
 }
 
 extern "C" moesq_status_t moesq_lora(const uint16_t *x, const int32_t *ids, int32_t T, const moesq_lora_t *adapters,
@@ -87,7 +360,8 @@ extern "C" moesq_status_t moesq_lora(const uint16_t *x, const int32_t *ids, int3
   if (epilogue != MOESQ_EPI_NONE && epilogue != MOESQ_EPI_SWIGLU)
     return fail(MOESQ_ERR_ARG, who + ": unknown epilogue");
   const bool swiglu = epilogue == MOESQ_EPI_SWIGLU;
-  if (swiglu && adapters->N % 16) return fail(MOESQ_ERR_SHAPE, who + ": SwiGLU needs N % 16 == 0");
+  if (swiglu && (adapters->N % 16 || adapters->slices == 3))
+    return fail(MOESQ_ERR_SHAPE, who + ": SwiGLU needs N % 16 == 0 and one slice or an even number");
   if (T == 0) return MOESQ_OK;
   if (!x || !ids || !adapters->a || !adapters->b || !adapters->scale || !y)
     return fail(MOESQ_ERR_NULL, who + ": NULL x, ids, adapters or y");
@@ -96,13 +370,10 @@ extern "C" moesq_status_t moesq_lora(const uint16_t *x, const int32_t *ids, int3
   if (swiglu && base == y) return fail(MOESQ_ERR_ARG, who + ": y may be base's buffer without an epilogue only");
   if (!ws || ws_bytes < moesq_lora_workspace_bytes(T, adapters))
     return fail(MOESQ_ERR_WORKSPACE, who + ": workspace missing or too small");
+  const LoraPlan p = lora_plan(*adapters, T);
   LoraArgs l{x, adapters->a, adapters->b, base, adapters->scale, ids, y, static_cast<float *>(ws),
-             T, adapters->adapters, adapters->rank, adapters->slices, adapters->N, adapters->K};
-  const dim3 grid(device_cu_count() * 8), block(256);
-  hipLaunchKernelGGL(lora_down_simple_kernel, grid, block, 0, stream, l);
-  if (swiglu)
-    hipLaunchKernelGGL(lora_up_simple_kernel<true>, grid, block, 0, stream, l);
-  else
-    hipLaunchKernelGGL(lora_up_simple_kernel<false>, grid, block, 0, stream, l);
+             T, adapters->adapters, adapters->rank, adapters->slices, adapters->N, adapters->K, p.splits, p.lanes, 0};
+  if (swiglu) launch_lora<true>(l, p, stream);
+  else launch_lora<false>(l, p, stream);
   return launch_status("moesq_lora");
 }

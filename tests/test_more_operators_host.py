@@ -149,7 +149,8 @@ def test_lora_rejects(m):
         assert call(d=bad) == m.ERR_SHAPE, bad
     assert call(T=-1) == m.ERR_SHAPE and call(T=(1 << 26) + 1) == m.ERR_SHAPE
     assert call(epi=2) == m.ERR_ARG and call(epi=m.OUT_FLAT) == m.ERR_ARG
-    assert call(epi=1, d=dict(N=72)) == m.ERR_SHAPE
+    assert call(epi=1, d=dict(N=72)) == m.ERR_SHAPE and call(epi=1, d=dict(N=96, slices=3)) == m.ERR_SHAPE
+    assert call(T=1 << 25, d=dict(rank=256, slices=2)) == m.ERR_SHAPE     # 2^34 sums
     assert call(x=None) == m.ERR_NULL and call(ids=None) == m.ERR_NULL and call(y=None) == m.ERR_NULL
     for name in ("a", "b", "scale"):
         assert call(d={name: None}) == m.ERR_NULL
