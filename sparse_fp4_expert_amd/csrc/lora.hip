@@ -19,7 +19,7 @@ struct LoraArgs {
   uint16_t *y;
   float *v;                    // [splits][T][slices * rank]
   int T, adapters, rank, slices, N, K;
-  int splits, lanes;           // of K; workgroups that share a tile's adapters
+  int splits, lanes;           // of K; workgroups that share a tile's adapters (of either product)
   int chunk;                   // columns of a wave of the second product
 };
 
@@ -65,7 +65,9 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
   b /= groups;
   const int split = b % l.splits;
   b /= l.splits;
-  const int mine = b % l.lanes, row0 = b / l.lanes * (16 * FM);
+  // (a tile's first adapter, often its only one, in the first of its workgroups, and those
+  // of all tiles before the others: one behind the other they go to different XCDs)
+  const int tiles = (l.T + 16 * FM - 1) / (16 * FM), mine = b / tiles, row0 = b % tiles * (16 * FM);
   const int first = split * 4 + wave, step = l.splits * 4;
   const int n = ((K + 63) / 64 - first + step - 1) / step;   // this wave's stages: first, first + step, ...
   const uint32_t lds0 = lds_offset(&ring[wave][0]);
@@ -149,55 +151,70 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
 
 // ------------------------------------------------------------------ base + scale v b'
 //
-// A wave takes 16 FM rows and `chunk` columns of one slice (with SwiGLU, of one slice
-// of each half).  v is the second operand of the MFMA, as two bf16 numbers whose
-// sum is within 2^-17 of the fp32 sum.  Two fragments of 16 columns are
-// interleaved by fours, so that a lane's results are eight neighbouring columns.
+// A workgroup takes 16 FM rows, a wave `chunk` columns of one slice (with SwiGLU, of
+// one slice of each half).  v is the second operand of the MFMA, as two bf16 numbers
+// whose sum is within 2^-17 of the fp32 sum: the workgroup adds up the splits' sums of its rows
+// and keeps them so in LDS.  Two fragments of 16 columns are interleaved by fours, so that a
+// lane's results are eight neighbouring columns.
 template <bool SWIGLU, int NS, int FM>             // NS: steps of 32 ranks
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs l) {
-  constexpr int H = SWIGLU ? 2 : 1;
+  constexpr int H = SWIGLU ? 2 : 1, PITCH = NS * 32 + 8;   // of a row in LDS: the rows that are read together in other banks
+  __shared__ __attribute__((aligned(16))) uint16_t sums[H][2][16 * FM][PITCH];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, rl = lane & 15;
   const int rank = l.rank, R = l.slices * rank, N = l.N, cols = N / H;
   const int seg = N / max(l.slices, H), per = (seg + l.chunk - 1) / l.chunk;   // columns of a slice, its chunks
-  const int all = cols / seg * per, groups = (all + 3) / 4;
-  const int row0 = blockIdx.x / groups * (16 * FM), c = blockIdx.x % groups * 4 + wave;
-  if (c >= all) return;
-  const int s = c / per, col0 = s * seg + c % per * l.chunk, end = min(col0 + l.chunk, (s + 1) * seg);
+  const int groups = (per + 3) / 4;                // of a slice's chunks, four waves each
+  const int tiles = (l.T + 16 * FM - 1) / (16 * FM), wg = blockIdx.x / groups;
+  const int c = blockIdx.x % groups * 4 + wave, row0 = wg % tiles * (16 * FM);
+  const int s = wg / tiles % (cols / seg), mine = wg / tiles / (cols / seg);
+  const int col0 = s * seg + c * l.chunk, end = min(col0 + l.chunk, (s + 1) * seg);
   const int id = lora_id(l, row0 + lane, lane < 16 * FM);
-
-  // v of this lane's rows
+  uint64_t own = 0;                                // rows of this workgroup's adapters
+  each_adapter(id, [&](int number, int, uint64_t rows) { own |= number % l.lanes == mine ? rows : 0; });
+  for (int u = threadIdx.x; u < H * 16 * FM * NS * 4; u += 256) {   // eight ranks at a time
+    const int p = u % (NS * 4) * 8, row = u / (NS * 4) % (16 * FM), h = u / (NS * 4 * 16 * FM);
+    f32x4_t sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    if (((own >> row) & 1) && p < rank) {
+      const float *v = l.v + (size_t)(row0 + row) * R + (l.slices == 1 ? 0 : s + h * (l.slices / 2)) * rank + p;
+      constexpr int MOST = 8;
+      f32x4_t part[MOST][2];
+#pragma unroll
+      for (int i = 0; i < MOST; ++i) {             // (all loads under way at once)
+        if (i >= l.splits) break;
+        const f32x4_t *from = reinterpret_cast<const f32x4_t *>(v + (size_t)i * l.T * R);
+        part[i][0] = from[0], part[i][1] = from[1];
+      }
+#pragma unroll
+      for (int i = 0; i < MOST; ++i) {
+        if (i >= l.splits) break;
+        sum[0] += part[i][0], sum[1] += part[i][1];
+      }
+    }
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x0 = sum[i / 2][2 * (i & 1)], x1 = sum[i / 2][2 * (i & 1) + 1];
+      hi[i] = pack_bf16x2(x0, x1);
+      const float y0 = x0 - bf16_lo(hi[i]), y1 = x1 - bf16_hi(hi[i]);
+      // (an infinite sum has no rest)
+      lo[i] = pack_bf16x2(fabsf(x0) < INFINITY ? y0 : 0.0f, fabsf(x1) < INFINITY ? y1 : 0.0f);
+    }
+    *reinterpret_cast<uint4 *>(&sums[h][0][row][p]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4 *>(&sums[h][1][row][p]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  __syncthreads();
+  if (c >= per) return;
   bf16x8_t hi[H][FM][NS], lo[H][FM][NS];
 #pragma unroll
   for (int h = 0; h < H; ++h)
 #pragma unroll
-    for (int g = 0; g < FM; ++g) {
-      const int row = row0 + 16 * g + rl;
-      const bool own = __shfl(id, 16 * g + rl, 64) >= 0;
-      const float *v = l.v + (size_t)row * R + (l.slices == 1 ? 0 : s + h * (l.slices / 2)) * rank;
+    for (int g = 0; g < FM; ++g)
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
-        const int p = 32 * j + 8 * q;
-        f32x4_t sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-        if (own && p < rank)
-          for (int i = 0; i < l.splits; ++i) {
-            const f32x4_t *from = reinterpret_cast<const f32x4_t *>(v + (size_t)i * l.T * R + p);
-            sum[0] += from[0];
-            sum[1] += from[1];
-          }
-        uint32_t u[4], w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x0 = sum[i / 2][2 * (i & 1)], x1 = sum[i / 2][2 * (i & 1) + 1];
-          u[i] = pack_bf16x2(x0, x1);
-          const float y0 = x0 - bf16_lo(u[i]), y1 = x1 - bf16_hi(u[i]);
-          // (an infinite sum has no rest)
-          w[i] = pack_bf16x2(fabsf(x0) < INFINITY ? y0 : 0.0f, fabsf(x1) < INFINITY ? y1 : 0.0f);
-        }
-        hi[h][g][j] = as_bf16x8(make_uint4(u[0], u[1], u[2], u[3]));
-        lo[h][g][j] = as_bf16x8(make_uint4(w[0], w[1], w[2], w[3]));
+        hi[h][g][j] = as_bf16x8(*reinterpret_cast<const uint4 *>(&sums[h][0][16 * g + rl][32 * j + 8 * q]));
+        lo[h][g][j] = as_bf16x8(*reinterpret_cast<const uint4 *>(&sums[h][1][16 * g + rl][32 * j + 8 * q]));
       }
-    }
 
   // The rows of one adapter (b: its matrix), or, b NULL, those without one.
   auto rows_of_adapter = [&](const uint16_t *b, float scale, uint64_t rows) {
@@ -254,9 +271,10 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs l) {
       }
     }
   };
-  each_adapter(id, [&](int, int cur, uint64_t rows) {
-    rows_of_adapter(l.b + (size_t)cur * N * rank, l.scale[cur], rows);
+  each_adapter(id, [&](int number, int cur, uint64_t rows) {
+    if (number % l.lanes == mine) rows_of_adapter(l.b + (size_t)cur * N * rank, l.scale[cur], rows);
   });
+  if (mine) return;
   const int there = min(l.T - row0, 16 * FM);
   const uint64_t none = ~__ballot(id >= 0) & (there >= 64 ? ~0ull : (1ull << there) - 1);
   if (none && (l.base != l.y || SWIGLU)) rows_of_adapter(nullptr, 0.0f, none);
@@ -268,35 +286,36 @@ struct LoraPlan {
   int fn, fm, splits, lanes;
 };
 
-// Workgroups of a launch that fill the chip.
-constexpr int LORA_WORKGROUPS = 256;
+constexpr int LORA_CUS = 256;                      // of an MI355X
 
 // How the first product is spread.  (By sizes alone: the workspace's size follows
 // from it.)  Large calls take 64 rows at a time, which reads an adapter once for them
-// where a request's rows are neighbours; small ones 16, with the tile's adapters and K
-// over workgroups until there are enough of them.
+// where a request's rows are neighbours; small ones 16.  K is split until there are
+// workgroups for the chip with an adapter a tile, and then the tile's adapters are.
 static LoraPlan lora_plan(const moesq_lora_t &l, int T) {
   LoraPlan p;
   const int R = l.slices * l.rank, stages = (l.K + 63) / 64;
   p.fn = R > 32 ? 4 : R > 16 ? 2 : 1;
   p.fm = T > 1024 ? 4 : 1;
-  const long long base = (long long)((T + 16 * p.fm - 1) / (16 * p.fm)) * ((R + 16 * p.fn - 1) / (16 * p.fn));
-  p.lanes = p.fm == 4 ? 1 : std::min(std::min(16, T), l.adapters);
-  const long long want = (2 * LORA_WORKGROUPS + base * p.lanes - 1) / std::max(base * p.lanes, 1ll);
-  p.splits = (int)std::max(1ll, std::min(std::min(8ll, (long long)(stages + 3) / 4), want));
+  const int tile = 16 * p.fm;
+  const long long base = std::max(1ll, (long long)((T + tile - 1) / tile) * ((R + 16 * p.fn - 1) / (16 * p.fn)));
+  auto within = [](long long v, long long most) { return (int)std::max(1ll, std::min(v, most)); };
+  p.splits = within(LORA_CUS / (p.fm == 4 ? 1 : 2) / base, std::min(8, (stages + 3) / 4));
+  p.lanes = within(4 * LORA_CUS / (base * p.splits), std::min(std::min(16, T), l.adapters));
   return p;
 }
 
 template <bool SWIGLU, int NS, int FM>
 static void launch_up(LoraArgs l, hipStream_t stream) {
-  const int seg = l.N / std::max(l.slices, SWIGLU ? 2 : 1), cols = l.N / (SWIGLU ? 2 : 1);
-  const long long tiles = (l.T + 16 * FM - 1) / (16 * FM);
-  // 32 columns a wave until there are four waves for every SIMD, then up to 512
+  const int seg = l.N / std::max(l.slices, SWIGLU ? 2 : 1), slices = l.N / (SWIGLU ? 2 : 1) / seg;
+  const long long tiles = (l.T + 16 * FM - 1) / (16 * FM) * slices;
+  // 32 columns a wave until there are four waves for every SIMD, then up to 256; few
+  // tiles: their adapters over workgroups
   l.chunk = 32;
-  while (l.chunk < 512 && tiles * (cols / l.chunk) > 16 * 4 * LORA_WORKGROUPS) l.chunk *= 2;
-  const int all = cols / seg * ((seg + l.chunk - 1) / l.chunk);
-  const long long grid = tiles * ((all + 3) / 4);
-  hipLaunchKernelGGL((lora_up_kernel<SWIGLU, NS, FM>), dim3((unsigned)grid), dim3(256), 0, stream, l);
+  while (l.chunk < 256 && tiles * (seg / l.chunk) > 16 * LORA_CUS) l.chunk *= 2;
+  const long long groups = ((seg + l.chunk - 1) / l.chunk + 3) / 4;
+  l.lanes = (int)std::max(1ll, std::min(4 * LORA_CUS / (tiles * groups), (long long)std::min(std::min(16, l.T), l.adapters)));
+  hipLaunchKernelGGL((lora_up_kernel<SWIGLU, NS, FM>), dim3((unsigned)(tiles * groups * l.lanes)), dim3(256), 0, stream, l);
 }
 
 template <bool SWIGLU>
