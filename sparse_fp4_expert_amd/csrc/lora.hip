@@ -216,68 +216,100 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs l) {
         lo[h][g][j] = as_bf16x8(*reinterpret_cast<const uint4 *>(&sums[h][1][16 * g + rl][32 * j + 8 * q]));
       }
 
-  // The rows of one adapter (b: its matrix), or, b NULL, those without one.
-  auto rows_of_adapter = [&](const uint16_t *b, float scale, uint64_t rows) {
-    for (int col = col0; col < end; col += 32) {
-      f32x4_t d[H][FM][2];
+  // this lane's rows: whether they have an adapter of this workgroup's, or (the first's) none
+  const int there = min(l.T - row0, 16 * FM);
+  const uint64_t live = there >= 64 ? ~0ull : (1ull << there) - 1;
+  const uint64_t none = mine == 0 && (l.base != l.y || SWIGLU) ? live & ~__ballot(id >= 0) : 0;
+  float scale[FM];
+  int ids[FM];
+#pragma unroll
+  for (int g = 0; g < FM; ++g) {
+    ids[g] = __shfl(id, 16 * g + rl, 64);
+    scale[g] = (own >> (16 * g + rl)) & 1 ? l.scale[ids[g]] : 0.0f;
+  }
+  struct Columns {
+    bf16x8_t b[H][2][NS];
+  };
+  for (int col = col0; col < end; col += 32) {
+    const int at = col + 8 * q;
+    uint4 base[H][FM];
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int g = 0; g < FM; ++g)
+        base[h][g] = l.base && at < end && (((own | none) >> (16 * g + rl)) & 1)
+                         ? *reinterpret_cast<const uint4 *>(l.base + (size_t)(row0 + 16 * g + rl) * N + at + h * cols)
+                         : make_uint4(0, 0, 0, 0);
+    // this lane's part of an adapter's columns
+    auto load = [&](Columns &to, int cur) {
+      const uint16_t *b = l.b + (size_t)cur * N * rank;
 #pragma unroll
       for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int g = 0; g < FM; ++g) d[h][g][0] = d[h][g][1] = f32x4_t{0, 0, 0, 0};
-      if (b) {
+        for (int f = 0; f < 2; ++f) {
+          const int n = min(col + 8 * (rl >> 2) + 4 * f + (rl & 3), end - 1) + h * cols;
 #pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const int n = min(col + 8 * (rl >> 2) + 4 * f + (rl & 3), end - 1) + h * cols;
-            bf16x8_t B[NS];
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-              const int p = 32 * j + 8 * q;
-              B[j] = as_bf16x8(p < rank ? *reinterpret_cast<const uint4 *>(b + (uint32_t)n * (uint32_t)rank + p)
-                                        : make_uint4(0, 0, 0, 0));
-            }
-#pragma unroll
-            for (int g = 0; g < FM; ++g)
-#pragma unroll
-              for (int j = 0; j < NS; ++j) {
-                d[h][g][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(B[j], lo[h][g][j], d[h][g][f], 0, 0, 0);
-                d[h][g][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(B[j], hi[h][g][j], d[h][g][f], 0, 0, 0);
-              }
-          }
-      }
-      const int at = col + 8 * q;
-#pragma unroll
-      for (int g = 0; g < FM; ++g) {
-        const int r = 16 * g + rl;
-        if (!((rows >> r) & 1) || at >= end) continue;
-        float p[H][8];
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (l.base) w = *reinterpret_cast<const uint4 *>(l.base + (size_t)(row0 + r) * N + at + h * cols);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float in = i & 1 ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]);
-            p[h][i] = b ? fmaf(scale, d[h][g][i / 4][i & 3], in) : in;
+          for (int j = 0; j < NS; ++j) {
+            const int p = 32 * j + 8 * q;
+            to.b[h][f][j] = as_bf16x8(p < rank ? *reinterpret_cast<const uint4 *>(b + (uint32_t)n * (uint32_t)rank + p)
+                                               : make_uint4(0, 0, 0, 0));
           }
         }
-        float o[8];
+    };
+    f32x4_t d[H][FM][2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = SWIGLU ? silu_f32(p[0][i]) * p[H - 1][i] : p[0][i];
-        *reinterpret_cast<uint4 *>(l.y + (size_t)(row0 + r) * cols + at) =
-            make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-      }
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int g = 0; g < FM; ++g) d[h][g][0] = d[h][g][1] = f32x4_t{0, 0, 0, 0};
+    // adapter by adapter, the next one's columns under way
+    uint64_t left = own;
+    int cur = left ? __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1) : -1;
+    Columns now, next;
+    if (cur >= 0) load(now, cur);
+    while (left) {
+      left &= ~__ballot(id == cur);
+      const int then = left ? __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1) : -1;
+      if (then >= 0) load(next, then);
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+          for (int g = 0; g < FM; ++g) {
+            f32x4_t v = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+              v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.b[h][f][j], lo[h][g][j], v, 0, 0, 0);
+              v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.b[h][f][j], hi[h][g][j], v, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[h][g][f][i] = ids[g] == cur ? v[i] : d[h][g][f][i];
+          }
+      now = next;
+      cur = then;
     }
-  };
-  each_adapter(id, [&](int number, int cur, uint64_t rows) {
-    if (number % l.lanes == mine) rows_of_adapter(l.b + (size_t)cur * N * rank, l.scale[cur], rows);
-  });
-  if (mine) return;
-  const int there = min(l.T - row0, 16 * FM);
-  const uint64_t none = ~__ballot(id >= 0) & (there >= 64 ? ~0ull : (1ull << there) - 1);
-  if (none && (l.base != l.y || SWIGLU)) rows_of_adapter(nullptr, 0.0f, none);
+#pragma unroll
+    for (int g = 0; g < FM; ++g) {
+      const int r = 16 * g + rl;
+      if (!(((own | none) >> r) & 1) || at >= end) continue;
+      const bool has = (own >> r) & 1;
+      float p[H][8];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const uint32_t u[4] = {base[h][g].x, base[h][g].y, base[h][g].z, base[h][g].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float in = i & 1 ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]);
+          p[h][i] = has ? fmaf(scale[g], d[h][g][i / 4][i & 3], in) : in;
+        }
+      }
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = SWIGLU ? silu_f32(p[0][i]) * p[H - 1][i] : p[0][i];
+      *reinterpret_cast<uint4 *>(l.y + (size_t)(row0 + r) * cols + at) =
+          make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+    }
+  }
 }
 
 // ------------------------------------------------------------------ launches
@@ -289,14 +321,14 @@ struct LoraPlan {
 constexpr int LORA_CUS = 256;                      // of an MI355X
 
 // How the first product is spread.  (By sizes alone: the workspace's size follows
-// from it.)  Large calls take 64 rows at a time, which reads an adapter once for them
-// where a request's rows are neighbours; small ones 16.  K is split until there are
+// from it.)  Large calls of high ranks take 64 rows at a time, which reads an adapter once for
+// them where a request's rows are neighbours; others 16.  K is split until there are
 // workgroups for the chip with an adapter a tile, and then the tile's adapters are.
 static LoraPlan lora_plan(const moesq_lora_t &l, int T) {
   LoraPlan p;
   const int R = l.slices * l.rank, stages = (l.K + 63) / 64;
   p.fn = R > 32 ? 4 : R > 16 ? 2 : 1;
-  p.fm = T > 1024 ? 4 : 1;
+  p.fm = T > 1024 && R > 32 ? 4 : 1;
   const int tile = 16 * p.fm;
   const long long base = std::max(1ll, (long long)((T + tile - 1) / tile) * ((R + 16 * p.fn - 1) / (16 * p.fn)));
   auto within = [](long long v, long long most) { return (int)std::max(1ll, std::min(v, most)); };
@@ -309,10 +341,10 @@ template <bool SWIGLU, int NS, int FM>
 static void launch_up(LoraArgs l, hipStream_t stream) {
   const int seg = l.N / std::max(l.slices, SWIGLU ? 2 : 1), slices = l.N / (SWIGLU ? 2 : 1) / seg;
   const long long tiles = (l.T + 16 * FM - 1) / (16 * FM) * slices;
-  // 32 columns a wave until there are four waves for every SIMD, then up to 256; few
+  // 32 columns a wave until there are four waves for every SIMD, then up to 128; few
   // tiles: their adapters over workgroups
   l.chunk = 32;
-  while (l.chunk < 256 && tiles * (seg / l.chunk) > 16 * LORA_CUS) l.chunk *= 2;
+  while (l.chunk < 128 && tiles * (seg / l.chunk) > 16 * LORA_CUS) l.chunk *= 2;
   const long long groups = ((seg + l.chunk - 1) / l.chunk + 3) / 4;
   l.lanes = (int)std::max(1ll, std::min(4 * LORA_CUS / (tiles * groups), (long long)std::min(std::min(16, l.T), l.adapters)));
   hipLaunchKernelGGL((lora_up_kernel<SWIGLU, NS, FM>), dim3((unsigned)(tiles * groups * l.lanes)), dim3(256), 0, stream, l);
@@ -327,15 +359,14 @@ static void launch_lora(const LoraArgs &l, const LoraPlan &p, hipStream_t stream
   if (p.fn == FN && p.fm == FM) hipLaunchKernelGGL((lora_down_kernel<FN, FM, DEPTH>), blocks, threads, 0, stream, l)
   DOWN(1, 1, 4);
   DOWN(2, 1, 4);
-  DOWN(4, 1, 4);
-  DOWN(1, 4, 2);
-  DOWN(2, 4, 2);
+  DOWN(4, 1, 2);
   DOWN(4, 4, 2);
 #undef DOWN
-  // few rows: one fragment of them a wave; ranks that leave registers for it, four or two
-  const bool few = l.T <= 1024;
-  if (l.rank <= 32) few ? launch_up<SWIGLU, 1, 1>(l, stream) : launch_up<SWIGLU, 1, SWIGLU ? 2 : 4>(l, stream);
-  else if (l.rank <= 64) few ? launch_up<SWIGLU, 2, 1>(l, stream) : launch_up<SWIGLU, 2, SWIGLU ? 2 : 4>(l, stream);
+  // Many rows of ranks up to 64: 32 at a time, which reads an adapter half as often (8192 rows,
+  // rank 64, to 4096: 49 us; 16 at a time 58, 64 at a time, with half the waves on a SIMD, 54).
+  const bool many = l.T > 1024;
+  if (l.rank <= 32) launch_up<SWIGLU, 1, 1>(l, stream);
+  else if (l.rank <= 64) many ? launch_up<SWIGLU, 2, 2>(l, stream) : launch_up<SWIGLU, 2, 1>(l, stream);
   else if (l.rank <= 128) launch_up<SWIGLU, 4, 1>(l, stream);
   else launch_up<SWIGLU, 8, 1>(l, stream);
 }

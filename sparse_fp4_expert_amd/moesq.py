@@ -662,14 +662,15 @@ def _swiglu(epilogue):
     return (epilogue & ~OUT_FLAT) == EPI_SWIGLU
 
 
-def _counts(*named):
-    for n, name in named:
-        _count(n, name)
+def _counts(**named):
+    if max(named.values()) >= 1 << 31:
+        for name, n in named.items():
+            _count(n, name)
 
 
 def moesq_gemm(x, perm, T: int, k: int, expert_offsets, M: int, w, E: int, N: int, K: int, epilogue: int, y,
                z=None, stream=None):
-    _counts((T, "T"), (k, "k"), (M, "M"), (E, "E"), (N, "N"), (K, "K"))
+    _counts(T=T, k=k, M=M, E=E, N=N, K=K)
     bf, i32 = torch.bfloat16, torch.int32
     dev, (xp, p, off, wp, yp, zp) = _pointers(
         (x, bf, (T if perm is not None else M) * K, "x"), (perm, i32, M, "perm"),
@@ -679,7 +680,7 @@ def moesq_gemm(x, perm, T: int, k: int, expert_offsets, M: int, w, E: int, N: in
 
 
 def moesq_gemm_dx(dy, expert_offsets, M: int, w, E: int, N: int, K: int, z, dx, stream=None):
-    _counts((M, "M"), (E, "E"), (N, "N"), (K, "K"))
+    _counts(M=M, E=E, N=N, K=K)
     bf = torch.bfloat16
     dev, (d, off, wp, zp, o) = _pointers(
         (dy, bf, M * N, "dy"), (expert_offsets, torch.int32, E + 1, "expert_offsets"), (w, bf, E * N * K, "w"),
@@ -691,7 +692,7 @@ def moesq_gemm_dw(dy, x, perm, T: int, k: int, expert_offsets, M: int, E: int, N
                   accumulate: bool = False, stream=None):
     """The type of dw (float32 or bfloat16) is the call's dtype."""
     dtype = _dtype(dw, "dw")
-    _counts((T, "T"), (k, "k"), (M, "M"), (E, "E"), (N, "N"), (K, "K"))
+    _counts(T=T, k=k, M=M, E=E, N=N, K=K)
     bf, i32 = torch.bfloat16, torch.int32
     dev, (d, xp, p, off, o) = _pointers(
         (dy, bf, M * N, "dy"), (x, bf, (T if perm is not None else M) * K, "x"), (perm, i32, M, "perm"),
@@ -700,7 +701,7 @@ def moesq_gemm_dw(dy, x, perm, T: int, k: int, expert_offsets, M: int, E: int, N
 
 
 def moesq_unpermute_backward(dout, y, inv_perm, topk_weights, T: int, k: int, N: int, dy, dw, stream=None):
-    _counts((T, "T"), (k, "k"), (N, "N"))
+    _counts(T=T, k=k, N=N)
     bf, f32, M = torch.bfloat16, torch.float32, T * k
     dev, (d, yp, inv, w, o, ow) = _pointers(
         (dout, bf, T * N, "dout"), (y, bf, M * N, "y"), (inv_perm, torch.int32, M, "inv_perm"),
