@@ -212,17 +212,17 @@ static void launch_stream(GemmArgs a, hipStream_t stream) {
 // ------------------------------------------------------------------ tiled kernel
 //
 // A workgroup computes BP columns x BQ rows.  Stages of 64 positions of both
-// operands are copied to LDS, two in turn, and contracted in two steps of 32 on
+// operands are copied to LDS, DEPTH in turn, and contracted in two steps of 32 on
 // the 16 x 16 x 32 MFMA.  (On that of 32 x 32 x 16 two waves of a SIMD lose a third of the
 // rate: 147 us for 99 in a loop of MFMAs alone, and on random values 165 for 120, where
 // power sets the clock.)  The one barrier of a stage is early in its second step, behind the
-// stage's reads: it hands the stage's buffer to the copies of the stage after the next and
+// stage's reads: it hands the stage's buffer to the copies of the stage DEPTH behind it and
 // says that the next has landed.  An operand of the next step is read into the
 // registers of this step's as soon as its MFMAs are issued (P), or into a
 // second set (Q).
 //
 // Every vector instruction beside the MFMAs takes time from them, so the loop has
-// none but what a gather needs: it is unrolled over the two buffers, so that reads
+// none but what a gather needs: it is unrolled over the buffers, so that reads
 // have constant offsets; copies go by the load's own offset, which counts in
 // memory and in LDS, and the offsets of positions that are not there are changed
 // once, before the last stages.
@@ -272,8 +272,8 @@ __device__ __forceinline__ int chunk_turn(int r) {
 }
 
 // WP waves over the columns (FP fragments of 16 each), WQ over the rows (FQ).
-template <int WHAT, bool SWIGLU, bool GATHER, bool WALK, int WP, int WQ, int FP, int FQ>
-__global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2) void gemm_tiled_kernel(GemmArgs a) {
+template <int WHAT, bool SWIGLU, bool GATHER, bool WALK, int DEPTH, int WP, int WQ, int FP, int FQ>
+__global__ __launch_bounds__(WP * WQ * 64, DEPTH > 2 ? 1 : 2) void gemm_tiled_kernel(GemmArgs a) {
   constexpr bool GATE = WHAT == GEMM_FWD && SWIGLU;
   constexpr bool PT = WHAT != GEMM_FWD, QT = WHAT == GEMM_DW;    // position by position
   constexpr int WAVES = WP * WQ, BP = WP * FP * 16, BQ = WQ * FQ * 16;
@@ -284,7 +284,7 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
   // fp32 where they are not yet the output's bf16, else all WB columns of the wave.
   constexpr int OF = GATE ? FP / 2 : FP, PF = OF < 4 ? OF : 4, W = PF * 16, WB = OF * 16;
   struct Lds {
-    uint8_t p[2][PB], q[2][QB];
+    uint8_t p[DEPTH][PB], q[DEPTH][QB];
     float out[WAVES][16 * W];                      // (or 16 * WB of bf16)
   };
   __shared__ __attribute__((aligned(1024))) Lds lds;
@@ -478,11 +478,14 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
     });
   };
   // this wave's copies have landed and its reads are done; then every wave's
-  auto arrive = [&] {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  // (all but the copies of the LATER last stages)
+  auto arrive = [&](auto later) {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(later)::value * (CP + CQ)) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
+  // (a gather waits for the loads of its rows' numbers, and with them for every copy)
+  static_assert(!GATHER || DEPTH == 2, "a gather runs two stages ahead");
   // Of the second step's MFMAS, those of AF fragments of P (ARRIVE) are before the barrier;
   // behind it a copy follows every EVERY.  (Copies one behind the other keep the wave from its
   // MFMAS until the address unit has taken them: on zeros, 4096 x 4096 x 7168, 153 us with all of
@@ -514,23 +517,23 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
       mfmas(i0, end, 0, [&](auto j) { reads(j, i0, S, 1); });
       mfmas(i0, mid, 1, [&](auto) {});
     }
-    arrive();
+    arrive(std::integral_constant<int, DEPTH - 2>{});
     use_src();
     if (busy) {
       // (behind the last stage, operands are read for nothing)
       mfmas(mid, end, 1, [&](auto j) {
         constexpr int n = decltype(j)::value - ARRIVE;
-        reads(j, std::integral_constant<int, AF>{}, S ^ 1, 0);
+        reads(j, std::integral_constant<int, AF>{}, (S + 1) % DEPTH, 0);
         if constexpr (n % EVERY == EVERY / 2 && n / EVERY < COPIES) copy(std::integral_constant<int, n / EVERY>{}, S);
       });
     } else {
       for_each<COPIES>([&](auto i) { copy(i, S); });
     }
-    next_p(t.C - 64 * (s + 3));
-    next_q(t.C - 64 * (s + 3));
+    next_p(t.C - 64 * (s + DEPTH + 1));
+    next_q(t.C - 64 * (s + DEPTH + 1));
   };
 
-  // The first copies of tile t: stages 0 and 1.
+  // The first copies of tile t: stages 0 to DEPTH - 1.
   auto start = [&] {
     set_up();
     load_src(0);
@@ -539,11 +542,14 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
     pbuf = moved(pbuf, 0 - pstep), next_p(t.C);
     qbuf = moved(qbuf, 0 - qstep), next_q(t.C);
     for_each<COPIES>([&](auto i) { copy(i, 0); });
-    next_p(t.C - 64), next_q(t.C - 64);
-    load_src(1);
-    use_src();
-    for_each<COPIES>([&](auto i) { copy(i, 1); });
-    next_p(t.C - 128), next_q(t.C - 128);
+    for_each<DEPTH - 1>([&](auto n) {
+      constexpr int c = decltype(n)::value + 1;
+      next_p(t.C - 64 * c), next_q(t.C - 64 * c);
+      load_src(c);
+      use_src();
+      for_each<COPIES>([&](auto i) { copy(i, c); });
+    });
+    next_p(t.C - 64 * DEPTH), next_q(t.C - 64 * DEPTH);
   };
   start();
   while (true) {
@@ -557,7 +563,7 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
     for (int f = 0; f < FP; ++f)
 #pragma unroll
       for (int g = 0; g < FQ; ++g) acc[f][g] = f32x4_t{0, 0, 0, 0};
-    arrive();
+    arrive(i0);
     if (busy) {
 #pragma unroll
       for (int g = 0; g < FQ; ++g) read_q(g, 0, 0);
@@ -565,17 +571,18 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
       for (int f = 0; f < FP; ++f) read_p(f, 0, 0);
     }
     const int stages = (t.C + 63) / 64;
-    for (int s = 0; s < stages; s += 2) {
-      stage(s, i0);
-      if (s + 1 < stages) stage(s + 1, std::integral_constant<int, 1>{});
-    }
+    for (int s = 0; s < stages; s += DEPTH)
+      for_each<DEPTH>([&](auto n) {
+        constexpr int S = decltype(n)::value;
+        if (s + S < stages) stage(s + S, n);
+      });
     const Tile done = t;
     const bool results = busy;
     if (WALK && next < last) {
       // every wave is done with the buffers: its last reads were before the last barrier (without
       // stages, the first), and its copies behind the end, zeros, have landed
       wait_copies<0>();
-      if (stages == 0) arrive();
+      if (stages == 0) arrive(i0);
       t = nxt;
       start();
     }
@@ -685,7 +692,7 @@ __global__ __launch_bounds__(WP * WQ * 64, WP * WQ == 4 && FP * FQ >= 32 ? 1 : 2
   wait_copies<0>();
 }
 
-template <int WHAT, bool SWIGLU, int WP, int WQ, int FP, int FQ>
+template <int WHAT, bool SWIGLU, int DEPTH, int WP, int WQ, int FP, int FQ>
 static void launch_tiled(GemmArgs a, hipStream_t stream) {
   constexpr int BQ = WQ * FQ * 16, BC = WP * FP * 16 / (WHAT == GEMM_FWD && SWIGLU ? 2 : 1);
   const int cols = WHAT == GEMM_FWD ? (SWIGLU ? a.N / 2 : a.N) : a.K;
@@ -693,16 +700,16 @@ static void launch_tiled(GemmArgs a, hipStream_t stream) {
   // As many workgroups as run at a time, each walking over its tiles; gradients of
   // weights, tiles of unequal length, get a workgroup each.
   constexpr bool WALK = WHAT != GEMM_DW;
-  constexpr int THREADS = WP * WQ * 64, PER_CU = THREADS == 512 ? 1 : 2;
+  constexpr int THREADS = WP * WQ * 64, PER_CU = THREADS == 512 || DEPTH > 2 ? 1 : 2;
   const long long items = tiles * ((cols + BC - 1) / BC);
   const long long slots = WALK ? (long long)device_cu_count() * PER_CU : MAX_LAUNCH_THREADS / THREADS;
   for (long long first = 0; first < items; first += slots) {
     a.item0 = (int)first;
     const dim3 grid((unsigned)((std::min(items - first, slots) + 7) & ~7ll)), block(THREADS);
     if (WHAT == GEMM_DW && a.perm)
-      hipLaunchKernelGGL((gemm_tiled_kernel<WHAT, SWIGLU, WHAT == GEMM_DW, WALK, WP, WQ, FP, FQ>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((gemm_tiled_kernel<WHAT, SWIGLU, WHAT == GEMM_DW, WALK, 2, WP, WQ, FP, FQ>), grid, block, 0, stream, a);
     else
-      hipLaunchKernelGGL((gemm_tiled_kernel<WHAT, SWIGLU, false, WALK, WP, WQ, FP, FQ>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((gemm_tiled_kernel<WHAT, SWIGLU, false, WALK, DEPTH, WP, WQ, FP, FQ>), grid, block, 0, stream, a);
     if (WALK) break;
   }
 }
@@ -721,6 +728,9 @@ struct GemmShape {
 //   4096 rows' through a block of 2048 (128 tiles)          144        107       152
 //   128 experts of 1536 x 2048, 256 uneven rows each        348        359       429
 //   the same, 128 rows each                                 252        238       275
+//   777 x 1536 x 2048                                        41         23        20 (four stages ahead 14)
+//   the same from the left, through a block of 768           52         27        22 (17)
+//   100 rows' gradient, 4096 x 7168                                     45        37 (23)
 static float tile_time(const GemmShape &g, int bp, int bq, int per_cu, float first, float round) {
   const long long tiles = g.tiles(bp, bq), slots = (long long)g.cus * per_cu;
   return g.stages * (tiles <= g.cus ? first : (float)((tiles + slots - 1) / slots) * round);
@@ -771,8 +781,11 @@ static moesq_status_t launch_gemm(const GemmArgs &a, hipStream_t stream, const c
   const int mean = (a.M + std::max(g.experts, 1) - 1) / std::max(g.experts, 1);
   g.rows = WHAT == GEMM_DW ? a.N : mean;
   g.stages = ((WHAT == GEMM_FWD ? a.K : WHAT == GEMM_DX ? a.N : mean) + 63) / 64;
+  // (few tiles, one on a CU, copy four stages ahead; not for weights' gradients of few rows, which would
+  // wait for all of them first)
+  const bool ahead = WHAT != GEMM_DW && g.tiles(128, 64) <= g.cus;
   const float large = tile_time(g, 256, 256, 1, 1.5f, 1.5f), mid = tile_time(g, 128, 128, 2, 0.5f, 0.9f),
-              small = tile_time(g, 128, 64, 2, 0.4f, 0.65f);
+              small = tile_time(g, 128, 64, 2, ahead ? 0.29f : 0.4f, 0.65f);
   if constexpr (WHAT == GEMM_FWD) {
     // (of equals the first)
     using Choice = Streams<Stream<SWIGLU, 2, 2, 1, 2>, Stream<SWIGLU, 4, 2, 1, 2>, Stream<SWIGLU, 4, 1, 1, 4>, Stream<SWIGLU, 2, 2, 2, 2>,
@@ -780,9 +793,11 @@ static moesq_status_t launch_gemm(const GemmArgs &a, hipStream_t stream, const c
                            Stream<SWIGLU, 4, 2, 4, 2>, Stream<SWIGLU, 4, 4, 4, 2>>;
     if (Choice::launch(g, a, stream, 0.9f * std::min(large, std::min(mid, small)))) return launch_status(who);
   }
-  if (large <= mid && large <= small) launch_tiled<WHAT, SWIGLU, 2, 4, 8, 4>(a, stream);
-  else if (mid <= small) launch_tiled<WHAT, SWIGLU, 2, 2, 4, 4>(a, stream);
-  else launch_tiled<WHAT, SWIGLU, 2, 2, 4, 2>(a, stream);
+  if (large <= mid && large <= small) return launch_tiled<WHAT, SWIGLU, 2, 2, 4, 8, 4>(a, stream), launch_status(who);
+  if (mid <= small) return launch_tiled<WHAT, SWIGLU, 2, 2, 2, 4, 4>(a, stream), launch_status(who);
+  if constexpr (WHAT != GEMM_DW)
+    if (ahead) return launch_tiled<WHAT, SWIGLU, 4, 2, 2, 4, 2>(a, stream), launch_status(who);
+  launch_tiled<WHAT, SWIGLU, 2, 2, 2, 4, 2>(a, stream);
   return launch_status(who);
 }
 
