@@ -256,6 +256,13 @@ __device__ __forceinline__ int fresh(int lane) {
   return lane;
 }
 
+// Stores 16 bytes a lane, of lanes with an offset of NOWHERE none.  (Not in asm: behind a
+// store the compiler keeps its registers until it has read them.)
+__device__ __forceinline__ void store16(void *p, uint32_t voff, uint4 v) {
+  const auto buf = __builtin_amdgcn_make_buffer_rsrc(p, 0, (int)NOWHERE, 0x20000);
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, v), buf, (int)voff, 0, 0);
+}
+
 // The buffer, moved on by `by` bytes.
 __device__ __forceinline__ i32x4_t moved(i32x4_t b, uint64_t by) {
   const uint64_t u = ((uint64_t)(uint32_t)b[1] << 32 | (uint32_t)b[0]) + by;
@@ -366,8 +373,8 @@ __global__ __launch_bounds__(WP * WQ * 64, DEPTH > 2 ? 1 : 2) void gemm_tiled_ke
       pbuf = from(a.w + (size_t)t.e * N * K, BIAS);
 #pragma unroll
       for (int i = 0; i < CP; ++i) {
-        // GATE: the first half of a wave's t.rows are gate t.rows, the second half the
-        // up t.rows of the same columns.  (Columns that are not there read another
+        // GATE: the first half of a wave's rows are gate rows, the second half the
+        // up rows of the same columns.  (Columns that are not there read another
         // row, and their results are not used.)
         constexpr int H = FP * 8;
         const int r = (wave * CP + i) * 8 + (ln >> 3);
@@ -605,7 +612,7 @@ __global__ __launch_bounds__(WP * WQ * 64, DEPTH > 2 ? 1 : 2) void gemm_tiled_ke
     auto pack = [](f32x4_t u, f32x4_t v) {
       return make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     };
-    // 16 rows x WB columns of bf16, and store(row, column, eight of them).
+    // 16 rows x WB columns of bf16, and store(row of the tile, column, eight of them, whether they are there).
     uint16_t *mineb = reinterpret_cast<uint16_t *>(mine);
     auto turnb = [](int row, int chunk) { return chunk ^ (row & (LB - 1)); };
     auto whole = [&](int g, auto &&value, auto &&store) {
@@ -622,9 +629,10 @@ __global__ __launch_bounds__(WP * WQ * 64, DEPTH > 2 ? 1 : 2) void gemm_tiled_ke
         const int row = i * (64 / LB) + ln / LB, ch = ln % LB;
         const uint4 v = *reinterpret_cast<const uint4 *>(mineb + row * WB + 8 * turnb(row, ch));
         const int q = (wq * FQ + g) * 16 + row, c = done.c0 + wp * WB + 8 * ch;
-        if (q < done.rows && c < cols) store(done.row0 + q, c, v);
+        store(q, c, v, q < done.rows && c < cols);
       }
     };
+    uint16_t *ytile = a.y + (WHAT == GEMM_DW ? (size_t)done.e * N + done.row0 : (size_t)done.row0) * cols;
     if (results && !(WHAT == GEMM_DX && SWIGLU) && !(WHAT == GEMM_DW && a.out32))
       for_each<FQ>([&](auto gc) {
         constexpr int g = decltype(gc)::value;
@@ -638,17 +646,22 @@ __global__ __launch_bounds__(WP * WQ * 64, DEPTH > 2 ? 1 : 2) void gemm_tiled_ke
               for (int j = 0; j < 4; ++j) v[j] = silu_f32(acc[f][g][j]) * acc[GATE ? f + OF : f][g][j];
               return v;
             },
-            [&](int r, int c, uint4 v) {           // r: routed row (dw: row of the matrix)
-              const int dst = WHAT == GEMM_FWD ? dst_row(a, r) : r;
-              const size_t at = WHAT == GEMM_DW ? (size_t)done.e * N + r : (size_t)dst;
-              if (dst >= 0) *reinterpret_cast<uint4 *>(a.y + at * cols + c) = v;
+            [&](int q, int c, uint4 v, bool there) {
+              if (WHAT == GEMM_FWD && a.flat) {
+                const int dst = there ? dst_row(a, done.row0 + q) : -1;
+                if (dst >= 0) *reinterpret_cast<uint4 *>(a.y + (size_t)dst * cols + c) = v;
+              } else {
+                store16(ytile, there ? ((uint32_t)q * (uint32_t)cols + c) * 2 : NOWHERE, v);
+              }
             });
         if constexpr (GATE)
           if (a.z)
 #pragma unroll
             for (int part = 0; part < 2; ++part)
               whole(g, [&](int f) { return acc[f + part * OF][g]; },
-                    [&](int r, int c, uint4 v) { *reinterpret_cast<uint4 *>(a.z + (size_t)r * N + part * cols + c) = v; });
+                    [&](int q, int c, uint4 v, bool there) {
+                      store16(a.z + (size_t)done.row0 * N, there ? ((uint32_t)q * (uint32_t)N + part * cols + c) * 2 : NOWHERE, v);
+                    });
       });
     if constexpr ((WHAT == GEMM_DX && SWIGLU) || WHAT == GEMM_DW) {
       if (results && (WHAT == GEMM_DX || a.out32))
