@@ -21,7 +21,10 @@ struct LoraArgs {
   int T, adapters, rank, slices, N, K;
   int splits, lanes;           // of K; workgroups that share a tile's adapters (of either product)
   int chunk;                   // columns of a wave of the second product
+  int wg0;                     // first workgroup of this launch of it
 };
+
+constexpr float BF16_MAX = 0x1.fep127f;
 
 constexpr uint32_t LORA_NOWHERE = 0xffff0000u;   // an offset behind every buffer: copies from it are zeros
 
@@ -165,8 +168,9 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs l) {
   const int rank = l.rank, R = l.slices * rank, N = l.N, cols = N / H;
   const int seg = N / max(l.slices, H), per = (seg + l.chunk - 1) / l.chunk;   // columns of a slice, its chunks
   const int groups = (per + 3) / 4;                // of a slice's chunks, four waves each
-  const int tiles = (l.T + 16 * FM - 1) / (16 * FM), wg = blockIdx.x / groups;
-  const int c = blockIdx.x % groups * 4 + wave, row0 = wg % tiles * (16 * FM);
+  const int tiles = (l.T + 16 * FM - 1) / (16 * FM);
+  const int at0 = l.wg0 + (int)blockIdx.x, wg = at0 / groups;
+  const int c = at0 % groups * 4 + wave, row0 = wg % tiles * (16 * FM);
   const int s = wg / tiles % (cols / seg), mine = wg / tiles / (cols / seg);
   const int col0 = s * seg + c * l.chunk, end = min(col0 + l.chunk, (s + 1) * seg);
   const int id = lora_id(l, row0 + lane, lane < 16 * FM);
@@ -195,10 +199,9 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs l) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float x0 = sum[i / 2][2 * (i & 1)], x1 = sum[i / 2][2 * (i & 1) + 1];
-      hi[i] = pack_bf16x2(x0, x1);
-      const float y0 = x0 - bf16_lo(hi[i]), y1 = x1 - bf16_hi(hi[i]);
-      // (an infinite sum has no rest)
-      lo[i] = pack_bf16x2(fabsf(x0) < INFINITY ? y0 : 0.0f, fabsf(x1) < INFINITY ? y1 : 0.0f);
+      // (what is larger than the largest finite bf16, infinite or not, is left to the rest)
+      hi[i] = pack_bf16x2(__builtin_amdgcn_fmed3f(x0, -BF16_MAX, BF16_MAX), __builtin_amdgcn_fmed3f(x1, -BF16_MAX, BF16_MAX));
+      lo[i] = pack_bf16x2(x0 - bf16_lo(hi[i]), x1 - bf16_hi(hi[i]));
     }
     *reinterpret_cast<uint4 *>(&sums[h][0][row][p]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4 *>(&sums[h][1][row][p]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -347,7 +350,11 @@ static void launch_up(LoraArgs l, hipStream_t stream) {
   while (l.chunk < 128 && tiles * (seg / l.chunk) > 16 * LORA_CUS) l.chunk *= 2;
   const long long groups = ((seg + l.chunk - 1) / l.chunk + 3) / 4;
   l.lanes = (int)std::max(1ll, std::min(4 * LORA_CUS / (tiles * groups), (long long)std::min(std::min(16, l.T), l.adapters)));
-  hipLaunchKernelGGL((lora_up_kernel<SWIGLU, NS, FM>), dim3((unsigned)(tiles * groups * l.lanes)), dim3(256), 0, stream, l);
+  const long long all = tiles * groups * l.lanes, part = MAX_LAUNCH_THREADS / 256;
+  for (long long first = 0; first < all; first += part) {
+    l.wg0 = (int)first;
+    hipLaunchKernelGGL((lora_up_kernel<SWIGLU, NS, FM>), dim3((unsigned)std::min(part, all - first)), dim3(256), 0, stream, l);
+  }
 }
 
 template <bool SWIGLU>
@@ -422,7 +429,7 @@ extern "C" moesq_status_t moesq_lora(const uint16_t *x, const int32_t *ids, int3
     return fail(MOESQ_ERR_WORKSPACE, who + ": workspace missing or too small");
   const LoraPlan p = lora_plan(*adapters, T);
   LoraArgs l{x, adapters->a, adapters->b, base, adapters->scale, ids, y, static_cast<float *>(ws),
-             T, adapters->adapters, adapters->rank, adapters->slices, adapters->N, adapters->K, p.splits, p.lanes, 0};
+             T, adapters->adapters, adapters->rank, adapters->slices, adapters->N, adapters->K, p.splits, p.lanes, 0, 0};
   if (swiglu) launch_lora<true>(l, p, stream);
   else launch_lora<false>(l, p, stream);
   return launch_status("moesq_lora");

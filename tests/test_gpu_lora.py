@@ -210,3 +210,46 @@ def test_far_rows_and_adapters(lib):
     y = lib.lora(x, lib.Lora(a, b, one), ids)
     want = lib.lora(x, lib.Lora(a[-1:].clone(), b[-1:].clone(), one[:1]), (ids == A - 1).int() - 1)
     assert torch.equal(y, want) and y[1].any() and not y[[0, 2, 4]].any()
+
+
+def test_sums_past_the_largest_bf16(lib):
+    """A sum between the largest bf16 and the largest fp32 number, of which no bf16 is
+    the nearest finite one, and infinite and NaN sums: a row of the second product
+    shows them as they are."""
+    def up(*e):
+        return sum(2.0 ** i for i in e)
+
+    x = torch.zeros(4, 8, dtype=BF)
+    x[:, :3] = torch.tensor([2.0 ** 64, 2.0 ** 64, 2.0 ** 64])
+    x[1] = -x[1]
+    x[2, 3], x[3, 3] = float("inf"), float("nan")
+    a = torch.zeros(1, 8, 8, dtype=BF)
+    a[0, 0, :3] = torch.tensor([255 * 2.0 ** 56, 2.0 ** 55, 2.0 ** 54])
+    a[0, :, 3] = 1                                                 # (every rank is infinite, none 0 * inf)
+    b = torch.zeros(1, 8, 8, dtype=BF)
+    b[0, :, :] = torch.tensor([2.0 ** -100, -(2.0 ** -120), 1.0, 2.0 ** -126, 2.0 ** -110, 2.0 ** -112, -1.0, 2.0 ** -90])[:, None]
+    v = 255 * 2.0 ** 120 + up(119, 118)                            # past the tie between the largest bf16 and infinity
+    assert torch.tensor(v).float().isfinite() and torch.tensor(v).to(BF).isinf()
+    lora = lib.Lora(a.cuda(), b.cuda(), torch.tensor([2.0 ** -10]).cuda())
+    y = f64(lib.lora(x.cuda(), lora, torch.zeros(4, dtype=torch.int32).cuda()))
+    p = np.outer([v, -v], f64(b)[0, :, 0]) * 2.0 ** -10
+    assert (np.abs(y[:2] - p) <= (2.0 ** -8 + 2.0 ** -16) * np.abs(p)).all()
+    assert np.array_equal(y[2], np.sign(f64(b)[0, :, 0]) * np.inf) and np.isnan(y[3]).all()
+
+
+def test_more_rows_than_one_launch_takes(lib):
+    """2^25 + 5 rows of four slices: more than 2^30 threads of the second product.  Small
+    integers, so that every sum and result is exact."""
+    T, K, rank, slices, N = (1 << 25) + 5, 8, 8, 4, 32
+    g = torch.Generator("cuda").manual_seed(0)
+    x = torch.randint(-1, 2, (T, K), dtype=torch.int8, device="cuda", generator=g).to(BF)
+    ids = torch.randint(-1, 2, (T,), dtype=torch.int32, device="cuda", generator=g)
+    a = torch.randint(-1, 2, (2, slices * rank, K), device="cuda", generator=g).to(BF)
+    b = torch.randint(-1, 2, (2, N, rank), device="cuda", generator=g).to(BF)
+    lora = lib.Lora(a, b, torch.tensor([1.0, 2.0]).cuda(), slices=slices)
+    y = lib.lora(x, lora, ids)
+    for lo in (0, (1 << 23) - 40, (1 << 24) - 100, 3 << 23, T - 77):
+        r = slice(lo, min(lo + 200, T))
+        want = oracle.lora(f64(x[r]), f64(a), f64(b), np.array([1.0, 2.0]), ids[r].cpu().numpy(),
+                           np.zeros((x[r].shape[0], N)), slices)
+        assert np.abs(want).max() <= 256 and np.array_equal(f64(y[r]), want)
