@@ -75,7 +75,8 @@ def build_host_checker(out_dir: str, verbose: bool = False, program: str = "abi_
     program needs (all).  The programs call entry points with arguments that
     the host checks reject before any HIP call, so they run without a GPU:
     abi_checks those of the sparse path, abi_checks_operators the router's,
-    the norm's and those on microscaled rows."""
+    the norm's and those on microscaled rows, abi_checks_more the bf16 product's,
+    the gradients' and the adapters'."""
     os.makedirs(out_dir, exist_ok=True)
     san = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
            "-Xarch_host", "-fno-sanitize-recover=all", "-Xarch_host", "-fno-omit-frame-pointer"]
