@@ -516,7 +516,9 @@ moesq_status_t moesq_mx_gemm(const moesq_mx_t *x, const int32_t *perm, int32_t T
  *                    a gated feed-forward block's two projections, activation
  *                    and product
  *   x [T][K] (with perm) or [M][K]; w [E][N][K]; expert_offsets, perm, T, k,
- *   MOESQ_OUT_FLAT, rows outside every expert range: as moesq_mx_gemm.
+ *   MOESQ_OUT_FLAT, rows outside every expert range: as moesq_mx_gemm (a row
+ *   with perm[r] outside [0, T*k) is the product of a row of zeros: zero with
+ *   finite weights).
  *   z [M][N] bf16 out or NULL: with SWIGLU, bf16_rne(acc) in routed order, what
  *   moesq_gemm_dx takes in the backward pass (y comes from the unrounded
  *   sums).  Not with epilogue NONE, not with MOESQ_OUT_FLAT.
@@ -558,7 +560,7 @@ moesq_status_t moesq_gemm_dx(const uint16_t *dy, const int32_t *expert_offsets, 
  *   dw[e][n][c] = d_e[n][c] in `dtype` (MOESQ_BF16 rounded to nearest even, or
  *   MOESQ_F32); with `accumulate` (MOESQ_F32 only) dw[e][n][c] + d_e[n][c].
  *   dy [M][N] routed rows; x, perm, T, k, expert_offsets as moesq_gemm: rows with
- *   perm[r] outside [0, T*k) count as zero.
+ *   perm[r] outside [0, T*k) count as rows of zeros.
  *   dw [E][N][K]: every matrix is written, zeros (with `accumulate`: what was
  *   there) for experts without rows.
  * All buffers 16-byte aligned.  Limits: as moesq_gemm.

@@ -56,18 +56,19 @@ __device__ __forceinline__ void for_each(F &&f) {
 // The product of few rows: bound by the stream of weights.  A wave contracts FN
 // fragments of 16 weight rows with FM of 16 rows of x in stages of 64 positions,
 // copied to a ring of its own in LDS, DEPTH stages deep: whole lines, and all of
-// them under way at once.  No wave waits for another but for the final sum: KSPLIT
-// waves of a workgroup share their rows, each with its own stages, and add their
-// sums in LDS in a fixed order.  Stages that are not there are copied as zeros, so that
+// them under way at once.  No wave waits for another but for the final sum: KSPLIT of
+// the four waves of a workgroup share their rows, each with its own stages, and add
+// their sums in LDS in a fixed order.  Stages that are not there are copied as zeros, so that
 // the counts of copies in flight are constants.
 //
 // SwiGLU: rows 0-7 of a fragment are gate rows, 8-15 the up rows of the same
 // eight columns.
-constexpr int stream_waves(int ksplit) { return ksplit < 4 ? 4 : ksplit; }
+constexpr int STREAM_WAVES = 4;
 
 template <bool SWIGLU, int KSPLIT, int FN, int FM, int DEPTH>
-__global__ __launch_bounds__(stream_waves(KSPLIT) * 64) void gemm_stream_kernel(GemmArgs a) {
-  constexpr int WAVES = stream_waves(KSPLIT), RG = WAVES / KSPLIT;   // row groups of FN fragments a workgroup
+__global__ __launch_bounds__(STREAM_WAVES * 64) void gemm_stream_kernel(GemmArgs a) {
+  static_assert(KSPLIT == 2 || KSPLIT == 4, "sums are joined in LDS");
+  constexpr int WAVES = STREAM_WAVES, RG = WAVES / KSPLIT;   // row groups of FN fragments a workgroup
   constexpr int FC = SWIGLU ? 8 : 16;              // output columns a fragment
   constexpr int WC = FN * 2, XC = FM * 2;          // copies of a stage
   struct Ring {
@@ -164,21 +165,16 @@ __global__ __launch_bounds__(stream_waves(KSPLIT) * 64) void gemm_stream_kernel(
   wait_copies<0>();
 #pragma unroll
   for (int f = 0; f < FN; ++f) {
-    if constexpr (KSPLIT > 1) {
-      __syncthreads();
+    __syncthreads();
 #pragma unroll
-      for (int g = 0; g < FM; ++g) part[(wave * FM + g) * 64 + lane] = acc[f][g];
-      __syncthreads();
-    }
+    for (int g = 0; g < FM; ++g) part[(wave * FM + g) * 64 + lane] = acc[f][g];
+    __syncthreads();
 #pragma unroll
     for (int g = 0; g < FM; ++g) {
-      if (KSPLIT > 1 && g % KSPLIT != kw) continue;
-      f32x4_t v = acc[f][g];
-      if constexpr (KSPLIT > 1) {
-        v = part[((wave - kw) * FM + g) * 64 + lane];
+      if (g % KSPLIT != kw) continue;
+      f32x4_t v = part[((wave - kw) * FM + g) * 64 + lane];
 #pragma unroll
-        for (int w = 1; w < KSPLIT; ++w) v += part[((wave - kw + w) * FM + g) * 64 + lane];
-      }
+      for (int w = 1; w < KSPLIT; ++w) v += part[((wave - kw + w) * FM + g) * 64 + lane];
       f32x4_t h = v;
       if constexpr (SWIGLU) {
 #pragma unroll
@@ -198,9 +194,9 @@ __global__ __launch_bounds__(stream_waves(KSPLIT) * 64) void gemm_stream_kernel(
 
 template <bool SWIGLU, int KSPLIT, int FN, int FM, int DEPTH>
 static void launch_stream(GemmArgs a, hipStream_t stream) {
-  constexpr int THREADS = stream_waves(KSPLIT) * 64;
+  constexpr int THREADS = STREAM_WAVES * 64;
   const int cols = SWIGLU ? a.N / 2 : a.N, frags = (cols + (SWIGLU ? 7 : 15)) / (SWIGLU ? 8 : 16);
-  const int rg = stream_waves(KSPLIT) / KSPLIT * FN, groups = (frags + rg - 1) / rg;
+  const int rg = STREAM_WAVES / KSPLIT * FN, groups = (frags + rg - 1) / rg;
   const long long tiles = most_tiles(a, 16 * FM), part = std::max(1, MAX_LAUNCH_THREADS / THREADS / groups);
   for (long long first = 0; first < tiles; first += part) {
     a.item0 = (int)first;
@@ -586,10 +582,10 @@ __global__ __launch_bounds__(WP * WQ * 64, DEPTH > 2 ? 1 : 2) void gemm_tiled_ke
     const Tile done = t;
     const bool results = busy;
     if (WALK && next < last) {
-      // every wave is done with the buffers: its last reads were before the last barrier (without
-      // stages, the first), and its copies behind the end, zeros, have landed
+      // every wave is done with the buffers: its last reads were before the last barrier, and its
+      // copies behind the end, zeros, have landed
+      static_assert(!WALK || WHAT != GEMM_DW, "a tile has a stage (the gradient of no rows has none)");
       wait_copies<0>();
-      if (stages == 0) arrive(i0);
       t = nxt;
       start();
     }
@@ -763,7 +759,7 @@ static float tile_time(const GemmShape &g, int bp, int bq, int per_cu, float fir
 template <bool SWIGLU, int KSPLIT, int FN, int FM, int DEPTH>
 struct Stream {
   static float time(const GemmShape &g) {
-    constexpr int RG = stream_waves(KSPLIT) / KSPLIT;
+    constexpr int RG = STREAM_WAVES / KSPLIT;
     const long long groups = g.tiles(RG * FN * 16, FM * 16);
     const float copies = (float)((groups + g.cus - 1) / g.cus) * g.stages * RG * (FN + FM) * 2 / 100;
     return std::max(copies, (float)((g.stages + KSPLIT - 1) / KSPLIT) * 0.9f / DEPTH);
