@@ -42,6 +42,13 @@ __device__ __forceinline__ uint32_t bf16_bits_rne(float f) {
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return bf16_bits_rne(lo) | (bf16_bits_rne(hi) << 16);
 }
+// The same in the one instruction that the compiler has for it (equal for every fp32 number;
+// a NaN keeps its sign and upper bits).
+__device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{lo, hi}), bf16x2_t));
+}
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 

@@ -155,7 +155,7 @@ __global__ __launch_bounds__(DISPATCH_THREADS) void combine_grad_kernel(
           for (int j = 0; j < 4; ++j) {
             sum = fmaf(bf16_lo(p[j]), bf16_lo(q[j]), sum);
             sum = fmaf(bf16_hi(p[j]), bf16_hi(q[j]), sum);
-            b[j] = pack_bf16x2(wi * bf16_lo(p[j]), wi * bf16_hi(p[j]));
+            b[j] = round_bf16x2(wi * bf16_lo(p[j]), wi * bf16_hi(p[j]));
           }
           if (dy && c < N8) o[c] = make_uint4(b[0], b[1], b[2], b[3]);
         }

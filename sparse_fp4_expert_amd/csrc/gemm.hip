@@ -37,10 +37,6 @@ __device__ __forceinline__ void swiglu_grad(float d, float g, float u, float &dg
   du = d * (g * s);
 }
 
-// Buffers cover all that an offset of 32 bits reaches up to here, and a copy
-// from this offset is behind them (whether or not the check of the range counts the load's own).
-constexpr uint32_t NOWHERE = 0xffff0000u;
-
 template <typename F, int... I>
 __device__ __forceinline__ void for_each_in(std::integer_sequence<int, I...>, F &&f) {
   (f(std::integral_constant<int, I>{}), ...);
@@ -184,10 +180,10 @@ __global__ __launch_bounds__(STREAM_WAVES * 64) void gemm_stream_kernel(GemmArgs
       if (r >= t.rows || c >= cols) continue;
       const int dst = dst_row(a, t.row0 + r);
       if (dst >= 0 && (!SWIGLU || q < 2))
-        *reinterpret_cast<uint2 *>(a.y + (size_t)dst * cols + c) = make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+        *reinterpret_cast<uint2 *>(a.y + (size_t)dst * cols + c) = make_uint2(round_bf16x2(h[0], h[1]), round_bf16x2(h[2], h[3]));
       if (SWIGLU && a.z)
         *reinterpret_cast<uint2 *>(a.z + (size_t)(t.row0 + r) * a.N + (q < 2 ? 0 : cols) + c) =
-            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            make_uint2(round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3]));
     }
   }
 }
@@ -250,13 +246,6 @@ __device__ __forceinline__ void copy16_to_lds_at(uint32_t lds, i32x4_t buf, uint
 __device__ __forceinline__ int fresh(int lane) {
   asm volatile("" : "+v"(lane));
   return lane;
-}
-
-// Stores 16 bytes a lane, of lanes with an offset of NOWHERE none.  (Not in asm: behind a
-// store the compiler keeps its registers until it has read them.)
-__device__ __forceinline__ void store16(void *p, uint32_t voff, uint4 v) {
-  const auto buf = __builtin_amdgcn_make_buffer_rsrc(p, 0, (int)NOWHERE, 0x20000);
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, v), buf, (int)voff, 0, 0);
 }
 
 // The buffer, moved on by `by` bytes.
@@ -606,7 +595,7 @@ __global__ __launch_bounds__(WP * WQ * 64, DEPTH > 2 ? 1 : 2) void gemm_tiled_ke
       asm volatile("" ::: "memory");
     };
     auto pack = [](f32x4_t u, f32x4_t v) {
-      return make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      return make_uint4(round_bf16x2(u[0], u[1]), round_bf16x2(u[2], u[3]), round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3]));
     };
     // 16 rows x WB columns of bf16, and store(row of the tile, column, eight of them, whether they are there).
     uint16_t *mineb = reinterpret_cast<uint16_t *>(mine);
@@ -617,7 +606,7 @@ __global__ __launch_bounds__(WP * WQ * 64, DEPTH > 2 ? 1 : 2) void gemm_tiled_ke
       for (int f = 0; f < OF; ++f) {
         const f32x4_t v = value(f);
         *reinterpret_cast<uint2 *>(mineb + (ln & 15) * WB + 8 * turnb((ln & 15), 2 * f + ((ln >> 4) >> 1)) + 4 * ((ln >> 4) & 1)) =
-            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            make_uint2(round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3]));
       }
       asm volatile("" ::: "memory");
 #pragma unroll

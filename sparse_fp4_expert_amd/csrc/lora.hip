@@ -26,9 +26,7 @@ struct LoraArgs {
 
 constexpr float BF16_MAX = 0x1.fep127f;
 
-constexpr uint32_t LORA_NOWHERE = 0xffff0000u;   // an offset behind every buffer: copies from it are zeros
-
-// The tile's adapters in order of their first rows: f(number, id, rows that have it).
+// The tile's adapters in order of their first rows: f(number, rows that have it).
 // Lane l holds the id of row l of the tile, -1 for none; all lanes take part.
 template <typename F>
 __device__ __forceinline__ void each_adapter(int id, F &&f) {
@@ -36,7 +34,7 @@ __device__ __forceinline__ void each_adapter(int id, F &&f) {
   for (int n = 0; left; ++n) {
     const int cur = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
     const uint64_t rows = __ballot(id == cur);
-    f(n, cur, rows);
+    f(n, rows);
     left &= ~rows;
   }
 }
@@ -51,7 +49,8 @@ __device__ __forceinline__ int lora_id(const LoraArgs &l, int row, bool there) {
 // 16 FM rows and 16 FN ranks a workgroup, K over `splits` workgroups and the four
 // waves of each: a wave copies stages of 64 positions of its own to a ring in LDS,
 // DEPTH deep, contracts them on the 16 x 16 x 32 MFMA, and the waves add their sums in
-// LDS in order.  Rows of other adapters are not copied (zeros).
+// LDS in order.  A tile's adapters follow one another in the stages, with zeros for the rows
+// of others, so that one accumulator, whose columns are the rows, takes them all.
 template <int FN, int FM, int DEPTH>
 __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
   constexpr int AC = FN * 2, XC = FM * 2;          // copies of a stage
@@ -75,81 +74,101 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
   const int n = ((K + 63) / 64 - first + step - 1) / step;   // this wave's stages: first, first + step, ...
   const uint32_t lds0 = lds_offset(&ring[wave][0]);
   auto pos = [&](int i) { return 8 * piece4(8 * i + (lane >> 3), lane & 7); };
-  const i32x4_t xbuf = raw_buffer(l.x + (size_t)row0 * K, LORA_NOWHERE);
+  const i32x4_t xbuf = raw_buffer(l.x + (size_t)row0 * K, NOWHERE);
 
-  each_adapter(lora_id(l, row0 + lane, lane < 16 * FM), [&](int number, int cur, uint64_t rows) {
-    if (number % l.lanes != mine) return;
-    const i32x4_t abuf = raw_buffer(l.a + (size_t)cur * R * K, LORA_NOWHERE);
-    uint32_t ao[AC], xo[XC];
+  const int id = lora_id(l, row0 + lane, lane < 16 * FM);
+  uint64_t left = __ballot(id >= 0), own = 0;      // rows that no copies were made for; of this workgroup's adapters
+  int number = 0, stage = 0, under_way = 0;        // of the adapter and of its stages that are copied next; stages in all
+  i32x4_t abuf = xbuf;
+  uint32_t ao[AC], xo[XC];
 #pragma unroll
-    for (int i = 0; i < AC; ++i) {
-      const int r = r0 + 8 * i + (lane >> 3);
-      ao[i] = r < R ? ((uint32_t)r * (uint32_t)K + pos(i)) * 2 : LORA_NOWHERE;
+  for (int i = 0; i < AC; ++i) {
+    const int r = r0 + 8 * i + (lane >> 3);
+    ao[i] = r < R ? ((uint32_t)r * (uint32_t)K + pos(i)) * 2 : NOWHERE;
+  }
+  // The next of this workgroup's adapters, if there is one.
+  auto next_adapter = [&] {
+    while (left) {
+      const int cur = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
+      const uint64_t rows = __ballot(id == cur);
+      left &= ~rows;
+      if (number++ % l.lanes != mine) continue;
+      abuf = raw_buffer(l.a + (size_t)cur * R * K, NOWHERE);
+#pragma unroll
+      for (int i = 0; i < XC; ++i) {
+        const int r = 8 * i + (lane >> 3);
+        xo[i] = (rows >> r) & 1 ? ((uint32_t)r * (uint32_t)K + pos(i)) * 2 : NOWHERE;
+      }
+      own |= rows;
+      stage = 0;
+      return;
     }
+    stage = n;
+  };
+  // Copies the next stage (zeros if there is none).
+  auto fetch = [&](int slot) {
+    if (stage == n && left) next_adapter();
+    const int c = stage < n ? first + stage * step : (K + 63) / 64;
+    const uint32_t to = lds0 + slot * (uint32_t)sizeof(Ring);
 #pragma unroll
-    for (int i = 0; i < XC; ++i) {
-      const int r = 8 * i + (lane >> 3);
-      xo[i] = (rows >> r) & 1 ? ((uint32_t)r * (uint32_t)K + pos(i)) * 2 : LORA_NOWHERE;
-    }
-    auto fetch = [&](int slot, int c) {            // (stages that are not there are copied as zeros)
-      const uint32_t to = lds0 + slot * (uint32_t)sizeof(Ring);
+    for (int i = 0; i < AC; ++i)
+      copy16_to_lds(to + i * 1024, abuf, ao[i] != NOWHERE && 64 * c + pos(i) < K ? ao[i] + 128 * c : NOWHERE);
 #pragma unroll
-      for (int i = 0; i < AC; ++i)
-        copy16_to_lds(to + i * 1024, abuf, ao[i] != LORA_NOWHERE && 64 * c + pos(i) < K ? ao[i] + 128 * c : LORA_NOWHERE);
+    for (int i = 0; i < XC; ++i)
+      copy16_to_lds(to + (AC + i) * 1024, xbuf, xo[i] != NOWHERE && 64 * c + pos(i) < K ? xo[i] + 128 * c : NOWHERE);
+    if (stage < n) ++stage, ++under_way;
+  };
+  next_adapter();
+  if (!own) return;
 #pragma unroll
-      for (int i = 0; i < XC; ++i)
-        copy16_to_lds(to + (AC + i) * 1024, xbuf, xo[i] != LORA_NOWHERE && 64 * c + pos(i) < K ? xo[i] + 128 * c : LORA_NOWHERE);
+  for (int i = 0; i < DEPTH; ++i) fetch(i);
+  f32x4_t acc[FN][FM];
+#pragma unroll
+  for (int f = 0; f < FN; ++f)
+#pragma unroll
+    for (int g = 0; g < FM; ++g) acc[f][g] = f32x4_t{0, 0, 0, 0};
+  for (int i = 0; i < under_way; ++i) {
+    wait_copies<(AC + XC) * (DEPTH - 1)>();
+    const Ring &k = ring[wave][i % DEPTH];
+    auto operand = [&](const uint8_t *p, int f, int s) {
+      const int r = 16 * f + rl;
+      return as_bf16x8(*reinterpret_cast<const uint4 *>(p + r * 128 + 16 * piece4(r, 4 * s + q)));
     };
 #pragma unroll
-    for (int i = 0; i < DEPTH; ++i) fetch(i, first + i * step);
-    f32x4_t acc[FN][FM];
+    for (int s = 0; s < 2; ++s) {
+      bf16x8_t X[FM];
 #pragma unroll
-    for (int f = 0; f < FN; ++f)
+      for (int g = 0; g < FM; ++g) X[g] = operand(k.x, g, s);
 #pragma unroll
-      for (int g = 0; g < FM; ++g) acc[f][g] = f32x4_t{0, 0, 0, 0};
-    for (int i = 0; i < n; ++i) {
-      wait_copies<(AC + XC) * (DEPTH - 1)>();
-      const Ring &k = ring[wave][i % DEPTH];
-      auto operand = [&](const uint8_t *p, int f, int s) {
-        const int r = 16 * f + rl;
-        return as_bf16x8(*reinterpret_cast<const uint4 *>(p + r * 128 + 16 * piece4(r, 4 * s + q)));
-      };
+      for (int f = 0; f < FN; ++f) {
+        const bf16x8_t A = operand(k.a, f, s);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        bf16x8_t X[FM];
-#pragma unroll
-        for (int g = 0; g < FM; ++g) X[g] = operand(k.x, g, s);
-#pragma unroll
-        for (int f = 0; f < FN; ++f) {
-          const bf16x8_t A = operand(k.a, f, s);
-#pragma unroll
-          for (int g = 0; g < FM; ++g) acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, X[g], acc[f][g], 0, 0, 0);
-        }
-      }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot's reads are done before it is written again
-      fetch(i % DEPTH, first + (i + DEPTH) * step);
-    }
-    wait_copies<0>();
-    f32x4_t *part = reinterpret_cast<f32x4_t *>(&ring[0][0]);     // [waves][FM][64]
-#pragma unroll
-    for (int f = 0; f < FN; ++f) {
-      __syncthreads();
-#pragma unroll
-      for (int g = 0; g < FM; ++g) part[(wave * FM + g) * 64 + lane] = acc[f][g];
-      __syncthreads();
-#pragma unroll
-      for (int g = 0; g < FM; ++g) {
-        if ((f * FM + g) % 4 != wave) continue;
-        f32x4_t v = part[g * 64 + lane];
-#pragma unroll
-        for (int w = 1; w < 4; ++w) v += part[(w * FM + g) * 64 + lane];
-        const int r = 16 * g + rl, j = r0 + 16 * f + 4 * q;
-        if (((rows >> r) & 1) && j < R)
-          *reinterpret_cast<f32x4_t *>(l.v + ((size_t)split * l.T + row0 + r) * R + j) = v;
+        for (int g = 0; g < FM; ++g) acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, X[g], acc[f][g], 0, 0, 0);
       }
     }
-    __syncthreads();                               // the sums are read before the next adapter's copies
-  });
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot's reads are done before it is written again
+    fetch(i % DEPTH);
+  }
+  while (left) next_adapter();                     // (a wave without stages has not gone over all of them)
+  wait_copies<0>();
+  f32x4_t *part = reinterpret_cast<f32x4_t *>(&ring[0][0]);     // [waves][FM][64]
+#pragma unroll
+  for (int f = 0; f < FN; ++f) {
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < FM; ++g) part[(wave * FM + g) * 64 + lane] = acc[f][g];
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < FM; ++g) {
+      if ((f * FM + g) % 4 != wave) continue;
+      f32x4_t v = part[g * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) v += part[(w * FM + g) * 64 + lane];
+      const int r = 16 * g + rl, j = r0 + 16 * f + 4 * q;
+      if (((own >> r) & 1) && j < R)
+        *reinterpret_cast<f32x4_t *>(l.v + ((size_t)split * l.T + row0 + r) * R + j) = v;
+    }
+  }
 }
 
 // ------------------------------------------------------------------ base + scale v b'
@@ -174,8 +193,11 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs l) {
   const int s = wg / tiles % (cols / seg), mine = wg / tiles / (cols / seg);
   const int col0 = s * seg + c * l.chunk, end = min(col0 + l.chunk, (s + 1) * seg);
   const int id = lora_id(l, row0 + lane, lane < 16 * FM);
-  uint64_t own = 0;                                // rows of this workgroup's adapters
-  each_adapter(id, [&](int number, int, uint64_t rows) { own |= number % l.lanes == mine ? rows : 0; });
+  uint64_t own = __ballot(id >= 0);                // rows of this workgroup's adapters
+  if (l.lanes > 1) {
+    own = 0;
+    each_adapter(id, [&](int number, uint64_t rows) { own |= number % l.lanes == mine ? rows : 0; });
+  }
   for (int u = threadIdx.x; u < H * 16 * FM * NS * 4; u += 256) {   // eight ranks at a time
     const int p = u % (NS * 4) * 8, row = u / (NS * 4) % (16 * FM), h = u / (NS * 4 * 16 * FM);
     f32x4_t sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
@@ -200,8 +222,8 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs l) {
     for (int i = 0; i < 4; ++i) {
       const float x0 = sum[i / 2][2 * (i & 1)], x1 = sum[i / 2][2 * (i & 1) + 1];
       // (what is larger than the largest finite bf16, infinite or not, is left to the rest)
-      hi[i] = pack_bf16x2(__builtin_amdgcn_fmed3f(x0, -BF16_MAX, BF16_MAX), __builtin_amdgcn_fmed3f(x1, -BF16_MAX, BF16_MAX));
-      lo[i] = pack_bf16x2(x0 - bf16_lo(hi[i]), x1 - bf16_hi(hi[i]));
+      hi[i] = round_bf16x2(__builtin_amdgcn_fmed3f(x0, -BF16_MAX, BF16_MAX), __builtin_amdgcn_fmed3f(x1, -BF16_MAX, BF16_MAX));
+      lo[i] = round_bf16x2(x0 - bf16_lo(hi[i]), x1 - bf16_hi(hi[i]));
     }
     *reinterpret_cast<uint4 *>(&sums[h][0][row][p]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4 *>(&sums[h][1][row][p]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -219,60 +241,76 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs l) {
         lo[h][g][j] = as_bf16x8(*reinterpret_cast<const uint4 *>(&sums[h][1][16 * g + rl][32 * j + 8 * q]));
       }
 
-  // this lane's rows: whether they have an adapter of this workgroup's, or (the first's) none
+  // rows without an adapter: the first workgroup's
   const int there = min(l.T - row0, 16 * FM);
   const uint64_t live = there >= 64 ? ~0ull : (1ull << there) - 1;
   const uint64_t none = mine == 0 && (l.base != l.y || SWIGLU) ? live & ~__ballot(id >= 0) : 0;
+  const int first = own ? __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)own) - 1) : -1;
+  const bool one = own == live && !(own & ~__ballot(id == first));   // one adapter for all rows
+  // This lane's rows.  Without an adapter the sum is 0 and the scale -0: the base stays as it is.
   float scale[FM];
   int ids[FM];
+  uint32_t from[FM], to[FM];                       // this lane's columns of the rows, in base and y
 #pragma unroll
   for (int g = 0; g < FM; ++g) {
-    ids[g] = __shfl(id, 16 * g + rl, 64);
-    scale[g] = (own >> (16 * g + rl)) & 1 ? l.scale[ids[g]] : 0.0f;
+    const int r = 16 * g + rl;
+    ids[g] = __shfl(id, r, 64);
+    scale[g] = (own >> r) & 1 ? l.scale[ids[g]] : -0.0f;
+    const bool mine = ((own | none) >> r) & 1;
+    from[g] = mine ? ((uint32_t)r * (uint32_t)N + 8 * q) * 2 : NOWHERE;
+    to[g] = mine ? ((uint32_t)r * (uint32_t)cols + 8 * q) * 2 : NOWHERE;
   }
+  // This lane's part of an adapter's columns.  (Those behind the last one are not stored, and
+  // behind the adapter zeros, as are ranks that are not there.)
+  constexpr uint32_t BEHIND = 1u << 31;
+  const uint32_t all = (uint32_t)N * (uint32_t)rank * 2;
+  uint32_t part_of[H][2], ranks[NS];
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+      part_of[h][f] = ((uint32_t)(8 * (rl >> 2) + 4 * f + (rl & 3) + h * cols) * (uint32_t)rank + 8 * q) * 2;
+#pragma unroll
+  for (int j = 0; j < NS; ++j) ranks[j] = 32 * j + 8 * q < rank ? 64 * j : BEHIND;
   struct Columns {
     bf16x8_t b[H][2][NS];
   };
+  auto load = [&](Columns &c, int cur, int col) {
+    const uint16_t *b = l.b + (size_t)cur * N * rank;
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+          c.b[h][f][j] = as_bf16x8(load16(b, all, part_of[h][f] + (uint32_t)col * (uint32_t)rank * 2 + ranks[j]));
+  };
+  const uint16_t *base0 = l.base + (size_t)row0 * N;
+  uint16_t *y0 = l.y + (size_t)row0 * cols;
   for (int col = col0; col < end; col += 32) {
-    const int at = col + 8 * q;
+    const bool in = col + 8 * q < end;
     uint4 base[H][FM];
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
       for (int g = 0; g < FM; ++g)
-        base[h][g] = l.base && at < end && (((own | none) >> (16 * g + rl)) & 1)
-                         ? *reinterpret_cast<const uint4 *>(l.base + (size_t)(row0 + 16 * g + rl) * N + at + h * cols)
-                         : make_uint4(0, 0, 0, 0);
-    // this lane's part of an adapter's columns
-    auto load = [&](Columns &to, int cur) {
-      const uint16_t *b = l.b + (size_t)cur * N * rank;
-#pragma unroll
-      for (int h = 0; h < H; ++h)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const int n = min(col + 8 * (rl >> 2) + 4 * f + (rl & 3), end - 1) + h * cols;
-#pragma unroll
-          for (int j = 0; j < NS; ++j) {
-            const int p = 32 * j + 8 * q;
-            to.b[h][f][j] = as_bf16x8(p < rank ? *reinterpret_cast<const uint4 *>(b + (uint32_t)n * (uint32_t)rank + p)
-                                               : make_uint4(0, 0, 0, 0));
-          }
-        }
-    };
+        base[h][g] = l.base ? load16(base0, NOWHERE, in && from[g] != NOWHERE ? from[g] + (col + h * cols) * 2 : NOWHERE)
+                            : make_uint4(0, 0, 0, 0);
     f32x4_t d[H][FM][2];
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
       for (int g = 0; g < FM; ++g) d[h][g][0] = d[h][g][1] = f32x4_t{0, 0, 0, 0};
-    // adapter by adapter, the next one's columns under way
+    // adapter by adapter, the next one's columns under way where there are registers for them
+    constexpr bool AHEAD = H * NS < 16;
     uint64_t left = own;
-    int cur = left ? __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1) : -1;
+    int cur = first;
     Columns now, next;
-    if (cur >= 0) load(now, cur);
+    if (left) load(now, cur, col);
     while (left) {
       left &= ~__ballot(id == cur);
       const int then = left ? __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1) : -1;
-      if (then >= 0) load(next, then);
+      if (AHEAD && left) load(next, then, col);
 #pragma unroll
       for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -285,32 +323,29 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs l) {
               v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.b[h][f][j], lo[h][g][j], v, 0, 0, 0);
               v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.b[h][f][j], hi[h][g][j], v, 0, 0, 0);
             }
+            if (one) d[h][g][f] = v;
+            else
 #pragma unroll
-            for (int i = 0; i < 4; ++i) d[h][g][f][i] = ids[g] == cur ? v[i] : d[h][g][f][i];
+              for (int i = 0; i < 4; ++i) d[h][g][f][i] = ids[g] == cur ? v[i] : d[h][g][f][i];
           }
-      now = next;
+      if (AHEAD) now = next;
+      else if (left) load(now, then, col);
       cur = then;
     }
 #pragma unroll
     for (int g = 0; g < FM; ++g) {
-      const int r = 16 * g + rl;
-      if (!(((own | none) >> r) & 1) || at >= end) continue;
-      const bool has = (own >> r) & 1;
       float p[H][8];
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         const uint32_t u[4] = {base[h][g].x, base[h][g].y, base[h][g].z, base[h][g].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float in = i & 1 ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]);
-          p[h][i] = has ? fmaf(scale[g], d[h][g][i / 4][i & 3], in) : in;
-        }
+        for (int i = 0; i < 8; ++i) p[h][i] = fmaf(scale[g], d[h][g][i / 4][i & 3], i & 1 ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]));
       }
       float o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = SWIGLU ? silu_f32(p[0][i]) * p[H - 1][i] : p[0][i];
-      *reinterpret_cast<uint4 *>(l.y + (size_t)(row0 + r) * cols + at) =
-          make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+      store16(y0, in && to[g] != NOWHERE ? to[g] + col * 2 : NOWHERE,
+              make_uint4(round_bf16x2(o[0], o[1]), round_bf16x2(o[2], o[3]), round_bf16x2(o[4], o[5]), round_bf16x2(o[6], o[7])));
     }
   }
 }
@@ -336,7 +371,7 @@ static LoraPlan lora_plan(const moesq_lora_t &l, int T) {
   const long long base = std::max(1ll, (long long)((T + tile - 1) / tile) * ((R + 16 * p.fn - 1) / (16 * p.fn)));
   auto within = [](long long v, long long most) { return (int)std::max(1ll, std::min(v, most)); };
   p.splits = within(LORA_CUS / (p.fm == 4 ? 1 : 2) / base, std::min(8, (stages + 3) / 4));
-  p.lanes = within(4 * LORA_CUS / (base * p.splits), std::min(std::min(16, T), l.adapters));
+  p.lanes = within((p.fm == 4 ? 1 : 4) * LORA_CUS / (base * p.splits), std::min(std::min(16, T), l.adapters));
   return p;
 }
 

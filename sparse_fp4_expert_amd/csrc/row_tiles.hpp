@@ -159,6 +159,23 @@ __device__ __forceinline__ void wait_copies() {   // all but the last N have lan
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// Buffers cover all that an offset of 32 bits reaches up to here, and a copy
+// from this offset is behind them (whether or not the check of the range counts the load's own).
+constexpr uint32_t NOWHERE = 0xffff0000u;
+
+// Stores 16 bytes a lane, of lanes with an offset of NOWHERE none.  (Not in asm: behind a
+// store the compiler keeps its registers until it has read them.)
+__device__ __forceinline__ void store16(void *p, uint32_t voff, uint4 v) {
+  const auto buf = __builtin_amdgcn_make_buffer_rsrc(p, 0, (int)NOWHERE, 0x20000);
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, v), buf, (int)voff, 0, 0);
+}
+
+// Loads 16 bytes a lane from the first `bytes` behind p, zeros for lanes with an offset behind those.
+__device__ __forceinline__ uint4 load16(const void *p, uint32_t bytes, uint32_t voff) {
+  const auto buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x20000);
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(buf, (int)voff, 0, 0));
+}
+
 // Chunk positions in LDS: rows are as in memory, their 16-byte pieces permuted
 // by the row number so that the 16 rows that read one piece together touch
 // all 64 banks once.  Piece c of row r of 128-byte rows (256 positions of
