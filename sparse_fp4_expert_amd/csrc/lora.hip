@@ -50,7 +50,7 @@ __device__ __forceinline__ int lora_id(const LoraArgs &l, int row, bool there) {
 // waves of each: a wave copies stages of 64 positions of its own to a ring in LDS,
 // DEPTH deep, contracts them on the 16 x 16 x 32 MFMA, and the waves add their sums in
 // LDS in order.  A tile's adapters follow one another in the stages, with zeros for the rows
-// of others, so that one accumulator, whose columns are the rows, takes them all.
+// of others, which keep their sums when an adapter ends.
 template <int FN, int FM, int DEPTH>
 __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
   constexpr int AC = FN * 2, XC = FM * 2;          // copies of a stage
@@ -79,6 +79,7 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
   const int id = lora_id(l, row0 + lane, lane < 16 * FM);
   uint64_t left = __ballot(id >= 0), own = 0;      // rows that no copies were made for; of this workgroup's adapters
   int number = 0, stage = 0, under_way = 0;        // of the adapter and of its stages that are copied next; stages in all
+  uint64_t its_rows = 0, rows_of[DEPTH] = {};      // its rows; those of the adapters of the stages in flight
   i32x4_t abuf = xbuf;
   uint32_t ao[AC], xo[XC];
 #pragma unroll
@@ -99,17 +100,20 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
         const int r = 8 * i + (lane >> 3);
         xo[i] = (rows >> r) & 1 ? ((uint32_t)r * (uint32_t)K + pos(i)) * 2 : NOWHERE;
       }
-      own |= rows;
+      own |= its_rows = rows;
       stage = 0;
       return;
     }
     stage = n;
   };
-  // Copies the next stage (zeros if there is none).
+  // Copies the next stage (zeros if there is none, so that the number of copies in flight is constant).
   auto fetch = [&](int slot) {
     if (stage == n && left) next_adapter();
     const int c = stage < n ? first + stage * step : (K + 63) / 64;
     const uint32_t to = lds0 + slot * (uint32_t)sizeof(Ring);
+#pragma unroll
+    for (int d = 0; d + 1 < DEPTH; ++d) rows_of[d] = rows_of[d + 1];
+    rows_of[DEPTH - 1] = stage < n ? its_rows : 0;
 #pragma unroll
     for (int i = 0; i < AC; ++i)
       copy16_to_lds(to + i * 1024, abuf, ao[i] != NOWHERE && 64 * c + pos(i) < K ? ao[i] + 128 * c : NOWHERE);
@@ -122,13 +126,14 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
   if (!own) return;
 #pragma unroll
   for (int i = 0; i < DEPTH; ++i) fetch(i);
-  f32x4_t acc[FN][FM];
+  f32x4_t acc[FN][FM], sum[FN][FM];
 #pragma unroll
   for (int f = 0; f < FN; ++f)
 #pragma unroll
-    for (int g = 0; g < FM; ++g) acc[f][g] = f32x4_t{0, 0, 0, 0};
+    for (int g = 0; g < FM; ++g) acc[f][g] = sum[f][g] = f32x4_t{0, 0, 0, 0};
   for (int i = 0; i < under_way; ++i) {
     wait_copies<(AC + XC) * (DEPTH - 1)>();
+    const uint64_t rows = rows_of[0];
     const Ring &k = ring[wave][i % DEPTH];
     auto operand = [&](const uint8_t *p, int f, int s) {
       const int r = 16 * f + rl;
@@ -136,14 +141,27 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
     };
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      bf16x8_t X[FM];
+      bf16x8_t A[FN];
 #pragma unroll
-      for (int g = 0; g < FM; ++g) X[g] = operand(k.x, g, s);
+      for (int f = 0; f < FN; ++f) A[f] = operand(k.a, f, s);
 #pragma unroll
-      for (int f = 0; f < FN; ++f) {
-        const bf16x8_t A = operand(k.a, f, s);
+      for (int g = 0; g < FM; ++g) {
+        const bf16x8_t X = operand(k.x, g, s);
 #pragma unroll
-        for (int g = 0; g < FM; ++g) acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, X[g], acc[f][g], 0, 0, 0);
+        for (int f = 0; f < FN; ++f) acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[f], X, acc[f][g], 0, 0, 0);
+      }
+    }
+    if (rows != rows_of[1]) {                      // the adapter's last stage
+#pragma unroll
+      for (int g = 0; g < FM; ++g) {
+        const bool its = rows >> (16 * g + rl) & 1;
+#pragma unroll
+        for (int f = 0; f < FN; ++f)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sum[f][g][i] = its ? acc[f][g][i] : sum[f][g][i];
+            acc[f][g][i] = 0.0f;
+          }
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot's reads are done before it is written again
@@ -156,7 +174,7 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
   for (int f = 0; f < FN; ++f) {
     __syncthreads();
 #pragma unroll
-    for (int g = 0; g < FM; ++g) part[(wave * FM + g) * 64 + lane] = acc[f][g];
+    for (int g = 0; g < FM; ++g) part[(wave * FM + g) * 64 + lane] = sum[f][g];
     __syncthreads();
 #pragma unroll
     for (int g = 0; g < FM; ++g) {

@@ -131,6 +131,27 @@ def test_a_row_is_its_own(lib):
         assert torch.equal(lib.lora(c.x, c.lora, ids, base=c.base)[live], want[live])
 
 
+@pytest.mark.parametrize("T, A, rank, runs", [(19, 3, 8, False), (40, 5, 24, False), (70, 4, 72, False), (1500, 3, 40, True),
+                                              (1300, 4, 64, False)])
+def test_other_adapters_infinite(lib, T, A, rank, runs):
+    """Rows of one tile with adapters of which one is not finite: the others' stay as they are."""
+    c = Case(lib, T, A, rank, 1, 72, 328, seed=3, runs=runs)
+    y = lib.lora(c.x, c.lora, c.ids, base=c.base)
+    for e, v in ((1, float("inf")), (2, float("nan"))):
+        keep = c.ids != e
+        assert keep.any() and not keep.all()
+        was = c.a[e].clone(), c.b[e].clone()
+        for a, b in ((True, False), (False, True)):
+            c.a[e], c.b[e] = was
+            if a:
+                c.a[e] = v
+            if b:
+                c.b[e] = v
+            got = lib.lora(c.x, c.lora, c.ids, base=c.base)
+            assert torch.equal(got[keep], y[keep]) and not got[~keep].isfinite().all()
+        c.a[e], c.b[e] = was
+
+
 def test_beside_projections(lib):
     """The shared expert of a serving step: gate and up with adapters of their
     own, SwiGLU behind them, the down projection with its adapters; MX and bf16
