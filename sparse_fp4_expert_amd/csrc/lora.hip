@@ -8,6 +8,12 @@
 // adapter or two a tile); in a decode batch every row may have its own, and its
 // adapter has to be read for it anyway.  No sorting, nothing that the host would
 // have to know.  Bound by memory: x in, base in, y out, and the adapters.
+//
+// Measured, first and second product: one row, rank 16, 2048 x 2048 3.9 + 3.9 us; 64 rows of
+// 32 adapters of rank 16, two slices, 4096 x 7168 with SwiGLU 9.7 + 6.8; 8192 rows of requests on 8
+// adapters of rank 64, 4096 x 7168, 41 + 46 with x and base from memory (34 + 37 where they are in
+// the caches).  With one adapter for all rows 25 + 40: a tile of several takes a pass over K for
+// each, and the last of them ends alone.
 #include "row_tiles.hpp"
 
 namespace moesq {
@@ -50,7 +56,8 @@ __device__ __forceinline__ int lora_id(const LoraArgs &l, int row, bool there) {
 // waves of each: a wave copies stages of 64 positions of its own to a ring in LDS,
 // DEPTH deep, contracts them on the 16 x 16 x 32 MFMA, and the waves add their sums in
 // LDS in order.  A tile's adapters follow one another in the stages, with zeros for the rows
-// of others, which keep their sums when an adapter ends.
+// of others, which keep their sums when an adapter ends.  (Leaving out the copies of 16 rows
+// without a row of the adapter's gave nothing.)
 template <int FN, int FM, int DEPTH>
 __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
   constexpr int AC = FN * 2, XC = FM * 2;          // copies of a stage
@@ -195,7 +202,10 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
 // one slice of each half).  v is the second operand of the MFMA, as two bf16 numbers
 // whose sum is within 2^-17 of the fp32 sum: the workgroup adds up the splits' sums of its rows
 // and keeps them so in LDS.  Two fragments of 16 columns are interleaved by fours, so that a
-// lane's results are eight neighbouring columns.
+// lane's results are eight neighbouring columns.  Instructions and latency bound it as much as memory
+// does: without base and y it takes 25 us of the 46 (8192 rows).  Loading the next columns ahead of
+// their use cost a wave of four on a SIMD and 2 us; storing whole lines of 128 bytes, by an exchange
+// between neighbouring rows, saved 3 us there and cost 10 % with many adapters a tile or SwiGLU.
 template <bool SWIGLU, int NS, int FM>             // NS: steps of 32 ranks
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs l) {
   constexpr int H = SWIGLU ? 2 : 1, PITCH = NS * 32 + 8;   // of a row in LDS: the rows that are read together in other banks
@@ -423,7 +433,8 @@ static void launch_lora(const LoraArgs &l, const LoraPlan &p, hipStream_t stream
   DOWN(4, 4, 2);
 #undef DOWN
   // Many rows of ranks up to 64: 32 at a time, which reads an adapter half as often (8192 rows,
-  // rank 64, to 4096: 49 us; 16 at a time 58, 64 at a time, with half the waves on a SIMD, 54).
+  // rank 64, to 4096, before the roundings took one instruction: 49 us; 16 at a time 58, 64 at a time, with
+  // half the waves on a SIMD, 54).
   const bool many = l.T > 1024;
   if (l.rank <= 32) launch_up<SWIGLU, 1, 1>(l, stream);
   else if (l.rank <= 64) many ? launch_up<SWIGLU, 2, 2>(l, stream) : launch_up<SWIGLU, 2, 1>(l, stream);
