@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
   uint64_t left = __ballot(id >= 0), own = 0;      // rows that no copies were made for; of this workgroup's adapters
   int number = 0, stage = 0, under_way = 0;        // of the adapter and of its stages that are copied next; stages in all
   uint64_t its_rows = 0, rows_of[DEPTH] = {};      // its rows; those of the adapters of the stages in flight
-  i32x4_t abuf = xbuf;
+  const uint16_t *its_a = l.a;
   uint32_t ao[AC], xo[XC];
 #pragma unroll
   for (int i = 0; i < AC; ++i) {
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
       const uint64_t rows = __ballot(id == cur);
       left &= ~rows;
       if (number++ % l.lanes != mine) continue;
-      abuf = raw_buffer(l.a + (size_t)cur * R * K, NOWHERE);
+      its_a = l.a + (size_t)cur * R * K;
 #pragma unroll
       for (int i = 0; i < XC; ++i) {
         const int r = 8 * i + (lane >> 3);
@@ -118,6 +118,7 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
     if (stage == n && left) next_adapter();
     const int c = stage < n ? first + stage * step : (K + 63) / 64;
     const uint32_t to = lds0 + slot * (uint32_t)sizeof(Ring);
+    const i32x4_t abuf = raw_buffer(its_a, NOWHERE);
 #pragma unroll
     for (int d = 0; d + 1 < DEPTH; ++d) rows_of[d] = rows_of[d + 1];
     rows_of[DEPTH - 1] = stage < n ? its_rows : 0;
