@@ -556,20 +556,26 @@ moesq_status_t moesq_gemm_dx(const uint16_t *dy, const int32_t *expert_offsets, 
 /*
  * Gradient of the weights of moesq_gemm:
  *   d_e[n][c] = sum over r in [offsets[e], offsets[e+1]) of dy[r][n] * x[src(r)][c]
- *                                                    (fp32 accumulation, in row order)
+ *                                                    (fp32 accumulation, in a fixed order)
  *   dw[e][n][c] = d_e[n][c] in `dtype` (MOESQ_BF16 rounded to nearest even, or
  *   MOESQ_F32); with `accumulate` (MOESQ_F32 only) dw[e][n][c] + d_e[n][c].
  *   dy [M][N] routed rows; x, perm, T, k, expert_offsets as moesq_gemm: rows with
  *   perm[r] outside [0, T*k) count as rows of zeros.
  *   dw [E][N][K]: every matrix is written, zeros (with `accumulate`: what was
  *   there) for experts without rows.
+ *   ws, ws_bytes: NULL, or a workspace of moesq_gemm_dw_workspace_bytes() bytes,
+ *   written and read by this call alone, with which few matrices of many rows
+ *   are summed in parts.  (Its size may be 0; results with and without it differ
+ *   by the order of their sums.)
  * All buffers 16-byte aligned.  Limits: as moesq_gemm.
  * Results are bit-identical on every run.
  */
 moesq_status_t moesq_gemm_dw(const uint16_t *dy, const uint16_t *x, const int32_t *perm, int32_t T,
                              int32_t k, const int32_t *expert_offsets, int32_t M, int32_t E,
                              int32_t N, int32_t K, int32_t dtype, int32_t accumulate, void *dw,
-                             hipStream_t stream);
+                             void *ws, size_t ws_bytes, hipStream_t stream);
+/* 0 also for sizes that moesq_gemm_dw refuses. */
+size_t moesq_gemm_dw_workspace_bytes(int32_t M, int32_t E, int32_t N, int32_t K);
 
 /*
  * Low-rank adapters of many requests beside a shared projection (whatever

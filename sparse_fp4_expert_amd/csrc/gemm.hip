@@ -24,6 +24,7 @@ struct GemmArgs {
   int k, M, E, N, K;
   int flat;
   bool out32, accumulate;
+  int parts;                   // dw: of each expert's rows, a result of their own for each, [parts][E][N][K]
   int item0;                   // first item of this launch: row tile (streaming kernel) or tile (dw)
   uint32_t k_mul, k_shift;     // n / k = (n * k_mul) >> (32 + k_shift) for k > 1 and n < 2^31
 };
@@ -305,11 +306,11 @@ __global__ __launch_bounds__(WP * WQ * 64, DEPTH > 2 ? 1 : 2) void gemm_tiled_ke
   // share panels of both operands in its L2; with WALK, each walks the run by the number of
   // them.  (Gradients of many experts' weights have nothing to share.)
   struct Tile {
-    int e, row0, rows, c0, lo, C;                  // rows [row0, row0 + rows) of expert e, columns from c0; C positions, from lo on (dw)
+    int e, row0, rows, c0, lo, C;                  // rows [row0, row0 + rows) of expert (dw: matrix) e, columns from c0; C positions, from lo on (dw)
   };
   const int qt = WHAT == GEMM_DW ? (a.N + BQ - 1) / BQ : __builtin_amdgcn_readfirstlane(count_tiles<BQ>(a, lane));
-  const int each = qt * nt, items = WHAT == GEMM_DW ? each * a.E : each;
-  const bool runs = WHAT != GEMM_DW || a.E == 1;
+  const int each = qt * nt, items = WHAT == GEMM_DW ? each * a.E * a.parts : each;
+  const bool runs = WHAT != GEMM_DW || a.E * a.parts == 1;
   const int run = (items + 7) >> 3, stride = runs ? (int)gridDim.x >> 3 : (int)gridDim.x;
   int item = runs ? (int)(blockIdx.x & 7) * run + (int)(blockIdx.x >> 3) : a.item0 + (int)blockIdx.x;
   const int last = runs ? min(items, ((int)(blockIdx.x & 7) + 1) * run) : items;
@@ -324,9 +325,11 @@ __global__ __launch_bounds__(WP * WQ * 64, DEPTH > 2 ? 1 : 2) void gemm_tiled_ke
     if constexpr (WHAT == GEMM_DW) {
       t.row0 = r * BQ;
       t.rows = min(BQ, a.N - t.row0);
-      const int2 of = a.offsets ? rows_of(a, t.e) : make_int2(0, a.M);
-      t.lo = __builtin_amdgcn_readfirstlane(of.x);
-      t.C = __builtin_amdgcn_readfirstlane(max(of.y - of.x, 0));
+      const int2 of = a.offsets ? rows_of(a, t.e % a.E) : make_int2(0, a.M);
+      const int all = __builtin_amdgcn_readfirstlane(max(of.y - of.x, 0)), part = ((all + 63) / 64 + a.parts - 1) / a.parts * 64;
+      const int before = t.e / a.E * part;         // whole stages
+      t.lo = __builtin_amdgcn_readfirstlane(of.x) + before;
+      t.C = max(min(part, all - before), 0);
     } else {
       const RowTile rt = find_tile<BQ>(a, r, lane);
       t.e = max(__builtin_amdgcn_readfirstlane(rt.e), 0);   // (offsets that changed meanwhile: no rows)
@@ -705,7 +708,7 @@ template <int WHAT, bool SWIGLU, int DEPTH, int WP, int WQ, int FP, int FQ>
 static void launch_tiled(GemmArgs a, hipStream_t stream) {
   constexpr int BQ = WQ * FQ * 16, BC = WP * FP * 16 / (WHAT == GEMM_FWD && SWIGLU ? 2 : 1);
   const int cols = WHAT == GEMM_FWD ? (SWIGLU ? a.N / 2 : a.N) : a.K;
-  const long long tiles = WHAT == GEMM_DW ? (long long)a.E * ((a.N + BQ - 1) / BQ) : most_tiles(a, BQ);
+  const long long tiles = WHAT == GEMM_DW ? (long long)a.E * a.parts * ((a.N + BQ - 1) / BQ) : most_tiles(a, BQ);
   // As many workgroups as run at a time, each walking over its tiles; gradients of
   // weights, tiles of unequal length, get a workgroup each.
   constexpr bool WALK = WHAT != GEMM_DW;
@@ -789,13 +792,11 @@ static moesq_status_t launch_gemm(const GemmArgs &a, hipStream_t stream, const c
   GemmShape g;
   g.cus = device_cu_count();
   g.n = WHAT == GEMM_FWD ? a.N : a.K;
-  g.experts = WHAT == GEMM_DW ? a.E : std::min(a.E, a.M);
-  const int mean = (a.M + std::max(g.experts, 1) - 1) / std::max(g.experts, 1);
-  g.rows = WHAT == GEMM_DW ? a.N : mean;
-  g.stages = ((WHAT == GEMM_FWD ? a.K : WHAT == GEMM_DX ? a.N : mean) + 63) / 64;
-  // (few tiles, one on a CU, copy four stages ahead; not for weights' gradients of few rows, which would
-  // wait for all of them first)
-  const bool ahead = WHAT != GEMM_DW && g.tiles(128, 64) <= g.cus;
+  g.experts = std::min(a.E, a.M);
+  g.rows = (a.M + std::max(g.experts, 1) - 1) / std::max(g.experts, 1);
+  g.stages = ((WHAT == GEMM_FWD ? a.K : a.N) + 63) / 64;
+  // (few tiles, one on a CU, copy four stages ahead)
+  const bool ahead = g.tiles(128, 64) <= g.cus;
   const float large = tile_time(g, 256, 256, 1, 1.5f, 1.5f), mid = tile_time(g, 128, 128, 2, 0.5f, 0.9f),
               small = tile_time(g, 128, 64, 2, ahead ? 0.29f : 0.4f, 0.65f);
   if constexpr (WHAT == GEMM_FWD) {
@@ -807,9 +808,68 @@ static moesq_status_t launch_gemm(const GemmArgs &a, hipStream_t stream, const c
   }
   if (large <= mid && large <= small) return launch_tiled<WHAT, SWIGLU, 2, 2, 4, 8, 4>(a, stream), launch_status(who);
   if (mid <= small) return launch_tiled<WHAT, SWIGLU, 2, 2, 2, 4, 4>(a, stream), launch_status(who);
-  if constexpr (WHAT != GEMM_DW)
-    if (ahead) return launch_tiled<WHAT, SWIGLU, 4, 2, 2, 4, 2>(a, stream), launch_status(who);
+  if (ahead) return launch_tiled<WHAT, SWIGLU, 4, 2, 2, 4, 2>(a, stream), launch_status(who);
   launch_tiled<WHAT, SWIGLU, 2, 2, 2, 4, 2>(a, stream);
+  return launch_status(who);
+}
+
+// Weights' gradients of few tiles and many rows: the rows in parts, over workgroups, whose
+// sums are then added in order.  By sizes alone, as the workspace's size follows from it.
+// (Four stages ahead would wait for all of them first where rows are few.)
+struct DwPlan {
+  int tile, parts;             // 256 x 256, 128 x 128, 128 x 64
+};
+
+constexpr int DW_CUS = 256;                        // of an MI355X
+
+static DwPlan dw_plan(int M, int E, int N, int K, bool split) {
+  GemmShape g{E, N, K, 0, DW_CUS};
+  const int stages = (int)(((long long)M + E - 1) / E + 63) / 64;
+  DwPlan best{0, 1};
+  float least = 0;
+  for (int tile = 0; tile < 3; ++tile) {
+    const int bp = tile == 0 ? 256 : 128, bq = tile == 0 ? 256 : tile == 1 ? 128 : 64;
+    const long long tiles = g.tiles(bp, bq);
+    for (int parts = 1; parts <= (split ? 32 : 1) && (parts == 1 || (tiles * parts <= DW_CUS && parts * 2 <= stages)); ++parts) {
+      g.stages = (stages + parts - 1) / parts;
+      float time = tile == 0 ? tile_time(g, 256, 256, 1, 1.5f, 1.5f)
+                             : tile == 1 ? tile_time(g, 128, 128, 2, 0.5f, 0.9f) : tile_time(g, 128, 64, 2, 0.4f, 0.65f);
+      // (the other launch, and the parts' sums there and back)
+      if (parts > 1) time += 5 + (float)parts * E * N * K * 8 / 3e6f;
+      if ((tile == 0 && parts == 1) || time < least) best = {tile, parts}, least = time;
+    }
+  }
+  return best;
+}
+
+// dw = the parts' sums in order, and (accumulate) what was there.
+__global__ __launch_bounds__(256) void dw_join_kernel(const f32x4_t *__restrict__ sums, int parts, long long fours, bool out32,
+                                                      bool accumulate, void *dw) {
+  for (long long i = blockIdx.x * 256 + threadIdx.x; i < fours; i += gridDim.x * 256) {
+    f32x4_t v = sums[i];
+    for (int p = 1; p < parts; ++p) v += sums[p * fours + i];
+    if (out32) {
+      f32x4_t *o = static_cast<f32x4_t *>(dw) + i;
+      *o = accumulate ? *o + v : v;
+    } else {
+      static_cast<uint2 *>(dw)[i] = make_uint2(round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3]));
+    }
+  }
+}
+
+static moesq_status_t launch_dw(GemmArgs a, float *ws, hipStream_t stream, const char *who) {
+  const DwPlan plan = dw_plan(a.M, a.E, a.N, a.K, ws != nullptr);
+  const GemmArgs to = a;
+  a.parts = plan.parts;
+  if (plan.parts > 1) a.y = reinterpret_cast<uint16_t *>(ws), a.out32 = true, a.accumulate = false;
+  if (plan.tile == 0) launch_tiled<GEMM_DW, false, 2, 2, 4, 8, 4>(a, stream);
+  else if (plan.tile == 1) launch_tiled<GEMM_DW, false, 2, 2, 2, 4, 4>(a, stream);
+  else launch_tiled<GEMM_DW, false, 2, 2, 2, 4, 2>(a, stream);
+  if (plan.parts > 1) {
+    const long long fours = (long long)a.E * a.N * a.K / 4;
+    hipLaunchKernelGGL(dw_join_kernel, dim3((unsigned)std::min((fours + 255) / 256, 8ll * DW_CUS)), dim3(256), 0, stream,
+                       reinterpret_cast<const f32x4_t *>(ws), plan.parts, fours, to.out32, to.accumulate, to.y);
+  }
   return launch_status(who);
 }
 
@@ -906,10 +966,17 @@ extern "C" moesq_status_t moesq_gemm_dx(const uint16_t *dy, const int32_t *exper
            : launch_gemm<GEMM_DX, false>(a, stream, "moesq_gemm_dx");
 }
 
+extern "C" size_t moesq_gemm_dw_workspace_bytes(int32_t M, int32_t E, int32_t N, int32_t K) {
+  const int32_t some = 0;                          // (stands for offsets: those are the call's)
+  if (check_sizes("moesq_gemm_dw_workspace_bytes", &some, M, E, N, K)) return 0;
+  const int parts = dw_plan(M, E, N, K, true).parts;
+  return parts > 1 ? (size_t)parts * E * N * K * 4 : 0;
+}
+
 extern "C" moesq_status_t moesq_gemm_dw(const uint16_t *dy, const uint16_t *x, const int32_t *perm, int32_t T,
                                         int32_t k, const int32_t *expert_offsets, int32_t M, int32_t E, int32_t N,
-                                        int32_t K, int32_t dtype, int32_t accumulate, void *dw,
-                                        hipStream_t stream) {
+                                        int32_t K, int32_t dtype, int32_t accumulate, void *dw, void *ws,
+                                        size_t ws_bytes, hipStream_t stream) {
   const std::string who("moesq_gemm_dw");
   clear_error();
   if (dtype != MOESQ_F32 && dtype != MOESQ_BF16) return fail(MOESQ_ERR_ARG, who + ": dtype must be fp32 or bf16");
@@ -918,11 +985,13 @@ extern "C" moesq_status_t moesq_gemm_dw(const uint16_t *dy, const uint16_t *x, c
   if (moesq_status_t st = check_sizes(who, expert_offsets, M, E, N, K)) return st;
   if (moesq_status_t st = check_gather(who, perm, T, k, expert_offsets, M, K)) return st;
   if (!dw || (M && (!dy || !x))) return fail(MOESQ_ERR_NULL, who + ": NULL dy, x or dw");
-  if (misaligned(dy, x, dw)) return fail(MOESQ_ERR_ARG, who + ": dy, x and dw must be 16-byte aligned");
+  if (misaligned(dy, x, dw, ws)) return fail(MOESQ_ERR_ARG, who + ": dy, x, dw and the workspace must be 16-byte aligned");
+  if (ws && ws_bytes < moesq_gemm_dw_workspace_bytes(M, E, N, K))
+    return fail(MOESQ_ERR_WORKSPACE, who + ": workspace too small");
   GemmArgs a{};
   a.dy = dy, a.x = x, a.perm = perm, a.offsets = expert_offsets, a.y = static_cast<uint16_t *>(dw);
   a.M = M, a.E = E, a.N = N, a.K = K;
   set_division(a, k);
   a.out32 = dtype == MOESQ_F32, a.accumulate = accumulate != 0;
-  return launch_gemm<GEMM_DW, false>(a, stream, "moesq_gemm_dw");
+  return launch_dw(a, static_cast<float *>(ws), stream, "moesq_gemm_dw");
 }

@@ -110,7 +110,8 @@ _mx_gemm = _sig("moesq_mx_gemm", _i32, ctypes.POINTER(MxDesc), _vp, _i32, _i32, 
 _gemm = _sig("moesq_gemm", _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp)
 _gemm_dx = _sig("moesq_gemm_dx", _i32, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _vp, _vp)
 _gemm_dw = _sig("moesq_gemm_dw", _i32, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp,
-                _vp)
+                _vp, _sz, _vp)
+_gemm_dw_ws = _sig("moesq_gemm_dw_workspace_bytes", _sz, _i32, _i32, _i32, _i32)
 _unpermute_bw = _sig("moesq_unpermute_backward", _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp)
 _lora = _sig("moesq_lora", _i32, _vp, _vp, _i32, ctypes.POINTER(LoraDesc), _vp, _i32, _vp, _vp, _sz, _vp)
 _lora_ws = _sig("moesq_lora_workspace_bytes", _sz, _i32, ctypes.POINTER(LoraDesc))
@@ -126,7 +127,8 @@ EXPORTED = ["moesq_route", "moesq_route_workspace_bytes", "moesq_route_noalloc",
             "moesq_pack_weights", "moesq_pack_weights_paired", "moesq_tile_weights",
             "moesq_decode_weights",
             "moesq_gate_topk", "moesq_mx_quantize", "moesq_mx_decode", "moesq_rmsnorm",
-            "moesq_mx_gemm", "moesq_gemm", "moesq_gemm_dx", "moesq_gemm_dw", "moesq_unpermute_backward",
+            "moesq_mx_gemm", "moesq_gemm", "moesq_gemm_dx", "moesq_gemm_dw",
+            "moesq_gemm_dw_workspace_bytes", "moesq_unpermute_backward",
             "moesq_lora", "moesq_lora_workspace_bytes",
             "moesq_validate", "moesq_stream_read", "moesq_status_string",
             "moesq_last_error", "moesq_version"]
@@ -688,16 +690,23 @@ def moesq_gemm_dx(dy, expert_offsets, M: int, w, E: int, N: int, K: int, z, dx, 
     _launch(dev, stream, _gemm_dx, d, off, M, wp, E, N, K, zp, o)
 
 
+def moesq_gemm_dw_workspace_bytes(M: int, E: int, N: int, K: int) -> int:
+    _counts(M=M, E=E, N=N, K=K)
+    return int(_gemm_dw_ws(M, E, N, K))
+
+
 def moesq_gemm_dw(dy, x, perm, T: int, k: int, expert_offsets, M: int, E: int, N: int, K: int, dw,
-                  accumulate: bool = False, stream=None):
+                  accumulate: bool = False, ws=None, stream=None):
     """The type of dw (float32 or bfloat16) is the call's dtype."""
     dtype = _dtype(dw, "dw")
     _counts(T=T, k=k, M=M, E=E, N=N, K=K)
     bf, i32 = torch.bfloat16, torch.int32
-    dev, (d, xp, p, off, o) = _pointers(
+    dev, (d, xp, p, off, o, w) = _pointers(
         (dy, bf, M * N, "dy"), (x, bf, (T if perm is not None else M) * K, "x"), (perm, i32, M, "perm"),
-        (expert_offsets, i32, E + 1, "expert_offsets"), (dw, dw.dtype, E * N * K, "dw"))
-    _launch(dev, stream, _gemm_dw, d, xp, p, T, k, off, M, E, N, K, dtype, int(bool(accumulate)), o)
+        (expert_offsets, i32, E + 1, "expert_offsets"), (dw, dw.dtype, E * N * K, "dw"),
+        (ws, torch.uint8, 0 if ws is None else ws.numel(), "ws"))
+    _launch(dev, stream, _gemm_dw, d, xp, p, T, k, off, M, E, N, K, dtype, int(bool(accumulate)), o, w,
+            0 if ws is None else ws.numel())
 
 
 def moesq_unpermute_backward(dout, y, inv_perm, topk_weights, T: int, k: int, N: int, dy, dw, stream=None):
@@ -1053,7 +1062,9 @@ def gemm_dw(dy, x, expert_offsets=None, E: int = 1, perm=None, k: int = 1, out=N
         out = torch.empty(E, N, K, dtype=dtype, device=dy.device)
     elif tuple(out.shape) != (E, N, K) and (E > 1 or tuple(out.shape) != (N, K)):
         raise ValueError(f"out must be {[E, N, K]}, got {tuple(out.shape)}")
-    moesq_gemm_dw(dy, x, perm, T if perm is not None else 0, k, expert_offsets, M, E, N, K, out, accumulate)
+    size = moesq_gemm_dw_workspace_bytes(M, E, N, K)
+    ws = torch.empty(size, dtype=torch.uint8, device=dy.device) if size else None
+    moesq_gemm_dw(dy, x, perm, T if perm is not None else 0, k, expert_offsets, M, E, N, K, out, accumulate, ws)
     return out
 
 

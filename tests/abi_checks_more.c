@@ -60,7 +60,7 @@ int main(void) {
   do {                                                                                                         \
     GEMM(what, want, x, NULL, 0, 0, off, M, w, E, N, K, 0, y, NULL);                                           \
     expect("gemm_dx " what, moesq_gemm_dx(x, off, M, w, E, N, K, NULL, y, NULL), want);                        \
-    expect("gemm_dw " what, moesq_gemm_dw(x, w, NULL, 0, 0, off, M, E, N, K, MOESQ_F32, 0, fp, NULL), want);   \
+    expect("gemm_dw " what, moesq_gemm_dw(x, w, NULL, 0, 0, off, M, E, N, K, MOESQ_F32, 0, fp, NULL, 0, NULL), want); \
   } while (0)
   SIZES("E=0", MOESQ_ERR_SHAPE, ip, 4, 0, 64, 64);
   SIZES("E lowest", MOESQ_ERR_SHAPE, ip, 4, low, 64, 64);
@@ -86,7 +86,7 @@ int main(void) {
   expect("gemm_dx NULL dx", moesq_gemm_dx(x, NULL, 4, w, 1, 64, 64, NULL, NULL, NULL), MOESQ_ERR_NULL);
   expect("gemm_dx z misaligned", moesq_gemm_dx(x, NULL, 4, w, 1, 64, 64, odd, y, NULL), MOESQ_ERR_ARG);
 #define DW(what, want, dy, x, perm, T, k, off, M, E, dtype, acc, dw) \
-  expect("gemm_dw " what, moesq_gemm_dw(dy, x, perm, T, k, off, M, E, 64, 64, dtype, acc, dw, NULL), want)
+  expect("gemm_dw " what, moesq_gemm_dw(dy, x, perm, T, k, off, M, E, 64, 64, dtype, acc, dw, NULL, 0, NULL), want)
   DW("dtype", MOESQ_ERR_ARG, x, w, NULL, 0, 0, NULL, 4, 1, top, 0, fp);
   DW("dtype lowest", MOESQ_ERR_ARG, x, w, NULL, 0, 0, NULL, 4, 1, low, 0, fp);
   DW("accumulate", MOESQ_ERR_ARG, x, w, NULL, 0, 0, NULL, 4, 1, MOESQ_F32, 2, fp);
@@ -97,6 +97,15 @@ int main(void) {
   DW("NULL dw", MOESQ_ERR_NULL, x, w, NULL, 0, 0, NULL, 0, 1, MOESQ_F32, 0, NULL);
   DW("NULL dy", MOESQ_ERR_NULL, NULL, w, NULL, 0, 0, NULL, 4, 1, MOESQ_F32, 0, fp);
   DW("dw misaligned", MOESQ_ERR_ARG, x, w, NULL, 0, 0, NULL, 4, 1, MOESQ_F32, 0, odd);
+
+  expect("gemm_dw workspace misaligned",
+         moesq_gemm_dw(x, w, NULL, 0, 0, NULL, 8192, 1, 64, 64, MOESQ_F32, 0, fp, P(0x104), 1 << 30, NULL), MOESQ_ERR_ARG);
+  expect("gemm_dw workspace too small",
+         moesq_gemm_dw(x, w, NULL, 0, 0, NULL, 8192, 1, 64, 64, MOESQ_F32, 0, fp, P(0x100), 16, NULL), MOESQ_ERR_WORKSPACE);
+  if (!moesq_gemm_dw_workspace_bytes(8192, 1, 64, 64) || moesq_gemm_dw_workspace_bytes(8192, 1, 64, 60) ||
+      moesq_gemm_dw_workspace_bytes(low, 1, 64, 64) || moesq_gemm_dw_workspace_bytes(0, 1, 64, 64) ||
+      moesq_gemm_dw_workspace_bytes(1 << 30, MOESQ_MAX_EXPERTS, 8, most))
+    printf("FAIL gemm_dw workspace sizes\n"), ++failures;
 
   /* the combine's gradient */
 #define COMBINE(what, want, d, y, inv, w, T, k, N, dy, dw) \

@@ -453,6 +453,44 @@ def test_adapters_in_training(lib):
             assert np.linalg.norm(f64(got) - ref) <= 1e-2 * np.linalg.norm(ref)
 
 
+@pytest.mark.parametrize("counts, k, N, K", [
+    (None, 0, 8, 8), (None, 0, 80, 3000), (None, 0, 136, 264), ([5000, 0, 17], 0, 72, 200), ([0, 9, 4000, 64], 4, 104, 328),
+    ([2100, 2148], 3, 16, 1000)])
+@pytest.mark.parametrize("dtype, add", [(torch.bfloat16, False), (torch.float32, False), (torch.float32, True)])
+def test_weight_gradient_in_parts(lib, counts, k, N, K, dtype, add):
+    """Few matrices of many rows: with a workspace the rows are summed in parts."""
+    rng = np.random.default_rng(N + K)
+    M = 4163 if counts is None else sum(counts)
+    E, off, perm, kk = 1 if counts is None else len(counts), None, None, max(k, 1)
+    if counts is not None:
+        M = M // kk * kk
+        counts = counts[:-1] + [counts[-1] - (sum(counts) - M)]
+        off, p, _ = plan(rng, counts, k)
+        perm = p if k else None
+    x, dy = rand(rng, M // kk, K), rand(rng, M, N, scale=0.1)
+    held = rand(rng, E, N, K).to(dtype)
+    size = lib.moesq_gemm_dw_workspace_bytes(M, E, N, K)
+    assert size % (E * N * K * 4) == 0 and (size > 0 or E > 1)             # (few rows an expert: one part)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")      # (NaN)
+    got, one = held.clone(), held.clone()
+    lib.moesq_gemm_dw(dy, x, perm, M // kk if k else 0, kk, off, M, E, N, K, got, add, ws)
+    lib.moesq_gemm_dw(dy, x, perm, M // kk if k else 0, kk, off, M, E, N, K, one, add)
+    assert torch.equal(lib.gemm_dw(dy, x, off, E=E, perm=perm, k=kk, out=held.clone(), accumulate=add), got)
+    offs = [0, M] if counts is None else off.cpu().numpy()
+    src = np.arange(M) if perm is None else perm.cpu().numpy() // kk
+    for e in range(E):
+        r = np.arange(offs[e], offs[e + 1])
+        d, xe = f64(dy)[r], f64(x)[src[r]]
+        ref, tol = d.T @ xe, acc(d.T, xe)
+        if add:
+            ref = ref + f64(held[e])
+            tol = tol + 2.0 ** -23 * (np.abs(ref) + tol)
+        if dtype == torch.bfloat16:
+            tol = bf16_tol(ref, tol)
+        within(f64(got[e]), ref, tol, ("parts", e))
+        within(f64(one[e]), ref, tol, ("one", e))
+
+
 def test_far_rows(lib):
     """The last rows of buffers over 4 GiB are what a call on them alone gives."""
     g = torch.Generator(device="cuda").manual_seed(3)

@@ -108,7 +108,7 @@ def test_gemm_dx_rejects(m):
 
 def test_gemm_dw_rejects(m):
     def call(dy=0x10, x=0x10, perm=None, T=0, k=1, off=0x10, M=4, E=8, N=64, K=64, dtype=1, add=0, dw=0x10):
-        return m._gemm_dw(dy, x, perm, T, k, off, M, E, N, K, dtype, add, dw, None)
+        return m._gemm_dw(dy, x, perm, T, k, off, M, E, N, K, dtype, add, dw, None, 0, None)
 
     assert call(dtype=2) == m.ERR_ARG and call(dtype=-1) == m.ERR_ARG
     assert call(add=2) == m.ERR_ARG and call(add=1) == m.ERR_ARG          # bf16 is not added to
