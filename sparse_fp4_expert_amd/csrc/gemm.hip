@@ -751,8 +751,9 @@ static float tile_time(const GemmShape &g, int bp, int bq, int per_cu, float fir
   return g.stages * (tiles <= g.cus ? first : (float)((tiles + slots - 1) / slots) * round);
 }
 
-// Streaming: a CU copies 100 KB/us to LDS, and a wave's ring takes 0.9 us from its
-// copies to their use.  Measured, us (in brackets the tiled kernel's best):
+// Streaming: a CU copies 100 KB/us to LDS, a wave's ring takes 0.9 us from its copies to
+// their use, and a workgroup behind another 2.5 us until its first ones have landed (32600 rows
+// of 128 x 736 on 13 experts: 49 us so, tiled 21).  Measured, us (in brackets the tiled kernel's best):
 //   KSPLIT/FN/FM/DEPTH  4/1/1/4 4/2/1/2 2/2/1/2 4/1/2/4 4/2/2/2 2/2/2/2 4/2/4/2 4/4/4/2 2/4/4/2
 //     16 x 4096 x 7168     13.7    15.6    25.0    14.4    18.3    29.2    20.8              (89)
 //     64 x 4096 x 7168     32.0    18.9    18.6    22.7    14.2    21.6    18.6    24.1  41.8 (61)
@@ -765,10 +766,10 @@ static float tile_time(const GemmShape &g, int bp, int bq, int per_cu, float fir
 template <bool SWIGLU, int KSPLIT, int FN, int FM, int DEPTH>
 struct Stream {
   static float time(const GemmShape &g) {
-    constexpr int RG = STREAM_WAVES / KSPLIT;
-    const long long groups = g.tiles(RG * FN * 16, FM * 16);
-    const float copies = (float)((groups + g.cus - 1) / g.cus) * g.stages * RG * (FN + FM) * 2 / 100;
-    return std::max(copies, (float)((g.stages + KSPLIT - 1) / KSPLIT) * 0.9f / DEPTH);
+    constexpr int RG = STREAM_WAVES / KSPLIT, AT_A_TIME = 160 / (STREAM_WAVES * DEPTH * (FN + FM) * 2);   // on a CU, by LDS
+    const long long groups = g.tiles(RG * FN * 16, FM * 16), each = (groups + g.cus - 1) / g.cus;
+    const float copies = (float)each * g.stages * RG * (FN + FM) * 2 / 100;
+    return std::max(copies, (float)((g.stages + KSPLIT - 1) / KSPLIT) * 0.9f / DEPTH) + (float)((each - 1) / AT_A_TIME) * 2.5f;
   }
   static void launch(const GemmArgs &a, hipStream_t stream) { launch_stream<SWIGLU, KSPLIT, FN, FM, DEPTH>(a, stream); }
 };
@@ -815,7 +816,9 @@ static moesq_status_t launch_gemm(const GemmArgs &a, hipStream_t stream, const c
 
 // Weights' gradients of few tiles and many rows: the rows in parts, over workgroups, whose
 // sums are then added in order.  By sizes alone, as the workspace's size follows from it.
-// (Four stages ahead would wait for all of them first where rows are few.)
+// (Four stages ahead would wait for all of them first where rows are few.)  Measured, us, in
+// one part and in several: 8192 rows, 128 x 7168 76 and 35; 4136 rows, 80 x 3008 34 and 17; 16384
+// rows, 64 x 4096 149 and 31; 6116 rows, 928 x 1240 64 and 36; 2000 rows, 512 x 512 13 and 11.
 struct DwPlan {
   int tile, parts;             // 256 x 256, 128 x 128, 128 x 64
 };
@@ -842,7 +845,8 @@ static DwPlan dw_plan(int M, int E, int N, int K, bool split) {
   return best;
 }
 
-// dw = the parts' sums in order, and (accumulate) what was there.
+// dw = the parts' sums in order, and (accumulate) what was there.  Bound by the launch (3 x 928 x
+// 1240: 14 MB from the caches in 5 us).
 __global__ __launch_bounds__(256) void dw_join_kernel(const f32x4_t *__restrict__ sums, int parts, long long fours, bool out32,
                                                       bool accumulate, void *dw) {
   for (long long i = blockIdx.x * 256 + threadIdx.x; i < fours; i += gridDim.x * 256) {
