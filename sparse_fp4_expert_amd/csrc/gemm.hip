@@ -62,7 +62,7 @@ __device__ __forceinline__ void for_each(F &&f) {
 // eight columns.
 //
 // Measured: one row of a SwiGLU of 1536 x 2048 4.2 us (a launch and the latency of
-// its stages), 16 rows of 4096 x 7168 13.7 us (4.3 TB/s), 16 tokens' 8 choices of
+// its stages), 16 rows of 4096 x 7168 11.5 us (5.1 TB/s, partly from the last level's cache), 16 tokens' 8 choices of
 // 128 experts of 1536 x 2048 49 us (327 MB of the experts used, 6.7 TB/s).
 constexpr int STREAM_WAVES = 4;
 
@@ -753,16 +753,19 @@ static float tile_time(const GemmShape &g, int bp, int bq, int per_cu, float fir
 
 // Streaming: a CU copies 100 KB/us to LDS, a wave's ring takes 0.9 us from its copies to
 // their use, and a workgroup behind another 2.5 us until its first ones have landed (32600 rows
-// of 128 x 736 on 13 experts: 49 us so, tiled 21).  Measured, us (in brackets the tiled kernel's best):
-//   KSPLIT/FN/FM/DEPTH  4/1/1/4 4/2/1/2 2/2/1/2 4/1/2/4 4/2/2/2 2/2/2/2 4/2/4/2 4/4/4/2 2/4/4/2
-//     16 x 4096 x 7168     13.7    15.6    25.0    14.4    18.3    29.2    20.8              (89)
-//     64 x 4096 x 7168     32.0    18.9    18.6    22.7    14.2    21.6    18.6    24.1  41.8 (61)
-//    200 x 4096 x 7168    101.9    60.7    57.5    72.0    42.9    36.8    34.4    22.9  37.5 (59)
-//    400 x 4096 x 7168     195     112      99.7   132      73.6    72.3    63.6    44.9  39.0 (62)
-//    777 x 1536 x 2048     35.9    24.6    21.7    36.2    18.7    18.0    19.2    18.4  15.7 (20)
+// of 128 x 736 on 13 experts: 49 us so, tiled 21).  Measured, us, one behind the other in a graph (in
+// brackets the tiled kernel, with the tile that the times above give it):
+//   KSPLIT/FN/FM/DEPTH  4/1/1/4 4/2/1/2 2/2/1/2 4/1/2/4 4/2/2/2 2/2/2/2 4/2/4/2 4/4/4/2
+//     16 x 4096 x 7168     11.4    11.6    17.6    11.9    12.3    18.9    14.0    18.9 (32)
+//     64 x 4096 x 7168     32.2    18.4    17.6    22.2    13.9    20.9    18.2    23.3 (35)
+//    200 x 4096 x 7168    102      60.0    57.5    70.6    42.3    36.3    33.9    22.4 (36)
+//    400 x 4096 x 7168    194     111      98.1   130      72.9    71.8    61.9    42.9 (37)
+//    777 x 1536 x 2048     34.5    23.1    20.4    34.8    17.9    17.3    18.5    17.3 (14)
 //   128 experts of 1536 x 2048, 8 choices of 16 tokens (52 of them used, 327 MB)
-//                          89.4    59.2    53.1   149      69.4    57.7   108      79.6  72.0 (75)
-//   the same, 512 tokens  362     220     194     440     205     171     262     191   175   (160)
+//                          79.2    50.7    49.5   122      57.8    51.8    85.7    64.5 (66)
+//   the same, 512 tokens  327     205     195     380     185     165     224     172   (140)
+// (2/4/4/2 was chosen for one in two thousand random sizes, and there as fast as what is chosen
+// without it: 8229 rows of 352 x 2512 on 214 experts 110 us for 112, 790 of 3888 x 7312 on 21 307 for 286.)
 template <bool SWIGLU, int KSPLIT, int FN, int FM, int DEPTH>
 struct Stream {
   static float time(const GemmShape &g) {
@@ -803,8 +806,8 @@ static moesq_status_t launch_gemm(const GemmArgs &a, hipStream_t stream, const c
   if constexpr (WHAT == GEMM_FWD) {
     // (of equals the first)
     using Choice = Streams<Stream<SWIGLU, 2, 2, 1, 2>, Stream<SWIGLU, 4, 2, 1, 2>, Stream<SWIGLU, 4, 1, 1, 4>, Stream<SWIGLU, 2, 2, 2, 2>,
-                           Stream<SWIGLU, 4, 2, 2, 2>, Stream<SWIGLU, 4, 1, 2, 4>, Stream<SWIGLU, 2, 4, 4, 2>,
-                           Stream<SWIGLU, 4, 2, 4, 2>, Stream<SWIGLU, 4, 4, 4, 2>>;
+                           Stream<SWIGLU, 4, 2, 2, 2>, Stream<SWIGLU, 4, 1, 2, 4>, Stream<SWIGLU, 4, 2, 4, 2>,
+                           Stream<SWIGLU, 4, 4, 4, 2>>;
     if (Choice::launch(g, a, stream, 0.9f * std::min(large, std::min(mid, small)))) return launch_status(who);
   }
   if (large <= mid && large <= small) return launch_tiled<WHAT, SWIGLU, 2, 2, 4, 8, 4>(a, stream), launch_status(who);
