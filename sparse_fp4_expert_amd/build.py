@@ -116,5 +116,33 @@ def build_host_checker(out_dir: str, verbose: bool = False, program: str = "abi_
     return exe
 
 
+def build_launch_recorder(out_dir: str, sources: tuple) -> str:
+    """Builds the host code of `sources` (of csrc/) with tests/launch_recorder.cpp, which
+    stands in for the HIP runtime and writes down the kernels that a call
+    launches, into out_dir/launch_recorder; returns its path.  Neither device code nor
+    the runtime is linked."""
+    os.makedirs(out_dir, exist_ok=True)
+    srcs = [p for p in _sources() if os.path.basename(p) in sources]
+    srcs.append(os.path.join(ROOT, "tests", "launch_recorder.cpp"))
+
+    def one(src):
+        obj = os.path.join(out_dir, os.path.basename(src) + ".host.o")
+        r = subprocess.run([HIPCC, "-x", "hip", "--cuda-host-only", "-O1", "-std=c++17", f"-I{INCLUDE}", f"-I{CSRC}",
+                            "-c", src, "-o", obj], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"host build failed for {src}:\n{r.stderr}")
+        return obj
+
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        objs = list(ex.map(one, srcs))
+    exe = os.path.join(out_dir, "launch_recorder")
+    clang = os.path.join(os.path.dirname(HIPCC), "..", "llvm", "bin", "clang++")
+    # (what stays undefined is the device code that is not there)
+    r = subprocess.run([clang, "-o", exe, *objs, "-Wl,--unresolved-symbols=ignore-all"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr}")
+    return exe
+
+
 if __name__ == "__main__":
     build()
