@@ -586,8 +586,8 @@ size_t moesq_gemm_dw_workspace_bytes(int32_t M, int32_t E, int32_t N, int32_t K)
  *   epilogue SWIGLU: with p = base + d: y[t][c] = bf16_rne(silu(p[t][c]) * p[t][c+N/2]),
  *                    y is [T][N/2]
  * id = ids[t]; a row with ids[t] outside [0, adapters) has no adapter (d = 0).
- * Sums are kept in fp32; v enters the second product as two bf16 numbers whose
- * sum is within 2^-17 of it.
+ * Sums are kept in fp32; v enters the second product as two bf16 numbers of its
+ * sign whose sum is within 2^-16 of it (from |v| = 2^-100 on).
  *   a [adapters][slices*rank][K], b [adapters][N][rank] bf16, scale [adapters]
  *   fp32: slices > 1 are projections that share one base, such as gate and up,
  *   each with adapters of its own.  An adapter of a lower rank has zeros behind it.

@@ -201,7 +201,7 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs l) {
 //
 // A workgroup takes 16 FM rows, a wave `chunk` columns of one slice (with SwiGLU, of
 // one slice of each half).  v is the second operand of the MFMA, as two bf16 numbers
-// whose sum is within 2^-17 of the fp32 sum: the workgroup adds up the splits' sums of its rows
+// whose sum is within 2^-16 of the fp32 sum: the workgroup adds up the splits' sums of its rows
 // and keeps them so in LDS.  Two fragments of 16 columns are interleaved by fours, so that a
 // lane's results are eight neighbouring columns.  Instructions and latency bound it as much as memory
 // does: without base and y it takes 25 us of the 46 (8192 rows).  Loading the next columns ahead of
@@ -250,9 +250,13 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs l) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float x0 = sum[i / 2][2 * (i & 1)], x1 = sum[i / 2][2 * (i & 1) + 1];
-      // (what is larger than the largest finite bf16, infinite or not, is left to the rest)
-      hi[i] = round_bf16x2(__builtin_amdgcn_fmed3f(x0, -BF16_MAX, BF16_MAX), __builtin_amdgcn_fmed3f(x1, -BF16_MAX, BF16_MAX));
-      lo[i] = round_bf16x2(x0 - bf16_lo(hi[i]), x1 - bf16_hi(hi[i]));
+      // Cut off and not rounded, and 2^-24 of it added to the rest: both parts of a sum have its sign
+      // and neither is zero, so that an infinite element of b makes an infinite product of each.
+      // (What is larger than the largest finite bf16, infinite or not, is left to the rest.)
+      hi[i] = __builtin_amdgcn_perm(__float_as_uint(__builtin_amdgcn_fmed3f(x1, -BF16_MAX, BF16_MAX)),
+                                    __float_as_uint(__builtin_amdgcn_fmed3f(x0, -BF16_MAX, BF16_MAX)), 0x07060302u);
+      const float h0 = bf16_lo(hi[i]), h1 = bf16_hi(hi[i]);
+      lo[i] = round_bf16x2(fmaf(h0, 0x1p-24f, x0 - h0), fmaf(h1, 0x1p-24f, x1 - h1));
     }
     *reinterpret_cast<uint4 *>(&sums[h][0][row][p]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4 *>(&sums[h][1][row][p]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
