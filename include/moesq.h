@@ -544,7 +544,7 @@ moesq_status_t moesq_gemm(const uint16_t *x, const int32_t *perm, int32_t T, int
  *              g = z[r][c], u = z[r][c+K], s = sigmoid(g):
  *                dx[r][c]   = bf16_rne(d[r][c] * u * s * (1 + g * (1 - s)))
  *                dx[r][c+K] = bf16_rne(d[r][c] * g * s)
- *              dx may be z's own buffer.
+ *              dx may be z's own buffer; it overlaps no other input.
  *   dy [M][N] routed rows; w [E][N][K]; expert_offsets as moesq_mx_gemm.
  * Rows of dx outside every expert range are not written.  All buffers 16-byte
  * aligned.  Limits: as moesq_gemm without a gather.
@@ -567,7 +567,8 @@ moesq_status_t moesq_gemm_dx(const uint16_t *dy, const int32_t *expert_offsets, 
  *   written and read by this call alone, with which few matrices of many rows
  *   are summed in parts.  (Its size may be 0; results with and without it differ
  *   by the order of their sums.)
- * All buffers 16-byte aligned.  Limits: as moesq_gemm.
+ * All buffers 16-byte aligned; dw and the workspace overlap no input and not each
+ * other.  Limits: as moesq_gemm.
  * Results are bit-identical on every run.
  */
 moesq_status_t moesq_gemm_dw(const uint16_t *dy, const uint16_t *x, const int32_t *perm, int32_t T,
@@ -592,9 +593,9 @@ size_t moesq_gemm_dw_workspace_bytes(int32_t M, int32_t E, int32_t N, int32_t K)
  *   fp32: slices > 1 are projections that share one base, such as gate and up,
  *   each with adapters of its own.  An adapter of a lower rank has zeros behind it.
  *   x [T][K] bf16; ids [T] int32; base [T][N] bf16 or NULL (zeros); y may be
- *   base's own buffer with epilogue NONE.
+ *   base's own buffer with epilogue NONE, else it overlaps none of base.
  *   ws, ws_bytes: workspace of moesq_lora_workspace_bytes() bytes, 16-byte
- *   aligned, written and read by this call alone.
+ *   aligned, written and read by this call alone, beside all other buffers.
  * The struct is a host object; its pointers are device pointers.  x, a, b, base
  * and y 16-byte aligned.
  * Limits: K % 8 == 0, rank % 8 == 0, rank <= MOESQ_LORA_MAX_RANK, 1 <= slices <=
@@ -638,7 +639,8 @@ moesq_status_t moesq_unpermute(const uint16_t *y, const int32_t *inv_perm,
  *   dw[i] = sum_n dout[i/k][n] * y[inv_perm[i]][n], fp32     (NULL: not wanted)
  *   dout [T][N], y [T*k][N] (needed for dw, else may be NULL) bf16, inv_perm
  *   [T*k] int32, topk_weights [T*k] fp32 (needed for dy, else may be NULL);
- *   dy [T*k][N] bf16, may be y's own buffer; dw [T*k] fp32.
+ *   dy [T*k][N] bf16, may be y's own buffer; dw [T*k] fp32; else they overlap no
+ *   input and not each other.
  * Entries of inv_perm outside [0, T*k) get dw 0; rows of dy that no entry names
  * are not written.  inv_perm names a row at most once.  dout, y and dy 16-byte
  * aligned.  Limits: N % 8 == 0, N > 0, T >= 0, k >= 1, T*k < 2^31.

@@ -24,6 +24,10 @@ int device_cu_count();
 constexpr int MAX_LAUNCH_THREADS = 1 << 30;
 // Clears the thread's last-error detail (start of every entry point).
 void clear_error();
+// Whether `n` bytes from p on and `m` from q on have some in common (no bytes at NULL).
+inline bool overlap(const void *p, size_t n, const void *q, size_t m) {
+  return p && q && (uintptr_t)p < (uintptr_t)q + m && (uintptr_t)q < (uintptr_t)p + n;
+}
 
 // ------------------------------------------------------------------ device side
 

@@ -239,7 +239,11 @@ extern "C" moesq_status_t moesq_unpermute_backward(const uint16_t *dout, const u
   if (dw && !y) return fail(MOESQ_ERR_NULL, who + ": dw needs y");
   if (((uintptr_t)dout | (uintptr_t)y | (uintptr_t)dy) & 15)
     return fail(MOESQ_ERR_ARG, who + ": dout, y and dy must be 16-byte aligned");
-  if (dy == dout) return fail(MOESQ_ERR_ARG, who + ": dy may not be dout's buffer");
+  const size_t nout = (size_t)T * N * 2, ny = (size_t)M * N * 2, nw = (size_t)M * 4;
+  if (overlap(dy, ny, dout, nout) || (dy != y && overlap(dy, ny, y, ny)) || overlap(dy, ny, inv_perm, nw) ||
+      overlap(dy, ny, topk_weights, nw) || overlap(dw, nw, dout, nout) || overlap(dw, nw, y, ny) || overlap(dw, nw, inv_perm, nw) ||
+      overlap(dw, nw, topk_weights, nw) || overlap(dw, nw, dy, ny))
+    return fail(MOESQ_ERR_ARG, who + ": dy and dw may overlap no input, but dy be y's own buffer, and not each other");
   hipLaunchKernelGGL(combine_grad_kernel, dim3(units_grid(M)), dim3(DISPATCH_THREADS), 0, stream,
                      (const uint4 *)dout, (const uint4 *)y, inv_perm, topk_weights, k, (int)M, N / 8,
                      (uint4 *)dy, dw);

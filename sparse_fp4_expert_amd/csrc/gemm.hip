@@ -950,6 +950,10 @@ extern "C" moesq_status_t moesq_gemm(const uint16_t *x, const int32_t *perm, int
   if (M == 0) return MOESQ_OK;
   if (!x || !w || !y) return fail(MOESQ_ERR_NULL, who + ": NULL x, w or y");
   if (misaligned(x, w, y, z)) return fail(MOESQ_ERR_ARG, who + ": x, w, y and z must be 16-byte aligned");
+  const size_t nx = (size_t)(perm ? T : M) * K * 2, nw = (size_t)E * N * K * 2, nz = (size_t)M * N * 2;
+  const size_t ny = epilogue == MOESQ_EPI_SWIGLU ? nz / 2 : nz;
+  if (overlap(y, ny, x, nx) || overlap(y, ny, w, nw) || overlap(y, ny, z, nz) || overlap(z, nz, x, nx) || overlap(z, nz, w, nw))
+    return fail(MOESQ_ERR_ARG, who + ": y and z may overlap no input and not each other");
   GemmArgs a{};
   a.x = x, a.w = w, a.perm = perm, a.offsets = expert_offsets, a.y = y, a.z = z;
   a.k = k, a.M = M, a.E = E, a.N = N, a.K = K, a.flat = flat;
@@ -966,6 +970,9 @@ extern "C" moesq_status_t moesq_gemm_dx(const uint16_t *dy, const int32_t *exper
   if (M == 0) return MOESQ_OK;
   if (!dy || !w || !dx) return fail(MOESQ_ERR_NULL, who + ": NULL dy, w or dx");
   if (misaligned(dy, w, z, dx)) return fail(MOESQ_ERR_ARG, who + ": dy, w, z and dx must be 16-byte aligned");
+  const size_t nx = (size_t)M * K * (z ? 4 : 2);
+  if (overlap(dx, nx, dy, (size_t)M * N * 2) || overlap(dx, nx, w, (size_t)E * N * K * 2) || (dx != z && overlap(dx, nx, z, nx)))
+    return fail(MOESQ_ERR_ARG, who + ": dx may overlap no input but be z's own buffer");
   GemmArgs a{};
   a.dy = dy, a.w = w, a.offsets = expert_offsets, a.y = dx, a.zin = z;
   a.k = 1, a.M = M, a.E = E, a.N = N, a.K = K;
@@ -995,6 +1002,10 @@ extern "C" moesq_status_t moesq_gemm_dw(const uint16_t *dy, const uint16_t *x, c
   if (misaligned(dy, x, dw, ws)) return fail(MOESQ_ERR_ARG, who + ": dy, x, dw and the workspace must be 16-byte aligned");
   if (ws && ws_bytes < moesq_gemm_dw_workspace_bytes(M, E, N, K))
     return fail(MOESQ_ERR_WORKSPACE, who + ": workspace too small");
+  const size_t ndy = (size_t)M * N * 2, nx = (size_t)(perm ? T : M) * K * 2, nw = (size_t)E * N * K * (dtype == MOESQ_F32 ? 4 : 2);
+  if (overlap(dw, nw, dy, ndy) || overlap(dw, nw, x, nx) || overlap(dw, nw, ws, ws_bytes) || overlap(ws, ws_bytes, dy, ndy) ||
+      overlap(ws, ws_bytes, x, nx))
+    return fail(MOESQ_ERR_ARG, who + ": dw and the workspace may overlap no input and not each other");
   GemmArgs a{};
   a.dy = dy, a.x = x, a.perm = perm, a.offsets = expert_offsets, a.y = static_cast<uint16_t *>(dw);
   a.M = M, a.E = E, a.N = N, a.K = K;

@@ -496,6 +496,10 @@ extern "C" moesq_status_t moesq_lora(const uint16_t *x, const int32_t *ids, int3
   if (swiglu && base == y) return fail(MOESQ_ERR_ARG, who + ": y may be base's buffer without an epilogue only");
   if (!ws || ws_bytes < moesq_lora_workspace_bytes(T, adapters))
     return fail(MOESQ_ERR_WORKSPACE, who + ": workspace missing or too small");
+  const size_t nb = (size_t)T * adapters->N * 2, ny = swiglu ? nb / 2 : nb;
+  if (base != y && overlap(y, ny, base, nb)) return fail(MOESQ_ERR_ARG, who + ": y may be base's own buffer, or overlap none of it");
+  if (overlap(ws, ws_bytes, x, (size_t)T * adapters->K * 2) || overlap(ws, ws_bytes, base, nb) || overlap(ws, ws_bytes, y, ny))
+    return fail(MOESQ_ERR_ARG, who + ": the workspace may overlap no other buffer");
   const LoraPlan p = lora_plan(*adapters, T);
   LoraArgs l{x, adapters->a, adapters->b, base, adapters->scale, ids, y, static_cast<float *>(ws),
              T, adapters->adapters, adapters->rank, adapters->slices, adapters->N, adapters->K, p.splits, p.lanes, 0, 0};

@@ -70,10 +70,12 @@ hipError_t hipDeviceGetAttribute(int *value, hipDeviceAttribute_t, int) { return
 }
 
 int main() {
-  uint16_t *const p[6] = {(uint16_t *)0x1000, (uint16_t *)0x2000, (uint16_t *)0x3000,
-                          (uint16_t *)0x4000, (uint16_t *)0x5000, (uint16_t *)0x6000};
-  int32_t *const ip = (int32_t *)0x7000;
-  float *const fp = (float *)0x8000;
+  // (buffers far from one another: a call may refuse those that overlap)
+  auto at = [](uintptr_t n) { return n << 42; };
+  uint16_t *const p[6] = {(uint16_t *)at(1), (uint16_t *)at(2), (uint16_t *)at(3),
+                          (uint16_t *)at(4), (uint16_t *)at(5), (uint16_t *)at(6)};
+  int32_t *const ip = (int32_t *)at(7);
+  float *const fp = (float *)at(8);
   std::string line;
   while (std::getline(std::cin, line)) {
     std::istringstream in(line);
