@@ -47,7 +47,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return bf16_bits_rne(lo) | (bf16_bits_rne(hi) << 16);
 }
 // The same in the one instruction that the compiler has for it (equal for every fp32 number;
-// a NaN keeps its sign and upper bits).
+// a NaN stays one, with its sign).
 __device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
   typedef float f32x2_t __attribute__((ext_vector_type(2)));
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
