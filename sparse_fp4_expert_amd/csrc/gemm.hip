@@ -236,7 +236,8 @@ static void launch_stream(GemmArgs a, hipStream_t stream) {
 //
 // Measured: 8192 x 4096 x 7168 333 us, 1440 TFLOP/s; 4096 rows' gradient 176 us, their
 // weights' 181 us (1370 and 1330).  There the MFMAs bound it, at the clock that their power
-// leaves: on zeros the product of 4096 rows takes 126 us for 173.  Grouped over experts
+// leaves: on zeros the product of 4096 rows takes 126 us for 173, and of launches one behind the
+// other after a pause the 8th to the 100th take up to 240 for the 176.  Grouped over experts
 // of a few hundred rows, tiles partly empty, the epilogues' stores, and the first copies of
 // tiles of few stages (128 experts of 1536 x 2048, 256 uneven rows each: forward 316 us, rows'
 // gradient 292, weights' 413, where 805 MB are written).
@@ -680,6 +681,8 @@ __global__ __launch_bounds__(WP * WQ * 64, DEPTH > 2 ? 1 : 2) void gemm_tiled_ke
               o[0] = a.accumulate ? o[0] + u : u;
               o[1] = a.accumulate ? o[1] + v : v;
             } else {
+              // (rounded to bf16, the operands of the MFMA that reads them next: what is made from
+              // them is off by 0.0024 of its norm then, its own rounding alone by 0.0017)
               const size_t at = (size_t)r * 2 * cols + c;
               const uint4 zg = *reinterpret_cast<const uint4 *>(a.zin + at);
               const uint4 zu = *reinterpret_cast<const uint4 *>(a.zin + at + cols);

@@ -1017,7 +1017,9 @@ def gemm(x, w, expert_offsets=None, perm=None, k: int = 1, epilogue: int = EPI_N
     [1, N, K], no expert_offsets), or grouped over the E experts of w [E, N, K].
     With `perm`, routed row r reads row perm[r] // k of x; else x's rows are the
     routed rows.  With EPI_SWIGLU and `save`, returns (y, z): z [rows, N] are the
-    projections before the activation, for gemm_dx."""
+    projections before the activation, for gemm_dx.  Rows outside every expert's
+    are not written.  Autograd records nothing here: the gradients are gemm_dx and
+    gemm_dw."""
     if stream is not None:
         with _current(stream, x):
             return gemm(x, w, expert_offsets, perm, k, epilogue, save, out)
@@ -1033,7 +1035,8 @@ def gemm(x, w, expert_offsets=None, perm=None, k: int = 1, epilogue: int = EPI_N
 def gemm_dx(dy, w, expert_offsets=None, z=None, out=None, stream=None):
     """Gradient of the (routed) rows of gemm from that of its result dy [rows, N]:
     [rows, K].  With z [rows, 2K], the projections that a gated block made these
-    rows from, the gradient of z instead (`out` may be z)."""
+    rows from, the gradient of z instead (`out` may be z).  Rows outside every
+    expert's are not written."""
     if stream is not None:
         with _current(stream, dy):
             return gemm_dx(dy, w, expert_offsets, z, out)
@@ -1071,7 +1074,8 @@ def gemm_dw(dy, x, expert_offsets=None, E: int = 1, perm=None, k: int = 1, out=N
 def unpermute_backward(dout, y, inv_perm, topk_weights, T: int, k: int, dy: bool = True, dw: bool = True,
                        stream=None):
     """Gradients of unpermute with weights from that of its result dout [T, N]:
-    (dy [T*k, N] in routed order, dw float32 [T*k]); None for one not wanted."""
+    (dy [T*k, N] in routed order, dw float32 [T*k]); None for one not wanted.  Rows
+    of dy that inv_perm does not name are not written."""
     if stream is not None:
         with _current(stream, dout):
             return unpermute_backward(dout, y, inv_perm, topk_weights, T, k, dy, dw)
@@ -1087,7 +1091,8 @@ def unpermute_backward(dout, y, inv_perm, topk_weights, T: int, k: int, dy: bool
 def lora(x, adapters: Lora, ids, base=None, epilogue: int = EPI_NONE, out=None, stream=None):
     """base + scale * (x a') b' with row t's adapter ids[t] (int32; a row with an
     id outside [0, adapters) has none), [T, N], or its SwiGLU, [T, N/2].  `base`
-    [T, N]: the shared projection's result, zeros if None; `out` may be base."""
+    [T, N]: the shared projection's result, zeros if None; `out` may be base.
+    Autograd records nothing here."""
     if stream is not None:
         with _current(stream, x):
             return lora(x, adapters, ids, base, epilogue, out)

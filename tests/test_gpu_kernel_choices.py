@@ -113,6 +113,10 @@ def check_gemm(lib, g, grouped, M, E, N, K, swiglu):
         lib.moesq_gemm(x, perm, M // k if perm is not None else 0, k, off, M, w, E, N, K,
                        (lib.EPI_SWIGLU if swiglu else lib.EPI_NONE) | (lib.OUT_FLAT if flat else 0), y.t, z.t if z else None)
         assert y.intact() and (z is None or z.intact())
+        if swiglu and perm is not None:                        # the same in flat order, without z
+            f = result(M, N // 2)
+            lib.moesq_gemm(x, perm, M // k, k, off, M, w, E, N, K, lib.EPI_SWIGLU | lib.OUT_FLAT, f.t)
+            assert f.intact() and torch.equal(f.t[perm.long()], y.t)
         for e, r in experts(off, M):
             src = r if perm is None else perm[r].long() // k
             xe, we = x[src].double(), w[e].double().t().contiguous()
